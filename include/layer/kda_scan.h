@@ -1,0 +1,122 @@
+/*
+ * kda_scan.h -- C ABI of the gated linear recurrence over long packed
+ * sequences and its backward pass on B200 (sm_100a), library libkda_layer.so.
+ *
+ * The operation is the recurrence of kda_decode.h over whole sequences: per
+ * sequence n and value head h, over its tokens t in order, on the fp32 state
+ * S[K][V]:
+ *
+ *     S   <- Diag(exp(g[t,h,:])) S
+ *     r   <- v[t,h,:] - S^T k[t,h,:]
+ *     S   <- S + beta[t,h] k[t,h,:] r^T
+ *     out[t,h,:] <- bf16(scale * S^T q[t,h,:])
+ *
+ * from an initial state to a final state.  kda_scan computes it for serving
+ * (packed prompts, states in slots) and training; kda_scan_backward the
+ * gradients of a loss with respect to q, k, v, g, beta and the initial states,
+ * given those with respect to out and the final states.  Single tokens are
+ * kda_decode's.
+ *
+ * Sequences.  Dense: cu_seqlens NULL, N sequences of T tokens, token t of
+ * sequence n in row n*T + t.  Packed: cu_seqlens (device int32 [N+1],
+ * non-decreasing from >= 0 to <= T), T the number of rows, sequence n in rows
+ * [cu_seqlens[n], cu_seqlens[n+1]); lengths may be 0.  Rows outside every
+ * sequence are neither read nor written.  Offsets outside [0, T] or decreasing
+ * are clamped: they never make an access out of range, but results of the
+ * sequences concerned are then undefined.
+ *
+ * Layouts.  q, k bf16 [rows, HV, K]; v, out bf16 [rows, HV, V]; g fp32
+ * [rows, HV, K] (log-decay, normally <= 0; growing decays are computed as long
+ * as a chunk's growth stays in fp32's range); beta fp32 [rows, HV].  Every one
+ * has a row stride in elements (>= the row's width), heads dense inside a row:
+ * q, k and v may be slices of one packed row buffer, and so may the gradients.
+ * States fp32 [N, HV, K, V], dense.  With slot_idx (device int32 [N],
+ * kda_scan only) sequence n's state is block slot_idx[n] of [num_slots, HV, K,
+ * V] pools instead; a slot < 0 or >= num_slots makes the sequence inactive
+ * (zero outputs, no state touched), active slots are distinct.
+ * initial_state NULL starts from zeros, final_state NULL drops the result;
+ * the two may be the same buffer (a pool updated in place).
+ *
+ * Supported sizes: K = V = 128, HV >= 1, N, T >= 0.  Alignment: q, k, v, out,
+ * d_out, dq, dk, dv 16 bytes with strides that are multiples of 8 elements;
+ * workspace and states 16 bytes; g, beta, dg, dbeta, cu_seqlens, slot_idx 4.
+ *
+ * Accuracy.  States, sums and every fp32 result are computed to fp32 accuracy
+ * (operands as fp16 or tf32 pairs of 22 bits, fp32 accumulation, decays
+ * accumulated in fp64); bf16 results are rounded once.  An infinity or NaN in a
+ * sequence's inputs makes that sequence's and head's results undefined from
+ * its chunk (64 tokens) on, nothing else.
+ *
+ * Workspace.  Caller-owned device memory of kda_scan_workspace_bytes bytes; the
+ * library allocates nothing.  With save = 1 (and a workspace sized for
+ * training) kda_scan leaves in it what kda_scan_backward reads: the same
+ * inputs, the untouched workspace and saved = 1 then run the backward pass
+ * alone; with saved = 0 kda_scan_backward recomputes the forward pass into the
+ * workspace first (any contents).  Calls that share a workspace must be
+ * ordered.  Its first int32 is an error word: the kernels' waits for their
+ * copies are bounded, and one that ever gives up stores 1 there and leaves
+ * results unwritten; the library never clears it.
+ *
+ * Execution: kda_scan enqueues 2 kernels, kda_scan_backward 2 (4 with saved =
+ * 0) on `stream`; no host synchronisation; can be captured in a CUDA graph.
+ * Results do not depend on the launch's timing (no atomics on data).
+ *
+ * Errors: as in kda_decode.h, nothing is enqueued unless KDA_OK is returned.
+ * KDA_ERR_ALIAS: an output overlaps an input, another output or the workspace
+ * (rows of one packed buffer with equal strides and disjoint columns do not).
+ */
+#ifndef KDA_SCAN_H
+#define KDA_SCAN_H
+
+#include "../kda_decode.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    const void *q;      int64_t q_row_stride;
+    const void *k;      int64_t k_row_stride;
+    const void *v;      int64_t v_row_stride;
+    const float *g;     int64_t g_row_stride;
+    const float *beta;  int64_t beta_row_stride;
+    const int32_t *cu_seqlens;
+    const float *initial_state;
+    float *final_state;          /* kda_scan_backward ignores it */
+    const int32_t *slot_idx;     /* kda_scan_backward: must be NULL */
+    int64_t num_slots;
+    void *out;          int64_t out_row_stride;   /* kda_scan_backward ignores it */
+    void *workspace;    int64_t workspace_bytes;
+    int64_t N, T, HV, K, V;
+    float scale;
+    int32_t save;                /* kda_scan: keep what the backward pass reads */
+} kda_scan_args;
+
+typedef struct {
+    const void *d_out;  int64_t d_out_row_stride;
+    const float *d_final_state;  /* NULL: zeros */
+    void *dq;           int64_t dq_row_stride;
+    void *dk;           int64_t dk_row_stride;
+    void *dv;           int64_t dv_row_stride;
+    float *dg;          int64_t dg_row_stride;
+    float *dbeta;       int64_t dbeta_row_stride;
+    float *d_initial_state;      /* NULL: not wanted */
+    int32_t saved;               /* the workspace holds this call's forward pass */
+} kda_scan_grads;
+
+/* Bytes of workspace (0 when there is nothing to do, -1 for unsupported or
+ * negative sizes).  packed: cu_seqlens will be set; training: for save = 1 and
+ * for kda_scan_backward. */
+KDA_API int64_t kda_scan_workspace_bytes(int64_t N, int64_t T, int32_t packed, int64_t HV, int64_t K, int64_t V,
+                                         int32_t training);
+
+KDA_API kda_status kda_scan(const kda_scan_args *args, kda_stream_t stream);
+
+/* args: the forward call's. */
+KDA_API kda_status kda_scan_backward(const kda_scan_args *args, const kda_scan_grads *grads, kda_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* KDA_SCAN_H */

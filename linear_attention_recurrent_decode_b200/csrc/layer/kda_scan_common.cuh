@@ -1,0 +1,173 @@
+// kda_scan_common.cuh -- parameters, workspace records and the decay factors
+// shared by the scan's kernels (see kda_scan_prep.cuh for the mathematics).
+#pragma once
+
+#include "kda_tiles.cuh"
+
+namespace kdal {
+
+struct ScanParams {
+  const __nv_bfloat16* q; int64_t q_ts;  // [tokens, HV, K], rows q_ts elements apart; likewise below
+  const __nv_bfloat16* k; int64_t k_ts;
+  const __nv_bfloat16* v; int64_t v_ts;
+  const float* g; int64_t g_ts;
+  const float* beta; int64_t beta_ts;
+  const int32_t* cu;        // [N + 1] packed sequences, or null: N sequences of T tokens
+  const float* s_in;        // [N or slots, HV, K, V] or null (zeros)
+  float* s_out;             // likewise, or null
+  const int32_t* slot_idx;  // [N] or null (sequence n uses block n)
+  int64_t num_slots;        // blocks of s_in and s_out when slot_idx is set
+  __nv_bfloat16* out; int64_t out_ts;
+  unsigned char* ws;
+  int64_t rec_bytes;        // bytes of one record
+  int64_t tokens, T, HV;
+  int32_t N, seq_chunks;    // seq_chunks: ceil(T / C) of the dense form
+  float scale;
+  int32_t save;             // the forward call keeps what the backward pass reads
+  // backward
+  const __nv_bfloat16* d_out; int64_t d_out_ts;
+  const float* d_final;     // [N, HV, K, V] or null
+  __nv_bfloat16* dq; int64_t dq_ts;
+  __nv_bfloat16* dk; int64_t dk_ts;
+  __nv_bfloat16* dv; int64_t dv_ts;
+  float* dg; int64_t dg_ts;
+  float* dbeta; int64_t dbeta_ts;
+  float* d_init;            // [N, HV, K, V] or null
+};
+
+// One record per (chunk slot, head); the chunk slots of sequence n start at
+// cu[n] / C + n (n seq_chunks in the dense form), which leaves room for every
+// sequence's ceil(length / C) chunks without a scan over the lengths.
+struct Record {
+  // header: floats
+  static constexpr int kDecay = 0;     // [128] exp(Gamma_C)
+  static constexpr int kBeta = 128;    // [64]
+  static constexpr int kScWr = 192, kScKe = 193, kScQt = 194, kScP = 195, kScY = 196;
+  static constexpr int kScS = 200, kScR = 208, kScDS = 216, kScDU = 224;  // [8] each: per 16 value columns
+  // byte offsets
+  static constexpr int kHdr = 1024;
+  static constexpr int kPlane = kC * kK * 2;       // 16 KB: a [64][128] (or [128][64]) plane
+  static constexpr int kP = kHdr;                  // P   [t][s] hi, lo (8 KB each)
+  static constexpr int kQt = kP + kC * kC * 4;     // Qt  [t][i] hi, lo
+  static constexpr int kWr = kQt + 2 * kPlane;     // Wr  [t][i] hi, lo
+  static constexpr int kKe = kWr + 2 * kPlane;     // Ke  [t][i] hi, lo
+  static constexpr int kRt = kKe + 2 * kPlane;     // Rt^T [v][t] fp32
+  static constexpr int64_t kForward = kRt + kV * kC * 4;
+  static constexpr int kY = static_cast<int>(kForward);  // beta_t Y [t][s] hi, lo
+  static constexpr int kS = kY + kC * kC * 4;      // S0^T [v][i] hi, lo (32 KB each)
+  static constexpr int kR = kS + kV * kK * 4;      // r^T  [v][t] hi, lo
+  static constexpr int kDS = kR + 2 * kPlane;      // dS1^T [v][i] hi, lo
+  static constexpr int kDU = kDS + kV * kK * 4;    // dU^T [v][t] hi, lo
+  static constexpr int64_t kTraining = kDU + 2 * kPlane;
+};
+constexpr int64_t kWsHeader = 256;  // word 0: the error word
+
+__device__ __forceinline__ void set_error(const ScanParams& p) { *reinterpret_cast<volatile int32_t*>(p.ws) = 1; }
+
+__device__ __forceinline__ unsigned char* record(const ScanParams& p, int64_t slot, int64_t h) {
+  return p.ws + kWsHeader + (slot * p.HV + h) * p.rec_bytes;
+}
+
+// Sequence n's first token and length; offsets are clamped to the tokens
+// there are, so that no offset makes an access out of range.
+__device__ __forceinline__ void seq_range(const ScanParams& p, int64_t n, int64_t& start, int64_t& len) {
+  if (p.cu == nullptr) {
+    start = n * p.T;
+    len = p.T;
+    return;
+  }
+  int64_t a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1);
+  a = a < 0 ? 0 : (a > p.tokens ? p.tokens : a);
+  b = b < a ? a : (b > p.tokens ? p.tokens : b);
+  start = a;
+  len = b - a;
+}
+__device__ __forceinline__ int64_t first_slot(const ScanParams& p, int64_t n, int64_t start) {
+  return p.cu == nullptr ? n * p.seq_chunks : start / kC + n;
+}
+// The state block of sequence n, or -1 for an inactive one.
+__device__ __forceinline__ int64_t state_block(const ScanParams& p, int64_t n) {
+  if (p.slot_idx == nullptr) return n;
+  const int64_t s = __ldg(p.slot_idx + n);
+  return s >= 0 && s < p.num_slots ? s : -1;
+}
+
+struct ChunkPos {
+  int64_t n, tok;  // sequence, first token of the chunk
+  int32_t tc;      // tokens of the chunk; 0: no such chunk
+};
+// The chunk of a chunk slot (all threads of the block call it; `sh` is shared).
+__device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot, ChunkPos* sh) {
+  if (p.cu == nullptr) {
+    ChunkPos c;
+    c.n = slot / p.seq_chunks;
+    const int64_t t = (slot - c.n * p.seq_chunks) * kC;
+    c.tok = c.n * p.T + t;
+    c.tc = static_cast<int32_t>(p.T - t < kC ? p.T - t : kC);
+    if (state_block(p, c.n) < 0) c.tc = 0;
+    return c;
+  }
+  if (threadIdx.x == 0) sh->tc = 0;
+  __syncthreads();
+  for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x) {
+    int64_t start, len;
+    seq_range(p, n, start, len);
+    const int64_t t = (slot - first_slot(p, n, start)) * kC;
+    if (t >= 0 && t < len) {
+      sh->n = n;
+      sh->tok = start + t;
+      sh->tc = state_block(p, n) < 0 ? 0 : static_cast<int32_t>(len - t < kC ? len - t : kC);
+    }
+  }
+  __syncthreads();
+  return *sh;
+}
+
+// exp of an fp64 argument to fp32 accuracy: the remainder of rounding it is
+// below half an ulp and enters to first order.
+__device__ __forceinline__ float exp_of(double x) {
+  const float hi = static_cast<float>(x);
+  return expf(hi) * (1.f + static_cast<float>(x - static_cast<double>(hi)));
+}
+// A log-decay; below -1e4 the decay is zero either way (and -inf would make NaN of differences).
+__device__ __forceinline__ float log_decay(float g) { return g < -1e4f ? -1e4f : g; }
+
+// Largest |L - mid| a sub-block may have for its factors exp(+-(L - mid)): they
+// and the products of two stay normal fp32 numbers.
+constexpr double kSafe = 60.0;
+
+// The decay factors of one sub-block and key channel.  L_t is the cumulative
+// log-decay from the sub-block's start.  up[t] = exp(L_t - mu), dn[t] = exp(md
+// - L_t).  Within range mu = md = mid, the middle of the L_t, so that
+// up[t] dn[s] = exp(L_t - L_s) for every pair; otherwise mu = 0 and md = L_end
+// (each factor at most 1 for g <= 0) and pairs inside the sub-block are formed
+// one by one from the differences (`exact`).
+struct SubFactors {
+  double mu, md, end;
+  bool exact;
+};
+__device__ __forceinline__ SubFactors sub_factors(const float (&g)[kB], float (&up)[kB], float (&dn)[kB]) {
+  SubFactors f;
+  double acc = 0.0, lo = 1e300, hi = -1e300;
+#pragma unroll
+  for (int t = 0; t < kB; ++t) {
+    acc += static_cast<double>(g[t]);
+    lo = fmin(lo, acc);
+    hi = fmax(hi, acc);
+  }
+  f.end = acc;
+  f.exact = !(hi - lo <= 2 * kSafe);
+  f.mu = f.exact ? 0.0 : 0.5 * (hi + lo);
+  f.md = f.exact ? acc : f.mu;
+  acc = 0.0;
+#pragma unroll
+  for (int t = 0; t < kB; ++t) {
+    acc += static_cast<double>(g[t]);
+    const float x = static_cast<float>(acc - f.mu);
+    up[t] = expf(x);
+    dn[t] = expf(f.exact ? static_cast<float>(f.md - acc) : -x);
+  }
+  return f;
+}
+
+}  // namespace kdal

@@ -1,0 +1,530 @@
+// kda_scan_grad.cuh -- the scan's gradients of a chunk, once the states and
+// their gradients are known at its ends (kda_scan_chain.cuh).
+//
+// With dU (the gradient of U = beta r), S0 and dS1 of the chunk:
+//   y = dU - Y^T (beta dU),  dR = beta y,  dV = dR,  dbeta = sum_v r y
+//   dQt = scale dO S0^T, dKt = -dR S0^T, dKe = (beta r) dS1^T
+//   dP = scale dO (beta r)^T (s <= t),  dA = -dR (beta r)^T (s < t)
+// and, over the pairs of the chunk with E_ts = exp(Gamma_t - Gamma_s),
+//   dq_t  = dQt_t exp(Gamma_t) + sum_s dP_ts k_s E_ts
+//   dk_t  = [dKt_t exp(Gamma_t) + sum_s dA_ts k_s E_ts]                      "row"
+//         + [dKe_t exp(Gamma_C - Gamma_t) + sum_s (dP_st q_s + dA_st k_s) E_st] "column"
+//   dg_t  = sum_{t' >= t} (q dq + k dk_row - k dk_column)_t' + sum_v S1 dS1,
+// the last term being exp(Gamma_C) sum_v S0 dS1 + sum_t Ke dKe per channel.
+//
+// The decays are applied sub-block by sub-block (16 tokens) on the
+// accumulators: a row block I starts from its dQt and, for J = 0 .. I - 1,
+// multiplies by the decay up to J's reference, adds dP_IJ (k dn)_J on the
+// tensor cores and multiplies by the rest of J's decay; column blocks run
+// through the later blocks in reverse the same way.  All factors stay at most
+// 1 (see SubFactors), and no product is formed twice.
+#pragma once
+
+#include "kda_scan_chain.cuh"
+
+namespace kdal {
+
+constexpr int kGradThreads = 256;
+constexpr int kGP = kK + 8;  // padded rows of the fp32 factors, read as [k][n] fragments
+constexpr int kDP = kC + 4;
+
+struct GradSmem {
+  // The operand tiles; later dP and dA over the first, and the factors after them.
+  unsigned char s0[kV * kK * 4];             // S0^T [v][i] hi, lo
+  unsigned char ds[kV * kK * 4];             // dS1^T; before: dU^T and beta Y
+  unsigned char dr[2 * Record::kPlane];      // dR^T [v][t]
+  unsigned char r[2 * Record::kPlane];       // r^T [v][t]
+  unsigned char dO[Record::kPlane];          // dO [t][v]
+  // exp(mu), exp(md), exp(end - mu), exp(end - md) per sub-block and channel
+  float emu[kNB][kK], emd[kNB][kK], eru[kNB][kK], erd[kNB][kK];
+  float hdr[Record::kHdr / 4];
+  float tail[2][kK];                         // sum_v S1 dS1, in two parts
+  float dbeta[8][kC];
+  float sc_dr[8];
+  uint32_t mx_do;
+  int exact[kNB];
+  uint64_t bar[2];
+  ChunkPos pos;
+};
+struct GradPairs {  // over s0 .. dO once those are dead
+  float dp[kC][kDP], da[kC][kDP];
+  float up[kC][kGP], dn[kC][kGP];            // exp(L - mu), exp(md - L)
+  float ku[kC][kGP], qu[kC][kGP], kd[kC][kGP];  // k up, q up, k dn
+};
+static_assert(sizeof(GradPairs) <= offsetof(GradSmem, emu), "the factors fit over the operand tiles");
+static_assert(2 * sizeof(float) * kC * kDP <= kV * kK * 4, "dP and dA fit over S0");
+
+// Direct sums inside sub-block b (its decays are out of the factors' range):
+// one accumulator element (t, i), pairs from the log-decays between them.
+__device__ __noinline__ float3 grad_exact_element(const ScanParams& p, const GradPairs& f, int b, int64_t tok, int tc, int64_t h,
+                                                  int t, int i) {
+  if (t >= tc) return make_float3(0.f, 0.f, 0.f);
+  float d = 0.f, dq = 0.f, dkr = 0.f, dkc = 0.f;
+  for (int s = t; s >= b * kB; --s) {
+    const float ke = __bfloat162float(p.k[(tok + s) * p.k_ts + h * kK + i]) * expf(d);
+    dq = fmaf(f.dp[t][s], ke, dq);
+    dkr = fmaf(f.da[t][s], ke, dkr);
+    d += log_decay(p.g[(tok + s) * p.g_ts + h * kK + i]);
+  }
+  d = 0.f;
+  for (int s = t; s < (b + 1) * kB && s < tc; ++s) {
+    if (s > t) d += log_decay(p.g[(tok + s) * p.g_ts + h * kK + i]);
+    const float e = expf(d);
+    dkc = fmaf(f.dp[s][t] * e, __bfloat162float(p.q[(tok + s) * p.q_ts + h * kK + i]), dkc);
+    dkc = fmaf(f.da[s][t] * e, __bfloat162float(p.k[(tok + s) * p.k_ts + h * kK + i]), dkc);
+  }
+  return make_float3(dq, dkr, dkc);
+}
+
+// acc [16 x 64] += a [16 x 16] x (b rows k0.., channels i0..), a stored [row][k] (or [k][row] if TRANS).
+template <bool TRANS>
+__device__ __forceinline__ void pair_a(const float (*a)[kDP], int r0, int k0, int kk, int lane, uint32_t (&ah)[4], uint32_t (&al)[4]) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = r0 + r + (j & 1) * 8, k = k0 + kk * 8 + c + (j >> 1) * 4;
+    tf32_split(TRANS ? a[k][row] : a[row][k], ah[j], al[j]);
+  }
+}
+__device__ __forceinline__ void pair_b(const float (*b)[kGP], int k0, int kk, int i0, int lane, uint32_t (&bh)[2], uint32_t (&bl)[2]) {
+  const int r = lane >> 2, c = lane & 3;
+  tf32_split(b[k0 + kk * 8 + c][i0 + r], bh[0], bl[0]);
+  tf32_split(b[k0 + kk * 8 + c + 4][i0 + r], bh[1], bl[1]);
+}
+__device__ __forceinline__ void scale_cols(float (&acc)[8][4], const float* f) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float2 d = *reinterpret_cast<const float2*>(f + n * 8);
+    acc[n][0] *= d.x;
+    acc[n][1] *= d.y;
+    acc[n][2] *= d.x;
+    acc[n][3] *= d.y;
+  }
+}
+
+__global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __grid_constant__ ScanParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  GradSmem& sm = *reinterpret_cast<GradSmem*>(smem_raw);
+  GradPairs& pr = *reinterpret_cast<GradPairs*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  if (tid == 0) {
+    mbar_init(&sm.bar[0], 1);
+    mbar_init(&sm.bar[1], 1);
+    mbar_fence_init();
+    sm.mx_do = 0;
+  }
+  if (tid < kNB) sm.exact[tid] = 0;
+  const ChunkPos pos = locate(p, slot, &sm.pos);
+  const int tc = pos.tc;
+  if (tc == 0) return;
+  __syncthreads();
+  const unsigned char* const rec = record(p, slot, h);
+  if (tid == 0) {
+    mbar_expect(&sm.bar[0], Record::kHdr + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
+    bulk_load(sm.hdr, rec, Record::kHdr, &sm.bar[0]);
+    bulk_load(sm.ds, rec + Record::kDU, 2 * Record::kPlane, &sm.bar[0]);
+    bulk_load(sm.ds + 2 * Record::kPlane, rec + Record::kY, kC * kC * 4, &sm.bar[0]);
+    bulk_load(sm.r, rec + Record::kR, 2 * Record::kPlane, &sm.bar[0]);
+    bulk_load(sm.s0, rec + Record::kS, kV * kK * 4, &sm.bar[0]);
+  }
+  // ---- dO as an fp16 tile (exact after scaling)
+  {
+    uint4 raw[4];
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = tid + j * kGradThreads, t = c >> 4, pc = c & 15;
+      raw[j] = t < tc ? *reinterpret_cast<const uint4*>(p.d_out + (pos.tok + t) * p.d_out_ts + h * kV + pc * 8) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+    }
+    m = warp_max(m);
+    if (lane == 0) atomicMax(&sm.mx_do, __float_as_uint(m));
+    __syncthreads();
+    const float sc = pow2_scale(__uint_as_float(sm.mx_do));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = tid + j * kGradThreads, t = c >> 4, pc = c & 15;
+      uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc, __uint_as_float(w[e] & 0xffff0000u) * sc));
+      *reinterpret_cast<uint4*>(sm.dO + off128(t, pc * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  const float sc_do = pow2_scale(__uint_as_float(sm.mx_do));
+  if (!__syncthreads_and(mbar_wait(&sm.bar[0], 0))) {  // the copies never came
+    if (tid == 0) set_error(p);
+    return;
+  }
+  const uint32_t a_s0 = smem_addr(sm.s0), a_ds = smem_addr(sm.ds), a_dr = smem_addr(sm.dr), a_r = smem_addr(sm.r), a_do = smem_addr(sm.dO);
+  const float* const beta = sm.hdr + Record::kBeta;
+
+  // ---- 1. y^T = dU^T - dU^T (beta Y); dR, dV, dbeta: warp = 16 value columns
+  {
+    const int v0 = warp * 16;
+    const uint32_t a_y = a_ds + 2 * Record::kPlane;
+    uint32_t uh[4][4], ul[4][4];
+    float acc[8][4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {  // s sub-block; Y[s][t] is zero for t >= s
+      load_a<64>(a_ds, v0, kk * 16, lane, uh[kk]);
+      load_a<64>(a_ds + Record::kPlane, v0, kk * 16, lane, ul[kk]);
+#pragma unroll
+      for (int nb = 0; nb <= kk; ++nb) {
+        uint32_t bh[4], bl[4];
+        load_b_t<64>(a_y, kk * 16, nb * 16, lane, bh);
+        load_b_t<64>(a_y + kC * kC * 2, kk * 16, nb * 16, lane, bl);
+        mma3(acc[2 * nb], acc[2 * nb + 1], uh[kk], ul[kk], bh, bl);
+      }
+    }
+    const float inv = pow2_inv(sm.hdr[Record::kScDU + warp]), inv_y = inv * pow2_inv(sm.hdr[Record::kScY]);
+    const float inv_r = pow2_inv(sm.hdr[Record::kScR + warp]);
+    float m = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t rh[4], rl[4];
+      load_a<64>(a_r, v0, kk * 16, lane, rh);
+      load_a<64>(a_r + Record::kPlane, v0, kk * 16, lane, rl);
+      float db[4] = {0.f, 0.f, 0.f, 0.f};  // tokens kk 16 + 2 (lane & 3) + {0, 1, 8, 9}
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {        // fragment register j: rows + (j & 1) 8, columns + (j >> 1) 8
+        const float2 du = join2(uh[kk][j], ul[kk][j]), r = join2(rh[j], rl[j]);
+        float(&c)[4] = acc[2 * kk + (j >> 1)];
+        const int e = (j & 1) * 2, t = kk * 16 + (j >> 1) * 8 + 2 * (lane & 3);
+        const float y0 = fmaf(-c[e], inv_y, du.x * inv), y1 = fmaf(-c[e + 1], inv_y, du.y * inv);
+        db[(j >> 1) * 2] = fmaf(y0, r.x * inv_r, db[(j >> 1) * 2]);
+        db[(j >> 1) * 2 + 1] = fmaf(y1, r.y * inv_r, db[(j >> 1) * 2 + 1]);
+        c[e] = y0 * beta[t];
+        c[e + 1] = y1 * beta[t + 1];
+        m = fmaxf(m, fmaxf(fabsf(c[e]), fabsf(c[e + 1])));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+        if (lane < 4) sm.dbeta[warp][kk * 16 + (j >> 1) * 8 + 2 * lane + (j & 1)] = db[j];
+      }
+    }
+    const float sc = pow2_scale(warp_max(m));
+    if (lane == 0) sm.sc_dr[warp] = sc;
+    __nv_bfloat16* const dv = p.dv + pos.tok * p.dv_ts + h * kV + v0;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t ah[4], al[4];
+      frag_a(acc[2 * kk], acc[2 * kk + 1], sc, ah, al);
+      store_frag<64>(sm.dr, Record::kPlane, v0, kk * 16, lane, ah, al);
+      store_out16(dv, p.dv_ts, kk * 16, tc, lane, acc[2 * kk], acc[2 * kk + 1], 1.f);
+    }
+  }
+  fence_async();  // the reads of dU and Y come before dS1 is copied over them
+  __syncthreads();
+  if (tid == 0) {
+    mbar_expect(&sm.bar[1], kV * kK * 4);
+    bulk_load(sm.ds, rec + Record::kDS, kV * kK * 4, &sm.bar[1]);
+  }
+  if (tid < tc) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sm.dbeta[w][tid];
+    p.dbeta[(pos.tok + tid) * p.dbeta_ts + h] = s;
+  }
+
+  // ---- 2. dQt = scale dO S0^T and dKt = -dR S0^T: warp = 16 tokens x 64 channels.  The value columns
+  // (contracted here) have a scale per group of 16, one k step: the common scale is put on the left operand.
+  const int I = warp & 3, i0 = (warp >> 2) * 64;
+  float c_s = sm.hdr[Record::kScS], c_dr = sm.sc_dr[0], c_r = sm.hdr[Record::kScR], c_ds = sm.hdr[Record::kScDS];
+  float c_dr_s = sm.sc_dr[0] * sm.hdr[Record::kScS], c_r_ds = sm.hdr[Record::kScR] * sm.hdr[Record::kScDS];
+  float c_dr_r = sm.sc_dr[0] * sm.hdr[Record::kScR];
+#pragma unroll
+  for (int g = 1; g < 8; ++g) {
+    c_s = fminf(c_s, sm.hdr[Record::kScS + g]);
+    c_dr = fminf(c_dr, sm.sc_dr[g]);
+    c_r = fminf(c_r, sm.hdr[Record::kScR + g]);
+    c_ds = fminf(c_ds, sm.hdr[Record::kScDS + g]);
+    c_dr_s = fminf(c_dr_s, sm.sc_dr[g] * sm.hdr[Record::kScS + g]);
+    c_r_ds = fminf(c_r_ds, sm.hdr[Record::kScR + g] * sm.hdr[Record::kScDS + g]);
+    c_dr_r = fminf(c_dr_r, sm.sc_dr[g] * sm.hdr[Record::kScR + g]);
+  }
+  float dq[8][4] = {}, dkr[8][4] = {};
+#pragma unroll 2
+  for (int g = 0; g < 8; ++g) {
+    uint32_t a[4], ah[4], al[4];
+    load_a<128>(a_do, I * 16, g * 16, lane, a);
+    load_a_t<64>(a_dr, I * 16, g * 16, lane, ah);
+    load_a_t<64>(a_dr + Record::kPlane, I * 16, g * 16, lane, al);
+    const float sc_s = sm.hdr[Record::kScS + g];
+    scale_frag(a, __float2half2_rn(c_s * pow2_inv(sc_s)));
+    const __half2 f = __float2half2_rn(c_dr_s * pow2_inv(sc_s) * pow2_inv(sm.sc_dr[g]));
+    scale_frag(ah, f);
+    scale_frag(al, f);
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      uint32_t bh[4], bl[4];
+      load_b_t<128>(a_s0, g * 16, i0 + nb * 16, lane, bh);
+      load_b_t<128>(a_s0 + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
+      mma2(dq[2 * nb], dq[2 * nb + 1], a, bh, bl);
+      mma3(dkr[2 * nb], dkr[2 * nb + 1], ah, al, bh, bl);
+    }
+  }
+  {
+    const float fq = pow2_inv(sc_do) * pow2_inv(c_s) * p.scale, fk = -pow2_inv(c_dr_s);
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dq[n][e] *= fq;
+        dkr[n][e] *= fk;
+      }
+  }
+  if (!__syncthreads_and(mbar_wait(&sm.bar[1], 0))) {
+    if (tid == 0) set_error(p);
+    return;
+  }
+  // ---- 3. exp(Gamma_C) sum_v S0 dS1 per channel: thread = two channels of a quarter of the value columns ...
+  float e0 = 0.f, e1 = 0.f;
+  {
+    const int i = (tid & 63) * 2, q4 = tid >> 6;
+#pragma unroll
+    for (int gg = 0; gg < 2; ++gg) {
+      const int g = q4 * 2 + gg;
+      float x0 = 0.f, x1 = 0.f;
+#pragma unroll 4
+      for (int v = g * 16; v < g * 16 + 16; ++v) {
+        const uint32_t off = off128(v, i);
+        const float2 s = join2(*reinterpret_cast<const uint32_t*>(sm.s0 + off), *reinterpret_cast<const uint32_t*>(sm.s0 + kV * kK * 2 + off));
+        const float2 d = join2(*reinterpret_cast<const uint32_t*>(sm.ds + off), *reinterpret_cast<const uint32_t*>(sm.ds + kV * kK * 2 + off));
+        x0 = fmaf(s.x, d.x, x0);
+        x1 = fmaf(s.y, d.y, x1);
+      }
+      const float inv = pow2_inv(sm.hdr[Record::kScS + g]) * pow2_inv(sm.hdr[Record::kScDS + g]);
+      e0 = fmaf(x0, inv, e0);
+      e1 = fmaf(x1, inv, e1);
+    }
+    e0 *= sm.hdr[Record::kDecay + i];
+    e1 *= sm.hdr[Record::kDecay + i + 1];
+  }
+  // ---- 4. dKe = (beta r) dS1^T
+  float dkc[8][4] = {};
+#pragma unroll 2
+  for (int g = 0; g < 8; ++g) {
+    uint32_t ah[4], al[4];
+    load_a_t<64>(a_r, I * 16, g * 16, lane, ah);
+    load_a_t<64>(a_r + Record::kPlane, I * 16, g * 16, lane, al);
+    const __half2 f = __float2half2_rn(c_r_ds * pow2_inv(sm.hdr[Record::kScR + g]) * pow2_inv(sm.hdr[Record::kScDS + g]));
+    scale_frag(ah, f);
+    scale_frag(al, f);
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      uint32_t bh[4], bl[4];
+      load_b_t<128>(a_ds, g * 16, i0 + nb * 16, lane, bh);
+      load_b_t<128>(a_ds + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
+      mma3(dkc[2 * nb], dkc[2 * nb + 1], ah, al, bh, bl);
+    }
+  }
+  const int row = I * 16 + (lane >> 2);  // this thread's rows: row, row + 8
+  {
+    const float inv = pow2_inv(c_r_ds), b0 = beta[row] * inv, b1 = beta[row + 8] * inv;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      dkc[n][0] *= b0;
+      dkc[n][1] *= b0;
+      dkc[n][2] *= b1;
+      dkc[n][3] *= b1;
+    }
+  }
+  __syncthreads();  // every warp is done with S0 (and with the sums over it)
+  // ---- 5. dP and dA over S0, a 16 x 16 block at a time (zeros above the diagonal)
+  for (int u = warp; u < 16; u += 8) {
+    const int ti = u >> 2, si = u & 3;
+    const int t = ti * 16 + (lane >> 2), s = si * 16 + 2 * (lane & 3);
+    float cp[2][4] = {}, ca[2][4] = {};
+    if (si <= ti) {
+#pragma unroll 2
+      for (int g = 0; g < 8; ++g) {
+        uint32_t a[4], ah[4], al[4], bh[4], bl[4];
+        load_a<128>(a_do, ti * 16, g * 16, lane, a);
+        load_a_t<64>(a_dr, ti * 16, g * 16, lane, ah);
+        load_a_t<64>(a_dr + Record::kPlane, ti * 16, g * 16, lane, al);
+        load_b_t<64>(a_r, g * 16, si * 16, lane, bh);
+        load_b_t<64>(a_r + Record::kPlane, g * 16, si * 16, lane, bl);
+        const float sc_r = sm.hdr[Record::kScR + g];
+        scale_frag(a, __float2half2_rn(c_r * pow2_inv(sc_r)));
+        const __half2 f = __float2half2_rn(c_dr_r * pow2_inv(sc_r) * pow2_inv(sm.sc_dr[g]));
+        scale_frag(ah, f);
+        scale_frag(al, f);
+        mma2(cp[0], cp[1], a, bh, bl);
+        mma3(ca[0], ca[1], ah, al, bh, bl);
+      }
+    }
+    const float fp = pow2_inv(sc_do) * pow2_inv(c_r) * p.scale, fa = -pow2_inv(c_dr_r);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tt = t + (e >> 1) * 8, ss = s + n * 8 + (e & 1);
+        const float b = beta[ss];
+        pr.dp[tt][ss] = ss <= tt ? cp[n][e] * fp * b : 0.f;
+        pr.da[tt][ss] = ss < tt ? ca[n][e] * fa * b : 0.f;
+      }
+  }
+  __syncthreads();  // every warp is done with the operand tiles
+  // ---- 6. decay factors
+  const int ch = tid & (kK - 1), half = tid >> 7;
+#pragma unroll
+  for (int b2 = 0; b2 < 2; ++b2) {
+    const int b = half * 2 + b2;
+    float g[kB], up[kB], dn[kB];
+#pragma unroll
+    for (int t = 0; t < kB; ++t)
+      g[t] = b * kB + t < tc ? log_decay(__ldg(p.g + (pos.tok + b * kB + t) * p.g_ts + h * kK + ch)) : 0.f;
+    const SubFactors f = sub_factors(g, up, dn);
+#pragma unroll
+    for (int t = 0; t < kB; ++t) {
+      const int64_t tk = pos.tok + b * kB + t;
+      const bool in = b * kB + t < tc;
+      const float kv = in ? __bfloat162float(p.k[tk * p.k_ts + h * kK + ch]) : 0.f;
+      const float qv = in ? __bfloat162float(p.q[tk * p.q_ts + h * kK + ch]) : 0.f;
+      pr.up[b * kB + t][ch] = up[t];
+      pr.dn[b * kB + t][ch] = dn[t];
+      pr.ku[b * kB + t][ch] = kv * up[t];
+      pr.qu[b * kB + t][ch] = qv * up[t];
+      pr.kd[b * kB + t][ch] = kv * dn[t];
+    }
+    if (f.exact) sm.exact[b] = 1;
+    sm.emu[b][ch] = exp_of(f.mu);
+    sm.emd[b][ch] = exp_of(f.md);
+    sm.eru[b][ch] = exp_of(f.end - f.mu);
+    sm.erd[b][ch] = exp_of(f.end - f.md);
+  }
+  // ... of the sum over v: Ke dKe joins in step 8
+  const int col = i0 + 2 * (lane & 3);  // this thread's channels: col + 8 n, + 1
+  __syncthreads();
+  float ke_sum[8][2];
+#pragma unroll
+  for (int n = 0; n < 8; ++n) ke_sum[n][0] = ke_sum[n][1] = 0.f;
+  {
+    // Ke = k dn exp(end - md) exp(later blocks): the column accumulator times it, before the decays go in
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = col + n * 8 + e;
+        float fct = sm.erd[I][i];
+        for (int j = I + 1; j < kNB; ++j) fct *= sm.emu[j][i] * sm.eru[j][i];
+        ke_sum[n][e] = fct * (pr.kd[row][i] * dkc[n][e] + pr.kd[row + 8][i] * dkc[n][2 + e]);
+      }
+  }
+
+  // ---- 7. the pairs
+  const bool exact = sm.exact[I] != 0;
+  for (int J = 0; J <= I; ++J) {  // row blocks: earlier tokens
+    scale_cols(dq, &(J < I ? sm.emd : sm.emu)[J][col]);
+    scale_cols(dkr, &(J < I ? sm.emd : sm.emu)[J][col]);
+    if (J == I && exact) break;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t ph[4], pl[4], ah[4], al[4];
+      pair_a<false>(pr.dp, I * 16, J * 16, kk, lane, ph, pl);
+      pair_a<false>(pr.da, I * 16, J * 16, kk, lane, ah, al);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        uint32_t bh[2], bl[2];
+        pair_b(pr.kd, J * 16, kk, i0 + n * 8, lane, bh, bl);
+        mma3_tf32(dq[n], ph, pl, bh, bl);
+        mma3_tf32(dkr[n], ah, al, bh, bl);
+      }
+    }
+    if (J < I) {
+      scale_cols(dq, &sm.erd[J][col]);
+      scale_cols(dkr, &sm.erd[J][col]);
+    }
+  }
+  for (int J = kNB - 1; J >= I; --J) {  // column blocks: later tokens
+    scale_cols(dkc, &(J > I ? sm.eru : sm.erd)[J][col]);
+    if (J == I && exact) break;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t ph[4], pl[4], ah[4], al[4];
+      pair_a<true>(pr.dp, I * 16, J * 16, kk, lane, ph, pl);
+      pair_a<true>(pr.da, I * 16, J * 16, kk, lane, ah, al);
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        uint32_t bh[2], bl[2];
+        pair_b(pr.qu, J * 16, kk, i0 + n * 8, lane, bh, bl);
+        mma3_tf32(dkc[n], ph, pl, bh, bl);
+        pair_b(pr.ku, J * 16, kk, i0 + n * 8, lane, bh, bl);
+        mma3_tf32(dkc[n], ah, al, bh, bl);
+      }
+    }
+    if (J > I) scale_cols(dkc, &sm.emu[J][col]);
+  }
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = row + (e >> 1) * 8, i = col + n * 8 + (e & 1);
+      const float u = pr.up[t][i];
+      dq[n][e] *= u;
+      dkr[n][e] *= u;
+      dkc[n][e] *= pr.dn[t][i];
+      if (exact) {
+        const float3 d = grad_exact_element(p, pr, I, pos.tok, tc, h, t, i);
+        dq[n][e] += d.x;
+        dkr[n][e] += d.y;
+        dkc[n][e] += d.z;
+      }
+    }
+  __syncthreads();  // the factors are dead: the decays' gradients go over them
+  // ---- 8. dq, dk; dg by a sum from the chunk's end
+  float (*const dgam)[kGP] = pr.up;
+  float (*const keb)[kK] = reinterpret_cast<float (*)[kK]>(&pr.ku[0][0]);  // [4 row blocks x 8 rows][128]
+  float (*const ev)[kK] = reinterpret_cast<float (*)[kK]>(&pr.qu[0][0]);   // [4][128]
+  ev[tid >> 6][(tid & 63) * 2] = e0;
+  ev[tid >> 6][(tid & 63) * 2 + 1] = e1;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) keb[I * 8 + (lane >> 2)][col + n * 8 + e] = ke_sum[n][e];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int t = row + hf * 8, i = col + n * 8;
+      float g0 = 0.f, g1 = 0.f;
+      if (t < tc) {
+        const int64_t tk = pos.tok + t;
+        const float2 q = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.q + tk * p.q_ts + h * kK + i));
+        const float2 k = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.k + tk * p.k_ts + h * kK + i));
+        const float q0 = dq[n][2 * hf], q1 = dq[n][2 * hf + 1], r0 = dkr[n][2 * hf], r1 = dkr[n][2 * hf + 1];
+        const float c0 = dkc[n][2 * hf], c1 = dkc[n][2 * hf + 1];
+        *reinterpret_cast<__nv_bfloat162*>(p.dq + tk * p.dq_ts + h * kK + i) = __floats2bfloat162_rn(q0, q1);
+        *reinterpret_cast<__nv_bfloat162*>(p.dk + tk * p.dk_ts + h * kK + i) = __floats2bfloat162_rn(r0 + c0, r1 + c1);
+        g0 = fmaf(q.x, q0, k.x * (r0 - c0));
+        g1 = fmaf(q.y, q1, k.y * (r1 - c1));
+      }
+      *reinterpret_cast<float2*>(&dgam[t][i]) = make_float2(g0, g1);
+    }
+  }
+  __syncthreads();
+  {
+    float sum = 0.f;  // tokens 32 half .. + 31, from the end
+    for (int t = 31; t >= 0; --t) sum += dgam[half * 32 + t][ch];
+    if (half == 1) sm.tail[1][ch] = sum;
+    else {
+      float e = (ev[0][ch] + ev[1][ch]) + (ev[2][ch] + ev[3][ch]);
+      for (int w = 0; w < 32; ++w) e += keb[w][ch];
+      sm.tail[0][ch] = e;
+    }
+    __syncthreads();
+    float acc = sm.tail[0][ch] + (half == 0 ? sm.tail[1][ch] : 0.f);
+    for (int t = 31; t >= 0; --t) {
+      const int tt = half * 32 + t;
+      acc += dgam[tt][ch];
+      if (tt < tc) p.dg[(pos.tok + tt) * p.dg_ts + h * kK + ch] = acc;
+    }
+  }
+}
+
+}  // namespace kdal
