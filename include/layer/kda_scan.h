@@ -43,7 +43,7 @@
  *
  * Accuracy.  States, sums and every fp32 result are computed to fp32 accuracy
  * (operands as fp16 or tf32 pairs of 22 bits, fp32 accumulation, decays
- * accumulated in fp64); bf16 results are rounded once.  An infinity or NaN in a
+ * accumulated in pairs of fp32); bf16 results are rounded once.  An infinity or NaN in a
  * sequence's inputs makes that sequence's and head's results undefined from
  * its chunk (64 tokens) on, nothing else.
  *
@@ -55,7 +55,7 @@
  * workspace first (any contents).  Calls that share a workspace must be
  * ordered.  Its first int32 is an error word: the kernels' waits for their
  * copies are bounded, and one that ever gives up stores 1 there and leaves
- * results unwritten; the library never clears it.
+ * results undefined; the library never clears it.
  *
  * Execution: kda_scan enqueues 2 kernels, kda_scan_backward 2 (4 with saved =
  * 0) on `stream`; no host synchronisation; can be captured in a CUDA graph.

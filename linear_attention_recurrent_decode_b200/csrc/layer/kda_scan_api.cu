@@ -13,8 +13,12 @@ namespace {
 using namespace kda_layer;
 namespace ks = kdal;
 
-constexpr int kChainForwardSmem = static_cast<int>(sizeof(ks::ChainSmem));
-constexpr int chain_backward_smem(int warps) { return kChainForwardSmem + warps * ks::kDoBytes; }
+template <int STRIPS>
+constexpr int kForwardSmem = static_cast<int>(sizeof(typename ks::ChainCfg<STRIPS>::Forward));
+template <int STRIPS>
+constexpr int kBackwardSmem = static_cast<int>(sizeof(typename ks::ChainCfg<STRIPS>::Backward));
+static_assert(kForwardSmem<4> <= 232448 && kBackwardSmem<4> <= 232448 && kForwardSmem<2> <= 232448 && kBackwardSmem<2> <= 232448,
+              "shared memory of an SM");
 
 // Dynamic shared memory allowances, once per device.
 cudaError_t prepare_kernels() {
@@ -28,10 +32,12 @@ cudaError_t prepare_kernels() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
   allow(ks::kda_scan_prep_kernel, static_cast<int>(sizeof(ks::PrepSmem)));
-  allow(ks::kda_scan_forward_kernel<4>, kChainForwardSmem);
-  allow(ks::kda_scan_forward_kernel<8>, kChainForwardSmem);
-  allow(ks::kda_scan_backward_kernel<4>, chain_backward_smem(4));
-  allow(ks::kda_scan_backward_kernel<8>, chain_backward_smem(8));
+  allow(ks::kda_scan_forward_kernel<1>, kForwardSmem<1>);
+  allow(ks::kda_scan_forward_kernel<2>, kForwardSmem<2>);
+  allow(ks::kda_scan_forward_kernel<4>, kForwardSmem<4>);
+  allow(ks::kda_scan_backward_kernel<1>, kBackwardSmem<1>);
+  allow(ks::kda_scan_backward_kernel<2>, kBackwardSmem<2>);
+  allow(ks::kda_scan_backward_kernel<4>, kBackwardSmem<4>);
   allow(ks::kda_scan_grad_kernel, static_cast<int>(sizeof(ks::GradSmem)));
   if (e == cudaSuccess && bit) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -140,16 +146,25 @@ bool launch(F kernel, int64_t grid, int threads, int smem, kda_stream_t stream, 
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
 }
 
-// Value columns per CTA of the chain kernels: 16 a warp.  Four warps give one
-// to each of an SM's schedulers; eight halve the CTAs (and the copies of a
-// chunk's tiles) once four would need more than one CTA per SM.
-bool wide_chain(int64_t units) { return units * 2 > sm_count(); }
+// Strips of 16 value columns a CTA of the chain kernels takes: one while every
+// strip can have an SM of its own, more as the CTAs would otherwise queue.
+int chain_strips(int64_t units) { return units * 8 <= sm_count() ? 1 : (units * 4 <= sm_count() ? 2 : 4); }
+
+template <int STRIPS>
+bool launch_chain(bool forward, const ks::ScanParams& p, kda_stream_t stream) {
+  const int64_t grid = p.N * p.HV * (8 / STRIPS);
+  return forward ? launch(ks::kda_scan_forward_kernel<STRIPS>, grid, STRIPS * 128, kForwardSmem<STRIPS>, stream, p)
+                 : launch(ks::kda_scan_backward_kernel<STRIPS>, grid, STRIPS * 128, kBackwardSmem<STRIPS>, stream, p);
+}
+bool launch_chain(bool forward, const ks::ScanParams& p, kda_stream_t stream) {
+  const int strips = chain_strips(p.N * p.HV);
+  return strips == 1 ? launch_chain<1>(forward, p, stream)
+                     : (strips == 2 ? launch_chain<2>(forward, p, stream) : launch_chain<4>(forward, p, stream));
+}
 
 bool launch_forward(const ks::ScanParams& p, int64_t slots, kda_stream_t stream) {
-  const int64_t units = p.N * p.HV;
-  if (!launch(ks::kda_scan_prep_kernel, slots * p.HV, ks::kPrepThreads, sizeof(ks::PrepSmem), stream, p)) return false;
-  return wide_chain(units) ? launch(ks::kda_scan_forward_kernel<8>, units, 8 * 32, kChainForwardSmem, stream, p)
-                           : launch(ks::kda_scan_forward_kernel<4>, units * 2, 4 * 32, kChainForwardSmem, stream, p);
+  return launch(ks::kda_scan_prep_kernel, slots * p.HV, ks::kPrepThreads, sizeof(ks::PrepSmem), stream, p) &&
+         launch_chain(true, p, stream);
 }
 
 }  // namespace
@@ -237,11 +252,7 @@ kda_status kda_scan_backward(const kda_scan_args* args, const kda_scan_grads* gr
   p.dbeta = d.dbeta, p.dbeta_ts = d.dbeta_row_stride;
   p.d_init = d.d_initial_state;
   if (!d.saved && !launch_forward(p, slots, stream)) return KDA_ERR_CUDA;  // p.out is null: states only
-  const int64_t units = a.N * a.HV;
-  const bool ok = wide_chain(units)
-                      ? launch(ks::kda_scan_backward_kernel<8>, units, 8 * 32, chain_backward_smem(8), stream, p)
-                      : launch(ks::kda_scan_backward_kernel<4>, units * 2, 4 * 32, chain_backward_smem(4), stream, p);
-  if (!ok) return KDA_ERR_CUDA;
+  if (!launch_chain(false, p, stream)) return KDA_ERR_CUDA;
   return launch(ks::kda_scan_grad_kernel, slots * a.HV, ks::kGradThreads, sizeof(ks::GradSmem), stream, p) ? KDA_OK
                                                                                                           : KDA_ERR_CUDA;
 }

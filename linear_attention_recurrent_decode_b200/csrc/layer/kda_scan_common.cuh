@@ -43,7 +43,6 @@ struct Record {
   static constexpr int kDecay = 0;     // [128] exp(Gamma_C)
   static constexpr int kBeta = 128;    // [64]
   static constexpr int kScWr = 192, kScKe = 193, kScQt = 194, kScP = 195, kScY = 196;
-  static constexpr int kScS = 200, kScR = 208, kScDS = 216, kScDU = 224;  // [8] each: per 16 value columns
   // byte offsets
   static constexpr int kHdr = 1024;
   static constexpr int kPlane = kC * kK * 2;       // 16 KB: a [64][128] (or [128][64]) plane
@@ -58,7 +57,11 @@ struct Record {
   static constexpr int kR = kS + kV * kK * 4;      // r^T  [v][t] hi, lo
   static constexpr int kDS = kR + 2 * kPlane;      // dS1^T [v][i] hi, lo
   static constexpr int kDU = kDS + kV * kK * 4;    // dU^T [v][t] hi, lo
-  static constexpr int64_t kTraining = kDU + 2 * kPlane;
+  // Scales of the last four, floats [8][4] each: per 16 value columns and per
+  // quarter of the channels (S, dS) or of the tokens (r, dU).
+  static constexpr int kSc = kDU + 2 * kPlane;
+  static constexpr int kScS = 0, kScR = 32, kScDS = 64, kScDU = 96, kScBytes = 512;
+  static constexpr int64_t kTraining = kSc + kScBytes;
 };
 constexpr int64_t kWsHeader = 256;  // word 0: the error word
 
@@ -123,18 +126,35 @@ __device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot, Ch
   return *sh;
 }
 
-// exp of an fp64 argument to fp32 accuracy: the remainder of rounding it is
-// below half an ulp and enters to first order.
-__device__ __forceinline__ float exp_of(double x) {
-  const float hi = static_cast<float>(x);
-  return expf(hi) * (1.f + static_cast<float>(x - static_cast<double>(hi)));
+// ---------------------------------------------------------------- decays
+// A log-decay sum as an unevaluated pair of floats: the low part takes what
+// rounding the high part dropped.  A plain fp32 sum over a chunk's tokens is
+// off by 1e-6 and more, and so would be the decays (fp64 is exact enough but
+// measured 3 us more per chunk here, mostly in its conversions).
+struct Sum {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum add(Sum a, float b) {
+  const float s = a.hi + b, v = s - a.hi;
+  return Sum{s, a.lo + ((a.hi - (s - v)) + (b - v))};
+}
+__device__ __forceinline__ Sum add(Sum a, Sum b) {
+  Sum r = add(a, b.hi);
+  r.lo += b.lo;
+  return r;
+}
+__device__ __forceinline__ Sum neg(Sum a) { return Sum{-a.hi, -a.lo}; }
+// exp of a pair: the low part enters to first order.
+__device__ __forceinline__ float exp_of(Sum x) {
+  const float e = expf(x.hi);
+  return fmaf(e, x.lo, e);
 }
 // A log-decay; below -1e4 the decay is zero either way (and -inf would make NaN of differences).
 __device__ __forceinline__ float log_decay(float g) { return g < -1e4f ? -1e4f : g; }
 
 // Largest |L - mid| a sub-block may have for its factors exp(+-(L - mid)): they
 // and the products of two stay normal fp32 numbers.
-constexpr double kSafe = 60.0;
+constexpr float kSafe = 60.f;
 
 // The decay factors of one sub-block and key channel.  L_t is the cumulative
 // log-decay from the sub-block's start.  up[t] = exp(L_t - mu), dn[t] = exp(md
@@ -143,31 +163,40 @@ constexpr double kSafe = 60.0;
 // (each factor at most 1 for g <= 0) and pairs inside the sub-block are formed
 // one by one from the differences (`exact`).
 struct SubFactors {
-  double mu, md, end;
+  Sum mu, md, end;
   bool exact;
 };
 __device__ __forceinline__ SubFactors sub_factors(const float (&g)[kB], float (&up)[kB], float (&dn)[kB]) {
   SubFactors f;
-  double acc = 0.0, lo = 1e300, hi = -1e300;
+  Sum L[kB];
+  Sum acc{0.f, 0.f};
+  float lo = 3e38f, hi = -3e38f;
 #pragma unroll
   for (int t = 0; t < kB; ++t) {
-    acc += static_cast<double>(g[t]);
-    lo = fmin(lo, acc);
-    hi = fmax(hi, acc);
+    acc = add(acc, g[t]);
+    L[t] = acc;
+    lo = fminf(lo, acc.hi);
+    hi = fmaxf(hi, acc.hi);
   }
   f.end = acc;
-  f.exact = !(hi - lo <= 2 * kSafe);
-  f.mu = f.exact ? 0.0 : 0.5 * (hi + lo);
+  f.exact = !(hi - lo <= 2.f * kSafe);
+  const float mid = 0.5f * (hi + lo);
+  f.mu = Sum{f.exact ? 0.f : mid, 0.f};
   f.md = f.exact ? acc : f.mu;
-  acc = 0.0;
 #pragma unroll
   for (int t = 0; t < kB; ++t) {
-    acc += static_cast<double>(g[t]);
-    const float x = static_cast<float>(acc - f.mu);
-    up[t] = expf(x);
-    dn[t] = expf(f.exact ? static_cast<float>(f.md - acc) : -x);
+    const Sum x = add(L[t], -f.mu.hi);
+    up[t] = exp_of(x);
+    dn[t] = exp_of(f.exact ? add(f.md, neg(L[t])) : neg(x));
   }
   return f;
+}
+
+// Round-to-nearest split of an fp32 value into a tf32 pair (the MMA reads the
+// upper 19 bits of each).
+__device__ __forceinline__ void tf32_pair(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 }  // namespace kdal

@@ -24,7 +24,7 @@
 
 namespace kdal {
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;  // 256 left the schedulers short of warps: each phase waits on its own loads
 constexpr int kGP = kK + 8;  // padded rows of the fp32 factors, read as [k][n] fragments
 constexpr int kDP = kC + 4;
 
@@ -38,9 +38,10 @@ struct GradSmem {
   // exp(mu), exp(md), exp(end - mu), exp(end - md) per sub-block and channel
   float emu[kNB][kK], emd[kNB][kK], eru[kNB][kK], erd[kNB][kK];
   float hdr[Record::kHdr / 4];
-  float tail[2][kK];                         // sum_v S1 dS1, in two parts
+  float sc[Record::kScBytes / 4];
+  float tail[kNB][kK];                       // the decays' gradients, summed per sub-block
   float dbeta[8][kC];
-  float sc_dr[8];
+  float sc_dr[8][kNB];
   uint32_t mx_do;
   int exact[kNB];
   uint64_t bar[2];
@@ -53,6 +54,7 @@ struct GradPairs {  // over s0 .. dO once those are dead
 };
 static_assert(sizeof(GradPairs) <= offsetof(GradSmem, emu), "the factors fit over the operand tiles");
 static_assert(2 * sizeof(float) * kC * kDP <= kV * kK * 4, "dP and dA fit over S0");
+static_assert(sizeof(GradSmem) <= 232448, "shared memory of an SM");
 
 // Direct sums inside sub-block b (its decays are out of the factors' range):
 // one accumulator element (t, i), pairs from the log-decays between them.
@@ -76,30 +78,41 @@ __device__ __noinline__ float3 grad_exact_element(const ScanParams& p, const Gra
   return make_float3(dq, dkr, dkc);
 }
 
-// acc [16 x 64] += a [16 x 16] x (b rows k0.., channels i0..), a stored [row][k] (or [k][row] if TRANS).
+// A operand a (rows r0.., k0.. k), stored [row][k] (or [k][row] if TRANS); B operand b rows k0.., channels i0...
 template <bool TRANS>
-__device__ __forceinline__ void pair_a(const float (*a)[kDP], int r0, int k0, int kk, int lane, uint32_t (&ah)[4], uint32_t (&al)[4]) {
+__device__ __forceinline__ void pair_a(const float (*a)[kDP], int r0, int k0, int lane, uint32_t (&ah)[4], uint32_t (&al)[4]) {
   const int r = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int row = r0 + r + (j & 1) * 8, k = k0 + kk * 8 + c + (j >> 1) * 4;
-    tf32_split(TRANS ? a[k][row] : a[row][k], ah[j], al[j]);
+    const int row = r0 + r + (j & 1) * 8, k = k0 + c + (j >> 1) * 4;
+    tf32_pair(TRANS ? a[k][row] : a[row][k], ah[j], al[j]);
   }
 }
-__device__ __forceinline__ void pair_b(const float (*b)[kGP], int k0, int kk, int i0, int lane, uint32_t (&bh)[2], uint32_t (&bl)[2]) {
+__device__ __forceinline__ void pair_b(const float (*b)[kGP], int k0, int i0, int lane, uint32_t (&bh)[2], uint32_t (&bl)[2]) {
   const int r = lane >> 2, c = lane & 3;
-  tf32_split(b[k0 + kk * 8 + c][i0 + r], bh[0], bl[0]);
-  tf32_split(b[k0 + kk * 8 + c + 4][i0 + r], bh[1], bl[1]);
+  tf32_pair(b[k0 + c][i0 + r], bh[0], bl[0]);
+  tf32_pair(b[k0 + c + 4][i0 + r], bh[1], bl[1]);
 }
-__device__ __forceinline__ void scale_cols(float (&acc)[8][4], const float* f) {
+// c += (ah + al) (bh + bl) without al.bl, the cross terms first.
+__device__ __forceinline__ void mma3_tf32(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2],
+                                          const uint32_t (&bl)[2]) {
+  mma_tf32(c, ah, bl);
+  mma_tf32(c, al, bh);
+  mma_tf32(c, ah, bh);
+}
+__device__ __forceinline__ void scale_cols(float (&acc)[4][4], const float* f) {
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
+  for (int n = 0; n < 4; ++n) {
     const float2 d = *reinterpret_cast<const float2*>(f + n * 8);
     acc[n][0] *= d.x;
     acc[n][1] *= d.y;
     acc[n][2] *= d.x;
     acc[n][3] *= d.y;
   }
+}
+__device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&x)[4], float f) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = fmaf(x[e], f, acc[e]);
 }
 
 __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __grid_constant__ ScanParams p) {
@@ -121,8 +134,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   __syncthreads();
   const unsigned char* const rec = record(p, slot, h);
   if (tid == 0) {
-    mbar_expect(&sm.bar[0], Record::kHdr + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
+    mbar_expect(&sm.bar[0], Record::kHdr + Record::kScBytes + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
     bulk_load(sm.hdr, rec, Record::kHdr, &sm.bar[0]);
+    bulk_load(sm.sc, rec + Record::kSc, Record::kScBytes, &sm.bar[0]);
     bulk_load(sm.ds, rec + Record::kDU, 2 * Record::kPlane, &sm.bar[0]);
     bulk_load(sm.ds + 2 * Record::kPlane, rec + Record::kY, kC * kC * 4, &sm.bar[0]);
     bulk_load(sm.r, rec + Record::kR, 2 * Record::kPlane, &sm.bar[0]);
@@ -130,10 +144,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   }
   // ---- dO as an fp16 tile (exact after scaling)
   {
-    uint4 raw[4];
+    uint4 raw[2];
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int c = tid + j * kGradThreads, t = c >> 4, pc = c & 15;
       raw[j] = t < tc ? *reinterpret_cast<const uint4*>(p.d_out + (pos.tok + t) * p.d_out_ts + h * kV + pc * 8) : make_uint4(0, 0, 0, 0);
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
@@ -146,7 +160,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     __syncthreads();
     const float sc = pow2_scale(__uint_as_float(sm.mx_do));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int c = tid + j * kGradThreads, t = c >> 4, pc = c & 15;
       uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
@@ -163,39 +177,43 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   const uint32_t a_s0 = smem_addr(sm.s0), a_ds = smem_addr(sm.ds), a_dr = smem_addr(sm.dr), a_r = smem_addr(sm.r), a_do = smem_addr(sm.dO);
   const float* const beta = sm.hdr + Record::kBeta;
 
-  // ---- 1. y^T = dU^T - dU^T (beta Y); dR, dV, dbeta: warp = 16 value columns
+  // ---- 1. y^T = dU^T - dU^T (beta Y); dR, dV, dbeta: warp = 16 value columns, token sub-blocks 0 and 3 or 1 and 2
+  // (five products each)
   {
-    const int v0 = warp * 16;
+    const int grp = warp & 7, v0 = grp * 16, first = warp >> 3;
     const uint32_t a_y = a_ds + 2 * Record::kPlane;
-    uint32_t uh[4][4], ul[4][4];
-    float acc[8][4] = {};
+    __nv_bfloat16* const dv = p.dv + pos.tok * p.dv_ts + h * kV + v0;
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {  // s sub-block; Y[s][t] is zero for t >= s
-      load_a<64>(a_ds, v0, kk * 16, lane, uh[kk]);
-      load_a<64>(a_ds + Record::kPlane, v0, kk * 16, lane, ul[kk]);
-#pragma unroll
-      for (int nb = 0; nb <= kk; ++nb) {
+    for (int u = 0; u < 2; ++u) {
+      const int nb = u ? 3 - first : first;  // the sub-block of tokens
+      float acc[2][4] = {};
+      uint32_t dh[4], dl[4];
+      for (int kk = 3; kk >= nb; --kk) {     // s sub-block; Y[s][t] is zero for t >= s
         uint32_t bh[4], bl[4];
+        load_a<64>(a_ds, v0, kk * 16, lane, dh);
+        load_a<64>(a_ds + Record::kPlane, v0, kk * 16, lane, dl);
         load_b_t<64>(a_y, kk * 16, nb * 16, lane, bh);
         load_b_t<64>(a_y + kC * kC * 2, kk * 16, nb * 16, lane, bl);
-        mma3(acc[2 * nb], acc[2 * nb + 1], uh[kk], ul[kk], bh, bl);
+        float x[2][4] = {};
+        mma_pair(x[0], x[1], dh, bl);
+        mma_pair(x[0], x[1], dl, bh);
+        mma_pair(x[0], x[1], dh, bh);
+        const float f = pow2_inv(sm.sc[Record::kScDU + grp * 4 + kk]) * pow2_inv(sm.hdr[Record::kScY]);
+        add_scaled(acc[0], x[0], f);
+        add_scaled(acc[1], x[1], f);
       }
-    }
-    const float inv = pow2_inv(sm.hdr[Record::kScDU + warp]), inv_y = inv * pow2_inv(sm.hdr[Record::kScY]);
-    const float inv_r = pow2_inv(sm.hdr[Record::kScR + warp]);
-    float m = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
+      // dh, dl now hold the sub-block's own dU
+      const float inv = pow2_inv(sm.sc[Record::kScDU + grp * 4 + nb]), inv_r = pow2_inv(sm.sc[Record::kScR + grp * 4 + nb]);
       uint32_t rh[4], rl[4];
-      load_a<64>(a_r, v0, kk * 16, lane, rh);
-      load_a<64>(a_r + Record::kPlane, v0, kk * 16, lane, rl);
-      float db[4] = {0.f, 0.f, 0.f, 0.f};  // tokens kk 16 + 2 (lane & 3) + {0, 1, 8, 9}
+      load_a<64>(a_r, v0, nb * 16, lane, rh);
+      load_a<64>(a_r + Record::kPlane, v0, nb * 16, lane, rl);
+      float m = 0.f, db[4] = {0.f, 0.f, 0.f, 0.f};  // tokens nb 16 + 2 (lane & 3) + {0, 1, 8, 9}
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {        // fragment register j: rows + (j & 1) 8, columns + (j >> 1) 8
-        const float2 du = join2(uh[kk][j], ul[kk][j]), r = join2(rh[j], rl[j]);
-        float(&c)[4] = acc[2 * kk + (j >> 1)];
-        const int e = (j & 1) * 2, t = kk * 16 + (j >> 1) * 8 + 2 * (lane & 3);
-        const float y0 = fmaf(-c[e], inv_y, du.x * inv), y1 = fmaf(-c[e + 1], inv_y, du.y * inv);
+      for (int j = 0; j < 4; ++j) {  // fragment register j: rows + (j & 1) 8, columns + (j >> 1) 8
+        const float2 du = join2(dh[j], dl[j]), r = join2(rh[j], rl[j]);
+        float(&c)[4] = acc[j >> 1];
+        const int e = (j & 1) * 2, t = nb * 16 + (j >> 1) * 8 + 2 * (lane & 3);
+        const float y0 = fmaf(du.x, inv, -c[e]), y1 = fmaf(du.y, inv, -c[e + 1]);
         db[(j >> 1) * 2] = fmaf(y0, r.x * inv_r, db[(j >> 1) * 2]);
         db[(j >> 1) * 2 + 1] = fmaf(y1, r.y * inv_r, db[(j >> 1) * 2 + 1]);
         c[e] = y0 * beta[t];
@@ -206,18 +224,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
-        if (lane < 4) sm.dbeta[warp][kk * 16 + (j >> 1) * 8 + 2 * lane + (j & 1)] = db[j];
+        if (lane < 4) sm.dbeta[grp][nb * 16 + (j >> 1) * 8 + 2 * lane + (j & 1)] = db[j];
       }
-    }
-    const float sc = pow2_scale(warp_max(m));
-    if (lane == 0) sm.sc_dr[warp] = sc;
-    __nv_bfloat16* const dv = p.dv + pos.tok * p.dv_ts + h * kV + v0;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t ah[4], al[4];
-      frag_a(acc[2 * kk], acc[2 * kk + 1], sc, ah, al);
-      store_frag<64>(sm.dr, Record::kPlane, v0, kk * 16, lane, ah, al);
-      store_out16(dv, p.dv_ts, kk * 16, tc, lane, acc[2 * kk], acc[2 * kk + 1], 1.f);
+      const float sc = pow2_scale(warp_max(m));
+      if (lane == 0) sm.sc_dr[grp][nb] = sc;
+      frag_a(acc[0], acc[1], sc, dh, dl);
+      store_frag<64>(sm.dr, Record::kPlane, v0, nb * 16, lane, dh, dl);
+      store_out16(dv, p.dv_ts, nb * 16, tc, lane, acc[0], acc[1], 1.f);
     }
   }
   fence_async();  // the reads of dU and Y come before dS1 is copied over them
@@ -233,103 +246,81 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     p.dbeta[(pos.tok + tid) * p.dbeta_ts + h] = s;
   }
 
-  // ---- 2. dQt = scale dO S0^T and dKt = -dR S0^T: warp = 16 tokens x 64 channels.  The value columns
-  // (contracted here) have a scale per group of 16, one k step: the common scale is put on the left operand.
-  const int I = warp & 3, i0 = (warp >> 2) * 64;
-  float c_s = sm.hdr[Record::kScS], c_dr = sm.sc_dr[0], c_r = sm.hdr[Record::kScR], c_ds = sm.hdr[Record::kScDS];
-  float c_dr_s = sm.sc_dr[0] * sm.hdr[Record::kScS], c_r_ds = sm.hdr[Record::kScR] * sm.hdr[Record::kScDS];
-  float c_dr_r = sm.sc_dr[0] * sm.hdr[Record::kScR];
-#pragma unroll
-  for (int g = 1; g < 8; ++g) {
-    c_s = fminf(c_s, sm.hdr[Record::kScS + g]);
-    c_dr = fminf(c_dr, sm.sc_dr[g]);
-    c_r = fminf(c_r, sm.hdr[Record::kScR + g]);
-    c_ds = fminf(c_ds, sm.hdr[Record::kScDS + g]);
-    c_dr_s = fminf(c_dr_s, sm.sc_dr[g] * sm.hdr[Record::kScS + g]);
-    c_r_ds = fminf(c_r_ds, sm.hdr[Record::kScR + g] * sm.hdr[Record::kScDS + g]);
-    c_dr_r = fminf(c_dr_r, sm.sc_dr[g] * sm.hdr[Record::kScR + g]);
-  }
-  float dq[8][4] = {}, dkr[8][4] = {};
+  // ---- 2. dQt = scale dO S0^T and dKt = -dR S0^T: warp = 16 tokens x 32 channels, a partial sum per 16 value columns
+  const int I = warp & 3, i4 = warp >> 2, i0 = i4 * 32;
+  float dq[4][4] = {}, dkr[4][4] = {};
 #pragma unroll 2
   for (int g = 0; g < 8; ++g) {
     uint32_t a[4], ah[4], al[4];
     load_a<128>(a_do, I * 16, g * 16, lane, a);
     load_a_t<64>(a_dr, I * 16, g * 16, lane, ah);
     load_a_t<64>(a_dr + Record::kPlane, I * 16, g * 16, lane, al);
-    const float sc_s = sm.hdr[Record::kScS + g];
-    scale_frag(a, __float2half2_rn(c_s * pow2_inv(sc_s)));
-    const __half2 f = __float2half2_rn(c_dr_s * pow2_inv(sc_s) * pow2_inv(sm.sc_dr[g]));
-    scale_frag(ah, f);
-    scale_frag(al, f);
+    const float inv_s = pow2_inv(sm.sc[Record::kScS + g * 4 + i4]);
+    const float fq = inv_s * (pow2_inv(sc_do) * p.scale), fk = -inv_s * pow2_inv(sm.sc_dr[g][I]);
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
+    for (int nb = 0; nb < 2; ++nb) {
       uint32_t bh[4], bl[4];
       load_b_t<128>(a_s0, g * 16, i0 + nb * 16, lane, bh);
       load_b_t<128>(a_s0 + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
-      mma2(dq[2 * nb], dq[2 * nb + 1], a, bh, bl);
-      mma3(dkr[2 * nb], dkr[2 * nb + 1], ah, al, bh, bl);
-    }
-  }
-  {
-    const float fq = pow2_inv(sc_do) * pow2_inv(c_s) * p.scale, fk = -pow2_inv(c_dr_s);
+      float x[2][4] = {}, y[2][4] = {};
+      mma_pair(x[0], x[1], a, bl);
+      mma_pair(y[0], y[1], ah, bl);
+      mma_pair(y[0], y[1], al, bh);
+      mma_pair(x[0], x[1], a, bh);
+      mma_pair(y[0], y[1], ah, bh);
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dq[n][e] *= fq;
-        dkr[n][e] *= fk;
+      for (int j = 0; j < 2; ++j) {
+        add_scaled(dq[2 * nb + j], x[j], fq);
+        add_scaled(dkr[2 * nb + j], y[j], fk);
       }
+    }
   }
   if (!__syncthreads_and(mbar_wait(&sm.bar[1], 0))) {
     if (tid == 0) set_error(p);
     return;
   }
-  // ---- 3. exp(Gamma_C) sum_v S0 dS1 per channel: thread = two channels of a quarter of the value columns ...
+  // ---- 3. exp(Gamma_C) sum_v S0 dS1 per channel: thread = two channels of 16 value columns ...
   float e0 = 0.f, e1 = 0.f;
   {
-    const int i = (tid & 63) * 2, q4 = tid >> 6;
-#pragma unroll
-    for (int gg = 0; gg < 2; ++gg) {
-      const int g = q4 * 2 + gg;
-      float x0 = 0.f, x1 = 0.f;
+    const int i = (tid & 63) * 2, g = tid >> 6;
 #pragma unroll 4
-      for (int v = g * 16; v < g * 16 + 16; ++v) {
-        const uint32_t off = off128(v, i);
-        const float2 s = join2(*reinterpret_cast<const uint32_t*>(sm.s0 + off), *reinterpret_cast<const uint32_t*>(sm.s0 + kV * kK * 2 + off));
-        const float2 d = join2(*reinterpret_cast<const uint32_t*>(sm.ds + off), *reinterpret_cast<const uint32_t*>(sm.ds + kV * kK * 2 + off));
-        x0 = fmaf(s.x, d.x, x0);
-        x1 = fmaf(s.y, d.y, x1);
-      }
-      const float inv = pow2_inv(sm.hdr[Record::kScS + g]) * pow2_inv(sm.hdr[Record::kScDS + g]);
-      e0 = fmaf(x0, inv, e0);
-      e1 = fmaf(x1, inv, e1);
+    for (int v = g * 16; v < g * 16 + 16; ++v) {
+      const uint32_t off = off128(v, i);
+      const float2 s = join2(*reinterpret_cast<const uint32_t*>(sm.s0 + off), *reinterpret_cast<const uint32_t*>(sm.s0 + kV * kK * 2 + off));
+      const float2 d = join2(*reinterpret_cast<const uint32_t*>(sm.ds + off), *reinterpret_cast<const uint32_t*>(sm.ds + kV * kK * 2 + off));
+      e0 = fmaf(s.x, d.x, e0);
+      e1 = fmaf(s.y, d.y, e1);
     }
-    e0 *= sm.hdr[Record::kDecay + i];
-    e1 *= sm.hdr[Record::kDecay + i + 1];
+    const float inv = pow2_inv(sm.sc[Record::kScS + g * 4 + (i >> 5)]) * pow2_inv(sm.sc[Record::kScDS + g * 4 + (i >> 5)]);
+    e0 *= inv * sm.hdr[Record::kDecay + i];
+    e1 *= inv * sm.hdr[Record::kDecay + i + 1];
   }
   // ---- 4. dKe = (beta r) dS1^T
-  float dkc[8][4] = {};
+  float dkc[4][4] = {};
 #pragma unroll 2
   for (int g = 0; g < 8; ++g) {
     uint32_t ah[4], al[4];
     load_a_t<64>(a_r, I * 16, g * 16, lane, ah);
     load_a_t<64>(a_r + Record::kPlane, I * 16, g * 16, lane, al);
-    const __half2 f = __float2half2_rn(c_r_ds * pow2_inv(sm.hdr[Record::kScR + g]) * pow2_inv(sm.hdr[Record::kScDS + g]));
-    scale_frag(ah, f);
-    scale_frag(al, f);
+    const float f = pow2_inv(sm.sc[Record::kScR + g * 4 + I]) * pow2_inv(sm.sc[Record::kScDS + g * 4 + i4]);
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
+    for (int nb = 0; nb < 2; ++nb) {
       uint32_t bh[4], bl[4];
       load_b_t<128>(a_ds, g * 16, i0 + nb * 16, lane, bh);
       load_b_t<128>(a_ds + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
-      mma3(dkc[2 * nb], dkc[2 * nb + 1], ah, al, bh, bl);
+      float x[2][4] = {};
+      mma_pair(x[0], x[1], ah, bl);
+      mma_pair(x[0], x[1], al, bh);
+      mma_pair(x[0], x[1], ah, bh);
+      add_scaled(dkc[2 * nb], x[0], f);
+      add_scaled(dkc[2 * nb + 1], x[1], f);
     }
   }
   const int row = I * 16 + (lane >> 2);  // this thread's rows: row, row + 8
   {
-    const float inv = pow2_inv(c_r_ds), b0 = beta[row] * inv, b1 = beta[row + 8] * inv;
+    const float b0 = beta[row], b1 = beta[row + 8];
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
+    for (int n = 0; n < 4; ++n) {
       dkc[n][0] *= b0;
       dkc[n][1] *= b0;
       dkc[n][2] *= b1;
@@ -337,87 +328,84 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     }
   }
   __syncthreads();  // every warp is done with S0 (and with the sums over it)
-  // ---- 5. dP and dA over S0, a 16 x 16 block at a time (zeros above the diagonal)
-  for (int u = warp; u < 16; u += 8) {
-    const int ti = u >> 2, si = u & 3;
+  // ---- 5. dP and dA over S0, 16 x 16 a warp (none above the diagonal)
+  if (const int ti = warp >> 2, si = warp & 3; si <= ti) {
     const int t = ti * 16 + (lane >> 2), s = si * 16 + 2 * (lane & 3);
     float cp[2][4] = {}, ca[2][4] = {};
-    if (si <= ti) {
 #pragma unroll 2
-      for (int g = 0; g < 8; ++g) {
-        uint32_t a[4], ah[4], al[4], bh[4], bl[4];
-        load_a<128>(a_do, ti * 16, g * 16, lane, a);
-        load_a_t<64>(a_dr, ti * 16, g * 16, lane, ah);
-        load_a_t<64>(a_dr + Record::kPlane, ti * 16, g * 16, lane, al);
-        load_b_t<64>(a_r, g * 16, si * 16, lane, bh);
-        load_b_t<64>(a_r + Record::kPlane, g * 16, si * 16, lane, bl);
-        const float sc_r = sm.hdr[Record::kScR + g];
-        scale_frag(a, __float2half2_rn(c_r * pow2_inv(sc_r)));
-        const __half2 f = __float2half2_rn(c_dr_r * pow2_inv(sc_r) * pow2_inv(sm.sc_dr[g]));
-        scale_frag(ah, f);
-        scale_frag(al, f);
-        mma2(cp[0], cp[1], a, bh, bl);
-        mma3(ca[0], ca[1], ah, al, bh, bl);
+    for (int g = 0; g < 8; ++g) {
+      uint32_t a[4], ah[4], al[4], bh[4], bl[4];
+      load_a<128>(a_do, ti * 16, g * 16, lane, a);
+      load_a_t<64>(a_dr, ti * 16, g * 16, lane, ah);
+      load_a_t<64>(a_dr + Record::kPlane, ti * 16, g * 16, lane, al);
+      load_b_t<64>(a_r, g * 16, si * 16, lane, bh);
+      load_b_t<64>(a_r + Record::kPlane, g * 16, si * 16, lane, bl);
+      const float inv_r = pow2_inv(sm.sc[Record::kScR + g * 4 + si]);
+      const float fp = inv_r * (pow2_inv(sc_do) * p.scale), fa = -inv_r * pow2_inv(sm.sc_dr[g][ti]);
+      float x[2][4] = {}, y[2][4] = {};
+      mma_pair(x[0], x[1], a, bl);
+      mma_pair(y[0], y[1], ah, bl);
+      mma_pair(y[0], y[1], al, bh);
+      mma_pair(x[0], x[1], a, bh);
+      mma_pair(y[0], y[1], ah, bh);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        add_scaled(cp[j], x[j], fp);
+        add_scaled(ca[j], y[j], fa);
       }
     }
-    const float fp = pow2_inv(sc_do) * pow2_inv(c_r) * p.scale, fa = -pow2_inv(c_dr_r);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int tt = t + (e >> 1) * 8, ss = s + n * 8 + (e & 1);
         const float b = beta[ss];
-        pr.dp[tt][ss] = ss <= tt ? cp[n][e] * fp * b : 0.f;
-        pr.da[tt][ss] = ss < tt ? ca[n][e] * fa * b : 0.f;
+        pr.dp[tt][ss] = ss <= tt ? cp[n][e] * b : 0.f;
+        pr.da[tt][ss] = ss < tt ? ca[n][e] * b : 0.f;
       }
   }
   __syncthreads();  // every warp is done with the operand tiles
   // ---- 6. decay factors
-  const int ch = tid & (kK - 1), half = tid >> 7;
+  const int ch = tid & (kK - 1), sub = tid >> 7;
+  {
+    float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
 #pragma unroll
-  for (int b2 = 0; b2 < 2; ++b2) {
-    const int b = half * 2 + b2;
-    float g[kB], up[kB], dn[kB];
-#pragma unroll
-    for (int t = 0; t < kB; ++t)
-      g[t] = b * kB + t < tc ? log_decay(__ldg(p.g + (pos.tok + b * kB + t) * p.g_ts + h * kK + ch)) : 0.f;
+    for (int t = 0; t < kB; ++t) {
+      const int64_t tk = pos.tok + sub * kB + t;
+      const bool in = sub * kB + t < tc;
+      g[t] = in ? log_decay(__ldg(p.g + tk * p.g_ts + h * kK + ch)) : 0.f;
+      kv[t] = in ? __bfloat162float(p.k[tk * p.k_ts + h * kK + ch]) : 0.f;
+      qv[t] = in ? __bfloat162float(p.q[tk * p.q_ts + h * kK + ch]) : 0.f;
+    }
     const SubFactors f = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
-      const int64_t tk = pos.tok + b * kB + t;
-      const bool in = b * kB + t < tc;
-      const float kv = in ? __bfloat162float(p.k[tk * p.k_ts + h * kK + ch]) : 0.f;
-      const float qv = in ? __bfloat162float(p.q[tk * p.q_ts + h * kK + ch]) : 0.f;
-      pr.up[b * kB + t][ch] = up[t];
-      pr.dn[b * kB + t][ch] = dn[t];
-      pr.ku[b * kB + t][ch] = kv * up[t];
-      pr.qu[b * kB + t][ch] = qv * up[t];
-      pr.kd[b * kB + t][ch] = kv * dn[t];
+      pr.up[sub * kB + t][ch] = up[t];
+      pr.dn[sub * kB + t][ch] = dn[t];
+      pr.ku[sub * kB + t][ch] = kv[t] * up[t];
+      pr.qu[sub * kB + t][ch] = qv[t] * up[t];
+      pr.kd[sub * kB + t][ch] = kv[t] * dn[t];
     }
-    if (f.exact) sm.exact[b] = 1;
-    sm.emu[b][ch] = exp_of(f.mu);
-    sm.emd[b][ch] = exp_of(f.md);
-    sm.eru[b][ch] = exp_of(f.end - f.mu);
-    sm.erd[b][ch] = exp_of(f.end - f.md);
+    if (f.exact) sm.exact[sub] = 1;
+    sm.emu[sub][ch] = exp_of(f.mu);
+    sm.emd[sub][ch] = exp_of(f.md);
+    sm.eru[sub][ch] = exp_of(add(f.end, neg(f.mu)));
+    sm.erd[sub][ch] = exp_of(add(f.end, neg(f.md)));
   }
   // ... of the sum over v: Ke dKe joins in step 8
   const int col = i0 + 2 * (lane & 3);  // this thread's channels: col + 8 n, + 1
   __syncthreads();
-  float ke_sum[8][2];
+  float ke_sum[4][2];
+  // Ke = k dn exp(end - md) exp(later blocks): the column accumulator times it, before the decays go in
 #pragma unroll
-  for (int n = 0; n < 8; ++n) ke_sum[n][0] = ke_sum[n][1] = 0.f;
-  {
-    // Ke = k dn exp(end - md) exp(later blocks): the column accumulator times it, before the decays go in
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = col + n * 8 + e;
-        float fct = sm.erd[I][i];
-        for (int j = I + 1; j < kNB; ++j) fct *= sm.emu[j][i] * sm.eru[j][i];
-        ke_sum[n][e] = fct * (pr.kd[row][i] * dkc[n][e] + pr.kd[row + 8][i] * dkc[n][2 + e]);
-      }
-  }
+    for (int e = 0; e < 2; ++e) {
+      const int i = col + n * 8 + e;
+      float fct = sm.erd[I][i];
+      for (int j = I + 1; j < kNB; ++j) fct *= sm.emu[j][i] * sm.eru[j][i];
+      ke_sum[n][e] = fct * (pr.kd[row][i] * dkc[n][e] + pr.kd[row + 8][i] * dkc[n][2 + e]);
+    }
 
   // ---- 7. the pairs
   const bool exact = sm.exact[I] != 0;
@@ -428,12 +416,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       uint32_t ph[4], pl[4], ah[4], al[4];
-      pair_a<false>(pr.dp, I * 16, J * 16, kk, lane, ph, pl);
-      pair_a<false>(pr.da, I * 16, J * 16, kk, lane, ah, al);
+      pair_a<false>(pr.dp, I * 16, J * 16 + kk * 8, lane, ph, pl);
+      pair_a<false>(pr.da, I * 16, J * 16 + kk * 8, lane, ah, al);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
+      for (int n = 0; n < 4; ++n) {
         uint32_t bh[2], bl[2];
-        pair_b(pr.kd, J * 16, kk, i0 + n * 8, lane, bh, bl);
+        pair_b(pr.kd, J * 16 + kk * 8, i0 + n * 8, lane, bh, bl);
         mma3_tf32(dq[n], ph, pl, bh, bl);
         mma3_tf32(dkr[n], ah, al, bh, bl);
       }
@@ -449,21 +437,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       uint32_t ph[4], pl[4], ah[4], al[4];
-      pair_a<true>(pr.dp, I * 16, J * 16, kk, lane, ph, pl);
-      pair_a<true>(pr.da, I * 16, J * 16, kk, lane, ah, al);
+      pair_a<true>(pr.dp, I * 16, J * 16 + kk * 8, lane, ph, pl);
+      pair_a<true>(pr.da, I * 16, J * 16 + kk * 8, lane, ah, al);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
+      for (int n = 0; n < 4; ++n) {
         uint32_t bh[2], bl[2];
-        pair_b(pr.qu, J * 16, kk, i0 + n * 8, lane, bh, bl);
+        pair_b(pr.qu, J * 16 + kk * 8, i0 + n * 8, lane, bh, bl);
         mma3_tf32(dkc[n], ph, pl, bh, bl);
-        pair_b(pr.ku, J * 16, kk, i0 + n * 8, lane, bh, bl);
+        pair_b(pr.ku, J * 16 + kk * 8, i0 + n * 8, lane, bh, bl);
         mma3_tf32(dkc[n], ah, al, bh, bl);
       }
     }
     if (J > I) scale_cols(dkc, &sm.emu[J][col]);
   }
 #pragma unroll
-  for (int n = 0; n < 8; ++n)
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int t = row + (e >> 1) * 8, i = col + n * 8 + (e & 1);
@@ -482,11 +470,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   // ---- 8. dq, dk; dg by a sum from the chunk's end
   float (*const dgam)[kGP] = pr.up;
   float (*const keb)[kK] = reinterpret_cast<float (*)[kK]>(&pr.ku[0][0]);  // [4 row blocks x 8 rows][128]
-  float (*const ev)[kK] = reinterpret_cast<float (*)[kK]>(&pr.qu[0][0]);   // [4][128]
+  float (*const ev)[kK] = reinterpret_cast<float (*)[kK]>(&pr.qu[0][0]);   // [8][128]
   ev[tid >> 6][(tid & 63) * 2] = e0;
   ev[tid >> 6][(tid & 63) * 2 + 1] = e1;
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
+  for (int n = 0; n < 4; ++n) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) keb[I * 8 + (lane >> 2)][col + n * 8 + e] = ke_sum[n][e];
 #pragma unroll
@@ -509,18 +497,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   }
   __syncthreads();
   {
-    float sum = 0.f;  // tokens 32 half .. + 31, from the end
-    for (int t = 31; t >= 0; --t) sum += dgam[half * 32 + t][ch];
-    if (half == 1) sm.tail[1][ch] = sum;
-    else {
-      float e = (ev[0][ch] + ev[1][ch]) + (ev[2][ch] + ev[3][ch]);
-      for (int w = 0; w < 32; ++w) e += keb[w][ch];
-      sm.tail[0][ch] = e;
-    }
+    float sum = 0.f;  // a sub-block's tokens, from the end
+#pragma unroll
+    for (int t = kB - 1; t >= 0; --t) sum += dgam[sub * kB + t][ch];
+    sm.tail[sub][ch] = sum;
+    float acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) acc += ev[w][ch];
+#pragma unroll 8
+    for (int w = 0; w < 32; ++w) acc += keb[w][ch];
     __syncthreads();
-    float acc = sm.tail[0][ch] + (half == 0 ? sm.tail[1][ch] : 0.f);
-    for (int t = 31; t >= 0; --t) {
-      const int tt = half * 32 + t;
+    for (int j = kNB - 1; j > sub; --j) acc += sm.tail[j][ch];
+#pragma unroll
+    for (int t = kB - 1; t >= 0; --t) {
+      const int tt = sub * kB + t;
       acc += dgam[tt][ch];
       if (tt < tc) p.dg[(pos.tok + tt) * p.dg_ts + h * kK + ch] = acc;
     }

@@ -16,54 +16,72 @@
 // serves the backward pass: one triangular solve for both, and beta = 0 needs
 // no division.  This kernel computes Wr = M Kt, Rt = M V, Ke, Qt, P (and Y).
 //
-// Decays.  Every factor is kept at most 1 (for g <= 0) by splitting the chunk
-// into sub-blocks of 16 tokens: for t in sub-block I and s in an earlier J,
-// exp(Gamma_t - Gamma_s) = up_t exp(mu_I + L_J+1 + .. + L_I-1 + L_J - md_J) dn_s
-// (see SubFactors), the middle factor per channel from fp64 sums; inside a
-// sub-block up_t dn_s alone.  These products run in tf32 pairs, whose range
-// takes the e^+-60 of a sub-block's factors; the triangular products that
-// follow in fp16 pairs.
+// Decays.  Every factor is kept at most 1 (for g <= 0) by a reference token
+// between t and s: pairs across the chunk's middle take their decays to it,
+// pairs of neighbouring sub-blocks (16 tokens) inside a half those to the
+// border between them, as fp16 pairs.  Inside a sub-block the reference is the
+// middle of its cumulative log-decays (see SubFactors), and the products run in
+// tf32 pairs, whose range takes the e^+-60 of those factors.
+//
+// What bounds it: the instructions of the factors and of the fp16 splits, not
+// the products.  512 threads, one sub-block and channel each (256 left the
+// schedulers short of warps); one CTA an SM, its shared memory.
 #pragma once
 
 #include "kda_scan_common.cuh"
 
 namespace kdal {
 
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 512, kPrepWarps = kPrepThreads / 32;
 constexpr int kFP = kK + 4;  // padded rows of the fp32 factors: MMA fragments then touch 32 banks
 constexpr int kAP = kC + 4;
+constexpr int kHalfPlane = Record::kPlane / 2;  // 32 rows of 128 columns
+
+struct PrepFactors {
+  float ku[kC][kFP];  // k up
+  float qu[kC][kFP];  // q up
+  float kd[kC][kFP];  // k dn
+};
+struct PrepTiles {    // over the factors once those are in registers; pairs (hi, lo)
+  unsigned char kt[2 * Record::kPlane];       // Kt; then Wr
+  unsigned char r32[2][2 * kHalfPlane];       // k, q of tokens 32.. with the decay from token 32's start
+  unsigned char c32[2 * kHalfPlane];          // k of tokens ..31 with the decay to there
+  unsigned char r16[2][2 * kHalfPlane];       // k, q of sub-blocks 1 and 3 with the decay from their starts
+  unsigned char c16[2 * kHalfPlane];          // k of sub-blocks 0 and 2 with the decay to their ends
+};
+enum PrepMax { kMxV, kMxKt, kMxQt, kMxKe, kMxR32K, kMxR32Q, kMxC32, kMxR16K, kMxR16Q, kMxC16, kMxP, kMxY, kMxWr, kMxBeta, kMxCount };
 
 struct PrepSmem {
-  float ku[kC][kFP];            // k up
-  float qu[kC][kFP];            // q up
-  float kd[kC][kFP];            // k dn
-  float a[kC][kAP];             // A; the first part holds the fp64 sums before
-  float pm[kC][kAP];            // P; then the tile M
-  float y[kC][kAP];             // Y
-  unsigned char kt[2 * Record::kPlane];  // Kt tile hi, lo; then Wr
-  unsigned char vt[Record::kPlane];      // V tile [t][v]
-  float up[kNB][kK];            // exp(Gamma at the sub-block's start + mu)
-  float dn[kNB][kK];            // exp(Gamma_C - (Gamma at its start + md))
-  float cross[6][kK];           // the middle factor of the six (I, J < I)
+  union {
+    PrepFactors f;
+    PrepTiles t;
+  };
+  unsigned char vt[Record::kPlane];     // V tile [t][v]
+  float a[kC][kAP];                     // A
+  float pm[kC][kAP];                    // P; then the tile M
+  float y[kC][kAP];                     // Y
+  Sum end[kNB][kK];                     // log-decay of a sub-block
+  float up[kNB][kK], dn[kNB][kK];       // to Kt and Qt, to Ke
+  float x32[kNB][kK], x16[kNB][kK];     // to the tiles r32 or c32, r16 or c16
   float beta[kC];
-  uint32_t mx[8];               // block maxima (float bits): v, kt, qt, ke, p, y, wr, beta
+  uint32_t mx[kMxCount];                // block maxima (float bits)
   int exact[kNB];
   ChunkPos pos;
 };
-static_assert(sizeof(double) * 3 * kNB * kK <= sizeof(float) * kC * kAP, "the fp64 sums fit into a");
 static_assert(2 * kC * kC * 2 <= sizeof(float) * kC * kAP, "the M tile fits into pm");
+static_assert(sizeof(PrepSmem) <= 232448, "shared memory of an SM");
 
 __device__ __forceinline__ void block_max(uint32_t* slot, float m, int lane) {
   m = warp_max(m);
   if (lane == 0) atomicMax(slot, __float_as_uint(m));
 }
 
-// Pairs inside sub-block `b` from the differences themselves: warp w takes two
-// rows, its lanes four channels each, s running down from t with the
+// Pairs inside sub-block `b` from the differences themselves: warp w takes row
+// w, its lanes four channels each, s running down from t with the
 // log-decay between s and t summed on the way.
 __device__ __noinline__ void prep_exact_block(const ScanParams& p, PrepSmem& sm, int b, int64_t tok, int tc, int64_t h) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < kB; r += kPrepThreads / 32) {
+  for (int r = warp; r < kB; r += kPrepWarps) {
     const int t = b * kB + r;
     if (t >= tc) continue;
     float kt[4], qt[4], d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -96,12 +114,96 @@ __device__ __noinline__ void prep_exact_block(const ScanParams& p, PrepSmem& sm,
   }
 }
 
+// A tile of an fp32 matrix as the A or B operand of the tf32 product, elements f(row, k) and f(k, column).
+template <typename F>
+__device__ __forceinline__ void tf32_a(F f, int lane, uint32_t (&h)[4], uint32_t (&l)[4]) {
+  const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) tf32_pair(f(r + (j & 1) * 8, c + (j >> 1) * 4), h[j], l[j]);
+}
+template <typename F>
+__device__ __forceinline__ void tf32_b(F f, int lane, uint32_t (&h)[2], uint32_t (&l)[2]) {
+  const int r = lane >> 2, c = lane & 3;
+  tf32_pair(f(c, r), h[0], l[0]);
+  tf32_pair(f(c + 4, r), h[1], l[1]);
+}
+
+// Y's block of ROWS rows from r0 under its diagonal blocks, columns c0 .. c0 + 7 of the ROWS columns from r0 - ROWS:
+//   Y21 = (I - Y2 diag(beta2)) A21 (I - diag(beta1) Y1).
+// One warp; it reads and writes these columns alone (and finished diagonal blocks).
+template <int ROWS>
+__device__ __forceinline__ void solve_below(PrepSmem& sm, int r0, int c0, int lane) {
+  constexpr int kM = ROWS / 16;
+  const int k0 = r0 - ROWS, r = lane >> 2, c = lane & 3, first = (c0 - k0) / 8;
+  float x[kM][4];
+#pragma unroll
+  for (int m = 0; m < kM; ++m) {
+    float lo[4] = {}, hi[4] = {};
+    for (int kk = first; kk < ROWS / 8; ++kk) {  // Y1[k][n] is zero for k <= n
+      uint32_t ah[4], al[4], bh[2], bl[2];
+      tf32_a([&](int i, int k) { return sm.a[r0 + m * 16 + i][k0 + kk * 8 + k]; }, lane, ah, al);
+      tf32_b([&](int k, int n) { return sm.beta[k0 + kk * 8 + k] * sm.y[k0 + kk * 8 + k][c0 + n]; }, lane, bh, bl);
+      mma_tf32(lo, ah, bl);
+      mma_tf32(lo, al, bh);
+      mma_tf32(hi, ah, bh);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = r0 + m * 16 + r + (e >> 1) * 8, col = c0 + 2 * c + (e & 1);
+      x[m][e] = sm.a[row][col] - (hi[e] + lo[e]);
+      sm.y[row][col] = x[m][e];
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < kM; ++m) {
+    float lo[4] = {}, hi[4] = {};
+#pragma unroll
+    for (int kk = 0; kk < 2 * (m + 1); ++kk) {  // Y2[t][k] is zero for k >= t
+      uint32_t ah[4], al[4], bh[2], bl[2];
+      tf32_a([&](int i, int k) { return sm.y[r0 + m * 16 + i][r0 + kk * 8 + k]; }, lane, ah, al);
+      tf32_b([&](int k, int n) { return sm.beta[r0 + kk * 8 + k] * sm.y[r0 + kk * 8 + k][c0 + n]; }, lane, bh, bl);
+      mma_tf32(lo, ah, bl);
+      mma_tf32(lo, al, bh);
+      mma_tf32(hi, ah, bh);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[m][e] -= hi[e] + lo[e];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int m = 0; m < kM; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sm.y[r0 + m * 16 + r + (e >> 1) * 8][c0 + 2 * c + (e & 1)] = x[m][e];
+  __syncwarp();
+}
+
+// 16 x 16 of a product over the 128 channels of two pair tiles [row][i].
+__device__ __forceinline__ void pair_product(uint32_t row_tile, int m0, uint32_t col_tile, int n0, int lane, float (&out)[2][4]) {
+  float hi[2][2][4] = {}, lo[2][4] = {};
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    uint32_t ah[4], al[4], bh[4], bl[4];
+    load_a<128>(row_tile, m0, kk * 16, lane, ah);
+    load_a<128>(row_tile + kHalfPlane, m0, kk * 16, lane, al);
+    load_b<128>(col_tile, kk * 16, n0, lane, bh);
+    load_b<128>(col_tile + kHalfPlane, kk * 16, n0, lane, bl);
+    mma_pair(lo[0], lo[1], ah, bl);
+    mma_pair(lo[0], lo[1], al, bh);
+    mma_pair(hi[kk & 1][0], hi[kk & 1][1], ah, bh);
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[n][e] = (hi[0][n][e] + hi[1][n][e]) + lo[n][e];
+}
+
 __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __grid_constant__ ScanParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
-  if (tid < 8) sm.mx[tid] = 0;
+  if (tid < kMxCount) sm.mx[tid] = 0;
   if (tid < kNB) sm.exact[tid] = 0;
   const ChunkPos pos = locate(p, slot, &sm.pos);
   const int tc = pos.tc;
@@ -109,14 +211,13 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   __syncthreads();
   unsigned char* const rec = record(p, slot, h);
   float* const hdr = reinterpret_cast<float*>(rec);
+  auto scale_of = [&](PrepMax i) { return pow2_scale(__uint_as_float(sm.mx[i])); };
 
-  // ---- 1. decay factors: thread = channel, two sub-blocks
-  const int ch = tid & (kK - 1), half = tid >> 7;
-  double* const dsum = reinterpret_cast<double*>(&sm.a[0][0]);  // [3][kNB][kK]: mu, md, end
-  float m_ku[2], m_qu[2], m_kd[2];
-#pragma unroll
-  for (int b2 = 0; b2 < 2; ++b2) {
-    const int b = half * 2 + b2;
+  // ---- 1. decay factors: thread = channel and sub-block
+  const int ch = tid & (kK - 1), b = tid >> 7;
+  SubFactors sf;
+  float m_ku = 0.f, m_qu = 0.f, m_kd = 0.f;
+  {
     float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
@@ -126,28 +227,25 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       kv[t] = in ? __bfloat162float(p.k[tk * p.k_ts + h * kK + ch]) : 0.f;
       qv[t] = in ? __bfloat162float(p.q[tk * p.q_ts + h * kK + ch]) : 0.f;
     }
-    const SubFactors f = sub_factors(g, up, dn);
-    m_ku[b2] = m_qu[b2] = m_kd[b2] = 0.f;
+    sf = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
-      const float a = kv[t] * up[t], c = qv[t] * up[t], d = kv[t] * dn[t];
-      sm.ku[b * kB + t][ch] = a;
-      sm.qu[b * kB + t][ch] = c;
-      sm.kd[b * kB + t][ch] = d;
-      m_ku[b2] = fmaxf(m_ku[b2], fabsf(a));
-      m_qu[b2] = fmaxf(m_qu[b2], fabsf(c));
-      m_kd[b2] = fmaxf(m_kd[b2], fabsf(d));
+      const float ku = kv[t] * up[t], qu = qv[t] * up[t], kd = kv[t] * dn[t];
+      sm.f.ku[b * kB + t][ch] = ku;
+      sm.f.qu[b * kB + t][ch] = qu;
+      sm.f.kd[b * kB + t][ch] = kd;
+      m_ku = fmaxf(m_ku, fabsf(ku));
+      m_qu = fmaxf(m_qu, fabsf(qu));
+      m_kd = fmaxf(m_kd, fabsf(kd));
     }
-    if (f.exact) sm.exact[b] = 1;
-    dsum[b * kK + ch] = f.mu;
-    dsum[(kNB + b) * kK + ch] = f.md;
-    dsum[(2 * kNB + b) * kK + ch] = f.end;
+    if (sf.exact) sm.exact[b] = 1;
+    sm.end[b][ch] = sf.end;
   }
   // v: 16-byte pieces, kept in registers until the scale is known
-  uint4 vraw[4];
+  uint4 vraw[2];
   float m_v = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     const int c = tid + j * kPrepThreads, t = c >> 4, pc = c & 15;
     vraw[j] = t < tc ? *reinterpret_cast<const uint4*>(p.v + (pos.tok + t) * p.v_ts + h * kV + pc * 8) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {vraw[j].x, vraw[j].y, vraw[j].z, vraw[j].w};
@@ -157,196 +255,221 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       m_v = fmaxf(m_v, fabsf(__uint_as_float(w[e] & 0xffff0000u)));
     }
   }
-  block_max(&sm.mx[0], m_v, lane);
+  block_max(&sm.mx[kMxV], m_v, lane);
   if (warp < 2) {
-    const float b = tid < tc ? __ldg(p.beta + (pos.tok + tid) * p.beta_ts + h) : 0.f;
-    sm.beta[tid] = b;
-    hdr[Record::kBeta + tid] = b;
-    block_max(&sm.mx[7], fabsf(b), lane);
+    const float be = tid < tc ? __ldg(p.beta + (pos.tok + tid) * p.beta_ts + h) : 0.f;
+    sm.beta[tid] = be;
+    hdr[Record::kBeta + tid] = be;
+    block_max(&sm.mx[kMxBeta], fabsf(be), lane);
   }
   __syncthreads();
 
   // ---- 2. channel constants
-#pragma unroll
-  for (int b2 = 0; b2 < 2; ++b2) {
-    const int b = half * 2 + b2;
-    double before = 0.0, after = 0.0;
-    for (int j = 0; j < b; ++j) before += dsum[(2 * kNB + j) * kK + ch];
-    for (int j = b + 1; j < kNB; ++j) after += dsum[(2 * kNB + j) * kK + ch];
-    const double mu = dsum[b * kK + ch], md = dsum[(kNB + b) * kK + ch], end = dsum[(2 * kNB + b) * kK + ch];
-    const float up = exp_of(before + mu), dn = exp_of(after + (end - md));
+  {
+    Sum before{0.f, 0.f}, after{0.f, 0.f};
+    for (int j = 0; j < b; ++j) before = add(before, sm.end[j][ch]);
+    for (int j = b + 1; j < kNB; ++j) after = add(after, sm.end[j][ch]);
+    const Sum rest = add(sf.end, neg(sf.md));
+    const float up = exp_of(add(before, sf.mu)), dn = exp_of(add(after, rest));
     sm.up[b][ch] = up;
     sm.dn[b][ch] = dn;
-    if (b == 0) hdr[Record::kDecay + ch] = exp_of(end + after);
-    m_ku[b2] *= up;
-    m_qu[b2] *= up;
-    m_kd[b2] *= dn;
-  }
-  for (int e = half; e < 6; e += 2) {  // (I, J): (1,0) (2,0) (2,1) (3,0) (3,1) (3,2)
-    const int I = e < 1 ? 1 : (e < 3 ? 2 : 3), J = e - I * (I - 1) / 2;
-    double s = dsum[I * kK + ch] + (dsum[(2 * kNB + J) * kK + ch] - dsum[(kNB + J) * kK + ch]);
-    for (int j = J + 1; j < I; ++j) s += dsum[(2 * kNB + j) * kK + ch];
-    sm.cross[e][ch] = exp_of(s);
-  }
-  block_max(&sm.mx[1], fmaxf(m_ku[0], m_ku[1]), lane);
-  block_max(&sm.mx[2], fmaxf(m_qu[0], m_qu[1]), lane);
-  block_max(&sm.mx[3], fmaxf(m_kd[0], m_kd[1]), lane);
-  __syncthreads();
-  for (int e = tid; e < kC * kAP; e += kPrepThreads) {
-    (&sm.a[0][0])[e] = 0.f;
-    (&sm.pm[0][0])[e] = 0.f;
-    (&sm.y[0][0])[e] = 0.f;
-  }
-  const float sc_v = pow2_scale(__uint_as_float(sm.mx[0])), sc_kt = pow2_scale(__uint_as_float(sm.mx[1]));
-  const float sc_qt = pow2_scale(__uint_as_float(sm.mx[2])), sc_ke = pow2_scale(__uint_as_float(sm.mx[3]));
-
-  // ---- 3. tiles of the decayed rows: Kt and V to shared memory, Qt and Ke to the record
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = tid + j * kPrepThreads, t = c >> 4, i0 = (c & 15) * 8, b = t / kB;
-    const uint32_t off = off128(t, i0);
-    uint32_t hi[4], lo[4], qh[4], ql[4], eh[4], el[4], vh[4];
-    const uint32_t w[4] = {vraw[j].x, vraw[j].y, vraw[j].z, vraw[j].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + 2 * e;
-      const float2 up = *reinterpret_cast<const float2*>(&sm.up[b][i]), dn = *reinterpret_cast<const float2*>(&sm.dn[b][i]);
-      const float2 ku = *reinterpret_cast<const float2*>(&sm.ku[t][i]), qu = *reinterpret_cast<const float2*>(&sm.qu[t][i]);
-      const float2 kd = *reinterpret_cast<const float2*>(&sm.kd[t][i]);
-      split2(ku.x * up.x * sc_kt, ku.y * up.y * sc_kt, hi[e], lo[e]);
-      split2(qu.x * up.x * sc_qt, qu.y * up.y * sc_qt, qh[e], ql[e]);
-      split2(kd.x * dn.x * sc_ke, kd.y * dn.y * sc_ke, eh[e], el[e]);
-      vh[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc_v, __uint_as_float(w[e] & 0xffff0000u) * sc_v));
+    if (b == 0) hdr[Record::kDecay + ch] = exp_of(add(sf.end, after));
+    const float x32 = exp_of(b == 0 ? add(rest, sm.end[1][ch]) : (b == 1 ? rest : (b == 2 ? sf.mu : add(sf.mu, sm.end[2][ch]))));
+    const float x16 = exp_of(b & 1 ? sf.mu : rest);
+    sm.x32[b][ch] = x32;
+    sm.x16[b][ch] = x16;
+    block_max(&sm.mx[kMxKt], m_ku * up, lane);
+    block_max(&sm.mx[kMxQt], m_qu * up, lane);
+    block_max(&sm.mx[kMxKe], m_kd * dn, lane);
+    if (b >= 2) {
+      block_max(&sm.mx[kMxR32K], m_ku * x32, lane);
+      block_max(&sm.mx[kMxR32Q], m_qu * x32, lane);
+    } else {
+      block_max(&sm.mx[kMxC32], m_kd * x32, lane);
     }
-    *reinterpret_cast<uint4*>(sm.kt + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(sm.kt + Record::kPlane + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(sm.vt + off) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
-    *reinterpret_cast<uint4*>(rec + Record::kQt + off) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
-    if (p.save) *reinterpret_cast<uint4*>(rec + Record::kQt + Record::kPlane + off) = make_uint4(ql[0], ql[1], ql[2], ql[3]);
-    *reinterpret_cast<uint4*>(rec + Record::kKe + off) = make_uint4(eh[0], eh[1], eh[2], eh[3]);
-    *reinterpret_cast<uint4*>(rec + Record::kKe + Record::kPlane + off) = make_uint4(el[0], el[1], el[2], el[3]);
+    if (b & 1) {
+      block_max(&sm.mx[kMxR16K], m_ku * x16, lane);
+      block_max(&sm.mx[kMxR16Q], m_qu * x16, lane);
+    } else {
+      block_max(&sm.mx[kMxC16], m_kd * x16, lane);
+    }
   }
-  __syncthreads();
-
-  // ---- 4. A and P: 40 units of 16 x 8 (ten sub-block pairs, A or P, two column tiles), five a warp
-  for (int u = warp; u < 40; u += kPrepThreads / 32) {
-    const int nt = u & 1, kind = (u >> 1) & 1, pr = u >> 2;  // pr: 0..5 below the diagonal, 6..9 on it
-    const int I = pr < 6 ? (pr < 1 ? 1 : (pr < 3 ? 2 : 3)) : pr - 6, J = pr < 6 ? pr - I * (I - 1) / 2 : I;
-    if (I == J && sm.exact[I]) continue;
-    const float (*const X)[kFP] = kind ? sm.qu : sm.ku;
+  // ---- 3. A and P inside a sub-block: warp = sub-block, A or P, eight columns
+  {
+    const int I = warp >> 2, kind = (warp >> 1) & 1, nt = warp & 1;
     const int r = lane >> 2, c = lane & 3;
-    const float* const x0 = &X[I * kB + r][c];
-    const float* const b0 = &sm.kd[J * kB + nt * 8 + r][c];
-    const float* const f = pr < 6 ? &sm.cross[pr][c] : nullptr;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int kk = 0; kk < kK; kk += 8) {
-      const float f0 = f ? f[kk] : 1.f, f1 = f ? f[kk + 4] : 1.f;
-      uint32_t ah[4], al[4], bh[2], bl[2];
-      tf32_split(x0[kk] * f0, ah[0], al[0]);
-      tf32_split(x0[8 * kFP + kk] * f0, ah[1], al[1]);
-      tf32_split(x0[kk + 4] * f1, ah[2], al[2]);
-      tf32_split(x0[8 * kFP + kk + 4] * f1, ah[3], al[3]);
-      tf32_split(b0[kk], bh[0], bl[0]);
-      tf32_split(b0[kk + 4], bh[1], bl[1]);
-      mma3_tf32(acc, ah, al, bh, bl);
+    float hi[2][4] = {}, lo[4] = {};
+    if (!sm.exact[I]) {
+      const float (*const X)[kFP] = kind ? sm.f.qu : sm.f.ku;
+      const float* const x0 = &X[I * kB + r][c];
+      const float* const b0 = &sm.f.kd[I * kB + nt * 8 + r][c];
+#pragma unroll
+      for (int kk = 0; kk < kK / 8; ++kk) {
+        uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tf32_pair(x0[(j & 1) * 8 * kFP + kk * 8 + (j >> 1) * 4], ah[j], al[j]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) tf32_pair(b0[kk * 8 + j * 4], bh[j], bl[j]);
+        mma_tf32(lo, ah, bl);
+        mma_tf32(lo, al, bh);
+        mma_tf32(hi[kk & 1], ah, bh);
+      }
     }
     float (*const dst)[kAP] = kind ? sm.pm : sm.a;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int t = I * kB + r + (e >> 1) * 8, s = J * kB + nt * 8 + 2 * c + (e & 1);
-      dst[t][s] = kind ? (s <= t ? acc[e] : 0.f) : (s < t ? acc[e] : 0.f);
+      const int t = I * kB + r + (e >> 1) * 8, s = I * kB + nt * 8 + 2 * c + (e & 1);
+      const float x = (hi[0][e] + hi[1][e]) + lo[e];
+      dst[t][s] = s < t + kind ? x : 0.f;
     }
   }
-  __syncthreads();
-  if (sm.exact[0] | sm.exact[1] | sm.exact[2] | sm.exact[3]) {
-    for (int b = 0; b < kNB; ++b)
-      if (sm.exact[b]) prep_exact_block(p, sm, b, pos.tok, tc, h);
-    __syncthreads();
-  }
-
-  // ---- 5. Y = A (I + diag(beta) A)^-1 by sub-blocks: the diagonal ones by substitution ...
-  if (tid < kC) {
-    const int b = tid / kB, j = tid % kB;
-    float yv[kB];
-#pragma unroll
-    for (int r = 0; r < kB; ++r) {
-      float x = sm.a[b * kB + r][tid];
-#pragma unroll
-      for (int s = 0; s < r; ++s) x = fmaf(-sm.a[b * kB + r][b * kB + s] * sm.beta[b * kB + s], yv[s], x);
-      yv[r] = r > j ? x : 0.f;
-      sm.y[b * kB + r][tid] = yv[r];
-    }
-  } else {
-    float m = 0.f;  // the other warps: P's maximum
-    for (int e = tid - kC; e < kC * kC; e += kPrepThreads - kC) m = fmaxf(m, fabsf(sm.pm[e >> 6][e & 63]));
-    block_max(&sm.mx[4], m, lane);
-  }
-  __syncthreads();
+  // ---- 4. tiles of the decayed rows, over the factors: Qt and Ke to the record, the others to shared memory
   {
-    const float sc_p = pow2_scale(__uint_as_float(sm.mx[4]));
-    if (tid == 0) hdr[Record::kScP] = sc_p;
+    float ku[2][8], qu[2][8], kd[2][8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = tid + j * kPrepThreads, t = c >> 3, s0 = (c & 7) * 8;
+      const int c = tid + j * kPrepThreads, t = c >> 4, i0 = (c & 15) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        *reinterpret_cast<float4*>(&ku[j][e]) = *reinterpret_cast<const float4*>(&sm.f.ku[t][i0 + e]);
+        *reinterpret_cast<float4*>(&qu[j][e]) = *reinterpret_cast<const float4*>(&sm.f.qu[t][i0 + e]);
+        *reinterpret_cast<float4*>(&kd[j][e]) = *reinterpret_cast<const float4*>(&sm.f.kd[t][i0 + e]);
+      }
+    }
+    __syncthreads();
+    // x[8] f[8] sc as a pair of 16-byte pieces
+    auto put = [&](unsigned char* hi, unsigned char* lo, uint32_t off, const float (&x)[8], const float (&f)[8], float sc) {
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2(x[2 * e] * f[2 * e] * sc, x[2 * e + 1] * f[2 * e + 1] * sc, h[e], l[e]);
+      *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+      if (lo != nullptr) *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    };
+    auto get = [&](const float* src, float (&f)[8]) {
+      *reinterpret_cast<float4*>(&f[0]) = *reinterpret_cast<const float4*>(src);
+      *reinterpret_cast<float4*>(&f[4]) = *reinterpret_cast<const float4*>(src + 4);
+    };
+    const float sc_v = scale_of(kMxV);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = tid + j * kPrepThreads, t = c >> 4, i0 = (c & 15) * 8, tb = t / kB;  // tb: 0, 1 and then 2, 3
+      const uint32_t off = off128(t, i0);
+      float f[8];
+      get(&sm.up[tb][i0], f);
+      put(sm.t.kt, sm.t.kt + Record::kPlane, off, ku[j], f, scale_of(kMxKt));
+      put(rec + Record::kQt, p.save ? rec + Record::kQt + Record::kPlane : nullptr, off, qu[j], f, scale_of(kMxQt));
+      get(&sm.dn[tb][i0], f);
+      put(rec + Record::kKe, rec + Record::kKe + Record::kPlane, off, kd[j], f, scale_of(kMxKe));
+      get(&sm.x32[tb][i0], f);
+      const uint32_t off32 = off128(t & 31, i0), off16 = off128((t >> 5) * kB + (t & 15), i0);
+      if (j == 1) {
+        put(sm.t.r32[0], sm.t.r32[0] + kHalfPlane, off32, ku[j], f, scale_of(kMxR32K));
+        put(sm.t.r32[1], sm.t.r32[1] + kHalfPlane, off32, qu[j], f, scale_of(kMxR32Q));
+      } else {
+        put(sm.t.c32, sm.t.c32 + kHalfPlane, off32, kd[j], f, scale_of(kMxC32));
+      }
+      get(&sm.x16[tb][i0], f);
+      if (tb & 1) {
+        put(sm.t.r16[0], sm.t.r16[0] + kHalfPlane, off16, ku[j], f, scale_of(kMxR16K));
+        put(sm.t.r16[1], sm.t.r16[1] + kHalfPlane, off16, qu[j], f, scale_of(kMxR16Q));
+      } else {
+        put(sm.t.c16, sm.t.c16 + kHalfPlane, off16, kd[j], f, scale_of(kMxC16));
+      }
+      const uint32_t w[4] = {vraw[j].x, vraw[j].y, vraw[j].z, vraw[j].w};
+      uint32_t vh[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        vh[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc_v, __uint_as_float(w[e] & 0xffff0000u) * sc_v));
+      *reinterpret_cast<uint4*>(sm.vt + off) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+    }
+  }
+  __syncthreads();
+
+  // ---- 5. A and P across sub-blocks: 16 x 16 a warp, eight across the middle, four inside the halves
+  if (warp < 12) {
+    const bool far = warp < 8;
+    const int kind = warp & 1, m0 = far ? ((warp >> 1) & 1) * 16 : ((warp >> 1) & 1) * 16, n0 = far ? (warp >> 2) * 16 : m0;
+    float x[2][4];
+    pair_product(smem_addr(far ? sm.t.r32[kind] : sm.t.r16[kind]), m0, smem_addr(far ? sm.t.c32 : sm.t.c16), n0, lane, x);
+    const float inv = far ? pow2_inv(scale_of(kind ? kMxR32Q : kMxR32K)) * pow2_inv(scale_of(kMxC32))
+                          : pow2_inv(scale_of(kind ? kMxR16Q : kMxR16K)) * pow2_inv(scale_of(kMxC16));
+    const int t0 = far ? 32 + m0 : 2 * m0 + 16, s0 = far ? n0 : 2 * m0;
+    float (*const dst)[kAP] = kind ? sm.pm : sm.a;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+        *reinterpret_cast<float2*>(&dst[t0 + (lane >> 2) + hf * 8][s0 + n * 8 + 2 * (lane & 3)]) =
+            make_float2(x[n][2 * hf] * inv, x[n][2 * hf + 1] * inv);
+  }
+  if (sm.exact[0] | sm.exact[1] | sm.exact[2] | sm.exact[3]) {
+    for (int j = 0; j < kNB; ++j)
+      if (sm.exact[j]) prep_exact_block(p, sm, j, pos.tok, tc, h);
+  }
+  __syncthreads();
+
+  // ---- 6. Y = A (I + diag(beta) A)^-1: four warps, the diagonal blocks by substitution, then pairs of blocks
+  if (warp < 4) {
+    if (lane < kB) {
+      const int r0 = warp * kB;
+      float x[kB];
+#pragma unroll
+      for (int r = 0; r < kB; ++r) x[r] = r > lane ? sm.a[r0 + r][r0 + lane] : 0.f;
+#pragma unroll
+      for (int s = 0; s < kB - 1; ++s) {
+        const float w = -sm.beta[r0 + s] * x[s];
+#pragma unroll
+        for (int r = s + 1; r < kB; ++r) x[r] = fmaf(sm.a[r0 + r][r0 + s], w, x[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < kB; ++r) sm.y[r0 + r][r0 + lane] = x[r];
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    solve_below<16>(sm, 16 + (warp >> 1) * 32, (warp >> 1) * 32 + (warp & 1) * 8, lane);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    solve_below<32>(sm, 32, warp * 8, lane);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    float m = 0.f;
+    for (int e = tid; e < kC * kC; e += 128)
+      if (((e >> 4) & 3) <= (e >> 10)) m = fmaxf(m, fabsf(sm.y[e >> 6][e & 63]));
+    block_max(&sm.mx[kMxY], m, lane);
+  } else {  // the other warps: P to the record
+    const int w = tid - 128;
+    float m = 0.f;
+    for (int e = w; e < kC * kC; e += kPrepThreads - 128)
+      if (((e >> 4) & 3) <= (e >> 10)) m = fmaxf(m, fabsf(sm.pm[e >> 6][e & 63]));
+    block_max(&sm.mx[kMxP], m, lane);
+    asm volatile("bar.sync 2, 384;" ::: "memory");
+    const float sc_p = scale_of(kMxP);
+    if (w == 0) hdr[Record::kScP] = sc_p;
+    for (int c = w; c < kC * kC / 8; c += kPrepThreads - 128) {
+      const int t = c >> 3, s0 = (c & 7) * 8;
+      const bool in = (s0 >> 4) <= (t >> 4);
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split2(sm.pm[t][s0 + 2 * e] * sc_p, sm.pm[t][s0 + 2 * e + 1] * sc_p, hi[e], lo[e]);
+      for (int e = 0; e < 4; ++e)
+        split2(in ? sm.pm[t][s0 + 2 * e] * sc_p : 0.f, in ? sm.pm[t][s0 + 2 * e + 1] * sc_p : 0.f, hi[e], lo[e]);
       *reinterpret_cast<uint4*>(rec + Record::kP + off64(t, s0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if (p.save)
         *reinterpret_cast<uint4*>(rec + Record::kP + kC * kC * 2 + off64(t, s0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
-  // ... the rows of sub-blocks below from Y_I = (I - Y_II beta) (A_I - A_I,<I beta Y_<I)
-  for (int I = 1; I < kNB; ++I) {
-    const int cols = I * kB;
-    float x[3];
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int e = tid + u * kPrepThreads, r = I * kB + (e & 15), j = e >> 4;
-      if (j < cols) {
-        float acc = sm.a[r][j];
-        for (int s = j & ~(kB - 1); s < cols; ++s) acc = fmaf(-sm.a[r][s] * sm.beta[s], sm.y[s][j], acc);
-        sm.y[r][j] = acc;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int e = tid + u * kPrepThreads, r = I * kB + (e & 15), j = e >> 4;
-      if (j < cols) {
-        x[u] = sm.y[r][j];
-        for (int s = I * kB; s < r; ++s) x[u] = fmaf(-sm.y[r][s] * sm.beta[s], sm.y[s][j], x[u]);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      const int e = tid + u * kPrepThreads, r = I * kB + (e & 15), j = e >> 4;
-      if (j < cols) sm.y[r][j] = x[u];
-    }
-    __syncthreads();
-  }
-  {
-    float m = 0.f;
-    for (int e = tid; e < kC * kC; e += kPrepThreads) m = fmaxf(m, fabsf(sm.y[e >> 6][e & 63]));
-    block_max(&sm.mx[5], m, lane);
-  }
   __syncthreads();
-  // ---- 6. the tile M = I - Y diag(beta) (over P), and diag(beta) Y to the record
-  const float y_beta = __uint_as_float(sm.mx[5]) * __uint_as_float(sm.mx[7]);
-  const float sc_m = pow2_scale(fmaxf(1.f, y_beta)), sc_y = pow2_scale(y_beta);
+  // ---- 7. the tile M = I - Y diag(beta) (over P), and diag(beta) Y to the record
+  const float y_beta = __uint_as_float(sm.mx[kMxY]) * __uint_as_float(sm.mx[kMxBeta]);
+  const float sc_m = pow2_scale(fmaxf(1.f, y_beta)), sc_y = pow2_scale(y_beta), sc_v = scale_of(kMxV), sc_kt = scale_of(kMxKt);
   unsigned char* const mt = reinterpret_cast<unsigned char*>(&sm.pm[0][0]);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int c = tid + j * kPrepThreads, t = c >> 3, s0 = (c & 7) * 8;
+  {
+    const int t = tid >> 3, s0 = (tid & 7) * 8;
+    const bool in = (s0 >> 4) <= (t >> 4);
+    const float bt = sm.beta[t];
     uint32_t hi[4], lo[4], yh[4], yl[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int s = s0 + 2 * e;
-      const float y0 = sm.y[t][s], y1 = sm.y[t][s + 1];
+      const float y0 = in ? sm.y[t][s] : 0.f, y1 = in ? sm.y[t][s + 1] : 0.f;
       split2(((t == s ? 1.f : 0.f) - y0 * sm.beta[s]) * sc_m, ((t == s + 1 ? 1.f : 0.f) - y1 * sm.beta[s + 1]) * sc_m, hi[e], lo[e]);
-      split2(y0 * sm.beta[t] * sc_y, y1 * sm.beta[t] * sc_y, yh[e], yl[e]);
+      split2(y0 * bt * sc_y, y1 * bt * sc_y, yh[e], yl[e]);
     }
     *reinterpret_cast<uint4*>(mt + off64(t, s0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(mt + kC * kC * 2 + off64(t, s0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -357,83 +480,81 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   }
   __syncthreads();
 
-  // ---- 7. Rt^T = V^T M^T: warp = 16 value columns
-  const uint32_t mt_a = smem_addr(mt), kt_a = smem_addr(sm.kt), vt_a = smem_addr(sm.vt);
-  {
-    float acc[8][4] = {};
+  // ---- 8. Rt^T = V^T M^T: warp = 16 value columns, token sub-blocks 0 and 3 or 1 and 2 (five products each)
+  const uint32_t mt_a = smem_addr(mt), kt_a = smem_addr(sm.t.kt), vt_a = smem_addr(sm.vt);
+  const int g16 = (warp & 7) * 16, first = warp >> 3;  // sub-blocks `first` and 3 - first
+  float* const rt = reinterpret_cast<float*>(rec + Record::kRt);
 #pragma unroll
-    for (int kk = 0; kk < kNB; ++kk) {  // s sub-block
-      uint32_t av[4];
-      load_a_t<128>(vt_a, warp * 16, kk * 16, lane, av);
-#pragma unroll
-      for (int nb = kk; nb < kNB; ++nb) {  // t sub-blocks from it on
-        uint32_t bh[4], bl[4];
-        load_b<64>(mt_a, kk * 16, nb * 16, lane, bh);
-        load_b<64>(mt_a + kC * kC * 2, kk * 16, nb * 16, lane, bl);
-        mma2(acc[2 * nb], acc[2 * nb + 1], av, bh, bl);
-      }
+  for (int u = 0; u < 2; ++u) {
+    const int nb = u ? 3 - first : first;
+    float hi[2][4] = {}, lo[2][4] = {};
+    for (int kk = 0; kk <= nb; ++kk) {  // s sub-blocks up to it
+      uint32_t av[4], bh[4], bl[4];
+      load_a_t<128>(vt_a, g16, kk * 16, lane, av);
+      load_b<64>(mt_a, kk * 16, nb * 16, lane, bh);
+      load_b<64>(mt_a + kC * kC * 2, kk * 16, nb * 16, lane, bl);
+      mma_pair(lo[0], lo[1], av, bl);
+      mma_pair(hi[0], hi[1], av, bh);
     }
     const float inv = pow2_inv(sc_m) * pow2_inv(sc_v);
-    float* const rt = reinterpret_cast<float*>(rec + Record::kRt);
-    const int v0 = warp * 16 + (lane >> 2), t0 = 2 * (lane & 3);
+    const int v0 = g16 + (lane >> 2), t0 = nb * 16 + 2 * (lane & 3);
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      *reinterpret_cast<float2*>(rt + v0 * kC + n * 8 + t0) = make_float2(acc[n][0] * inv, acc[n][1] * inv);
-      *reinterpret_cast<float2*>(rt + (v0 + 8) * kC + n * 8 + t0) = make_float2(acc[n][2] * inv, acc[n][3] * inv);
-    }
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+        *reinterpret_cast<float2*>(rt + (v0 + hf * 8) * kC + t0 + n * 8) =
+            make_float2((hi[n][2 * hf] + lo[n][2 * hf]) * inv, (hi[n][2 * hf + 1] + lo[n][2 * hf + 1]) * inv);
   }
-  // ---- 8. Wr = M Kt: warp = 16 key channels, all rows
-  float acc[4][2][4] = {};
+  // ---- 9. Wr = M Kt: warp = 16 key channels, the same token sub-blocks
+  float acc[2][2][4];
+  float m_wr = 0.f;
 #pragma unroll
-  for (int kk = 0; kk < kNB; ++kk) {
-    uint32_t bh[4], bl[4];
-    load_b_t<128>(kt_a, kk * 16, warp * 16, lane, bh);
-    load_b_t<128>(kt_a + Record::kPlane, kk * 16, warp * 16, lane, bl);
-#pragma unroll
-    for (int mb = kk; mb < kNB; ++mb) {
-      uint32_t ah[4], al[4];
+  for (int u = 0; u < 2; ++u) {
+    const int mb = u ? 3 - first : first;
+    float hi[2][4] = {}, lo[2][4] = {};
+    for (int kk = 0; kk <= mb; ++kk) {
+      uint32_t ah[4], al[4], bh[4], bl[4];
+      load_b_t<128>(kt_a, kk * 16, g16, lane, bh);
+      load_b_t<128>(kt_a + Record::kPlane, kk * 16, g16, lane, bl);
       load_a<64>(mt_a, mb * 16, kk * 16, lane, ah);
       load_a<64>(mt_a + kC * kC * 2, mb * 16, kk * 16, lane, al);
-      mma3(acc[mb][0], acc[mb][1], ah, al, bh, bl);
+      mma_pair(lo[0], lo[1], ah, bl);
+      mma_pair(lo[0], lo[1], al, bh);
+      mma_pair(hi[0], hi[1], ah, bh);
     }
-  }
-  {
     const float inv = pow2_inv(sc_m) * pow2_inv(sc_kt);
-    float m = 0.f;
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[mb][n][e] *= inv;
-          m = fmaxf(m, fabsf(acc[mb][n][e]));
-        }
-    block_max(&sm.mx[6], m, lane);
+      for (int e = 0; e < 4; ++e) {
+        acc[u][n][e] = (hi[n][e] + lo[n][e]) * inv;
+        m_wr = fmaxf(m_wr, fabsf(acc[u][n][e]));
+      }
   }
+  block_max(&sm.mx[kMxWr], m_wr, lane);
   __syncthreads();  // every warp is done with Kt
-  const float sc_wr = pow2_scale(__uint_as_float(sm.mx[6]));
+  const float sc_wr = scale_of(kMxWr);
 #pragma unroll
-  for (int mb = 0; mb < 4; ++mb)
+  for (int u = 0; u < 2; ++u)
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t hi, lo;
-        split2(acc[mb][n][2 * hf] * sc_wr, acc[mb][n][2 * hf + 1] * sc_wr, hi, lo);
-        const uint32_t off = off128(mb * 16 + hf * 8 + (lane >> 2), warp * 16 + n * 8 + 2 * (lane & 3));
-        *reinterpret_cast<uint32_t*>(sm.kt + off) = hi;
-        *reinterpret_cast<uint32_t*>(sm.kt + Record::kPlane + off) = lo;
+        split2(acc[u][n][2 * hf] * sc_wr, acc[u][n][2 * hf + 1] * sc_wr, hi, lo);
+        const uint32_t off = off128((u ? 3 - first : first) * 16 + hf * 8 + (lane >> 2), g16 + n * 8 + 2 * (lane & 3));
+        *reinterpret_cast<uint32_t*>(sm.t.kt + off) = hi;
+        *reinterpret_cast<uint32_t*>(sm.t.kt + Record::kPlane + off) = lo;
       }
   if (tid == 0) {
     hdr[Record::kScWr] = sc_wr;
-    hdr[Record::kScKe] = sc_ke;
-    hdr[Record::kScQt] = sc_qt;
+    hdr[Record::kScKe] = scale_of(kMxKe);
+    hdr[Record::kScQt] = scale_of(kMxQt);
     hdr[Record::kScY] = sc_y;
   }
   __syncthreads();
   for (int c = tid; c < 2 * Record::kPlane / 16; c += kPrepThreads)
-    *reinterpret_cast<uint4*>(rec + Record::kWr + 16 * c) = *reinterpret_cast<const uint4*>(sm.kt + 16 * c);
+    *reinterpret_cast<uint4*>(rec + Record::kWr + 16 * c) = *reinterpret_cast<const uint4*>(sm.t.kt + 16 * c);
 }
 
 }  // namespace kdal

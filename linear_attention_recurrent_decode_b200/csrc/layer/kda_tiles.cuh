@@ -117,23 +117,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c0, c1 += (ah + al) (bh + bl) for two 8-column tiles, without al.bl.
-__device__ __forceinline__ void mma3(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                     const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
-  mma_f16(c0, ah, bl[0], bl[1]);
-  mma_f16(c1, ah, bl[2], bl[3]);
-  mma_f16(c0, al, bh[0], bh[1]);
-  mma_f16(c1, al, bh[2], bh[3]);
-  mma_f16(c0, ah, bh[0], bh[1]);
-  mma_f16(c1, ah, bh[2], bh[3]);
-}
-// c0, c1 += a (bh + bl), a exact in fp16.
-__device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[4], const uint32_t (&bh)[4],
-                                     const uint32_t (&bl)[4]) {
-  mma_f16(c0, a, bl[0], bl[1]);
-  mma_f16(c1, a, bl[2], bl[3]);
-  mma_f16(c0, a, bh[0], bh[1]);
-  mma_f16(c1, a, bh[2], bh[3]);
+// The MMA adds to its accumulator with truncation, half an ulp of the running
+// sum low on average, so a long chain of them is biased by more than fp32
+// rounding.  The cross terms (2^-11 of the product) therefore go ahead of the
+// hi.hi terms or into accumulators of their own, and partial sums over a few
+// k steps are joined by ordinary additions.
+__device__ __forceinline__ void mma_pair(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+  mma_f16(c0, a, b[0], b[1]);
+  mma_f16(c1, a, b[2], b[3]);
 }
 // The A fragment pair of 16 accumulator columns (two 8-column tiles) times s.
 __device__ __forceinline__ void frag_a(const float (&c0)[4], const float (&c1)[4], float s, uint32_t (&ah)[4],
@@ -157,22 +148,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // ---------------------------------------------------------------- tf32 pairs
 // For operands whose range is too wide for one fp16 scale (decay factors of up
 // to e^+-80 inside a sub-block): x = hi + lo in tf32, three MMAs of k = 8.
-__device__ __forceinline__ void tf32_split(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
-}
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-__device__ __forceinline__ void mma3_tf32(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                          const uint32_t (&bh)[2], const uint32_t (&bl)[2]) {
-  mma_tf32(c, ah, bl);
-  mma_tf32(c, al, bh);
-  mma_tf32(c, ah, bh);
-}
-
 // ---------------------------------------------------------------- bulk copies
 __device__ __forceinline__ void mbar_init(uint64_t* mbar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(mbar)), "r"(count) : "memory");
