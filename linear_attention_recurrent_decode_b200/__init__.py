@@ -31,8 +31,8 @@ __all__ = ["kda_decode", "kda_decode_gated_rmsnorm", "kda_decode_ex", "HostStep"
            "KDA_ERR_MISALIGNED", "KDA_ERR_DEVICE", "KDA_ERR_CUDA", "KDA_ERR_SCRATCH_LIMIT", "KDA_STATE_FP32",
            "KDA_STATE_BF16",
            "KDA_LAYOUT_KV", "KDA_LAYOUT_VK", "LIBRARY_PATH", "EXPORTED_SYMBOLS",
-           "kda_scan", "kda_scan_backward", "scan_workspace_bytes", "scan_error", "layer_library", "LAYER_LIBRARY_PATH",
-           "LAYER_SYMBOLS"]
+           "kda_scan", "kda_scan_backward", "scan_workspace_bytes", "scan_error", "kda_qk_norm_rope",
+           "kda_qk_norm_rope_backward", "rope_frequencies", "layer_library", "LAYER_LIBRARY_PATH", "LAYER_SYMBOLS"]
 
 LIBRARY_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda_decode.so")
 
@@ -581,5 +581,5 @@ def kda_prefill(q, k, v, g, beta, state_pool, slot_idx, out=None, scale: float |
 
 
 # ---------------------------------------------------------------- the operators around the decode step
-from .layer import (LAYER_LIBRARY_PATH, LAYER_SYMBOLS, kda_scan, kda_scan_backward, layer_library,  # noqa: E402
-                    scan_error, scan_workspace_bytes)
+from .layer import (LAYER_LIBRARY_PATH, LAYER_SYMBOLS, kda_qk_norm_rope, kda_qk_norm_rope_backward,  # noqa: E402
+                    kda_scan, kda_scan_backward, layer_library, rope_frequencies, scan_error, scan_workspace_bytes)

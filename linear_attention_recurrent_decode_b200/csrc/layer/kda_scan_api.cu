@@ -43,18 +43,6 @@ cudaError_t prepare_kernels() {
   return e;
 }
 
-int sm_count() {
-  static std::atomic<int> cache[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  int v = dev < kMaxDevices ? cache[dev].load(std::memory_order_relaxed) : 0;
-  if (v == 0) {
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
-    if (dev < kMaxDevices) cache[dev].store(v, std::memory_order_relaxed);
-  }
-  return v;
-}
-
 // Chunk slots of the whole call (see Record); false on overflow.
 bool chunk_slots(int64_t N, int64_t T, bool packed, int64_t* slots) {
   if (packed) return !__builtin_add_overflow(T / ks::kC, N, slots);

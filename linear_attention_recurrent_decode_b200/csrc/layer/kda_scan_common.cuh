@@ -192,6 +192,28 @@ __device__ __forceinline__ SubFactors sub_factors(const float (&g)[kB], float (&
   return f;
 }
 
+// The log-decays, keys and queries of sub-block b's 16 tokens in channel `col` (a head's column), zeros behind the
+// chunk.  Every load is issued ahead of any use and without a branch (rows behind the chunk read its last one): as
+// conditional loads they ran one after the other, 17000 cycles against 4000.
+__device__ __forceinline__ void load_sub_block(const ScanParams& p, int64_t tok, int tc, int b, int64_t col, float (&g)[kB],
+                                               float (&k)[kB], float (&q)[kB]) {
+  __nv_bfloat16 kr[kB], qr[kB];
+#pragma unroll
+  for (int t = 0; t < kB; ++t) {
+    const int64_t tk = tok + (b * kB + t < tc ? b * kB + t : tc - 1);
+    g[t] = __ldg(p.g + tk * p.g_ts + col);
+    kr[t] = p.k[tk * p.k_ts + col];
+    qr[t] = p.q[tk * p.q_ts + col];
+  }
+#pragma unroll
+  for (int t = 0; t < kB; ++t) {
+    const bool in = b * kB + t < tc;
+    g[t] = in ? log_decay(g[t]) : 0.f;
+    k[t] = in ? __bfloat162float(kr[t]) : 0.f;
+    q[t] = in ? __bfloat162float(qr[t]) : 0.f;
+  }
+}
+
 // Round-to-nearest split of an fp32 value into a tf32 pair (the MMA reads the
 // upper 19 bits of each).
 __device__ __forceinline__ void tf32_pair(float x, uint32_t& hi, uint32_t& lo) {

@@ -369,14 +369,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   const int ch = tid & (kK - 1), sub = tid >> 7;
   {
     float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
-#pragma unroll
-    for (int t = 0; t < kB; ++t) {
-      const int64_t tk = pos.tok + sub * kB + t;
-      const bool in = sub * kB + t < tc;
-      g[t] = in ? log_decay(__ldg(p.g + tk * p.g_ts + h * kK + ch)) : 0.f;
-      kv[t] = in ? __bfloat162float(p.k[tk * p.k_ts + h * kK + ch]) : 0.f;
-      qv[t] = in ? __bfloat162float(p.q[tk * p.q_ts + h * kK + ch]) : 0.f;
-    }
+    load_sub_block(p, pos.tok, tc, sub, h * kK + ch, g, kv, qv);
     const SubFactors f = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
@@ -466,6 +459,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         dkc[n][e] += d.z;
       }
     }
+  __nv_bfloat162 qk[4][2][2];  // q and k again, at this thread's elements (rows behind the chunk: the last one's)
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int64_t tk = pos.tok + (row + hf * 8 < tc ? row + hf * 8 : tc - 1);
+      qk[n][hf][0] = *reinterpret_cast<const __nv_bfloat162*>(p.q + tk * p.q_ts + h * kK + col + n * 8);
+      qk[n][hf][1] = *reinterpret_cast<const __nv_bfloat162*>(p.k + tk * p.k_ts + h * kK + col + n * 8);
+    }
   __syncthreads();  // the factors are dead: the decays' gradients go over them
   // ---- 8. dq, dk; dg by a sum from the chunk's end
   float (*const dgam)[kGP] = pr.up;
@@ -480,19 +482,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int t = row + hf * 8, i = col + n * 8;
-      float g0 = 0.f, g1 = 0.f;
+      const int64_t tk = pos.tok + t;
+      const float2 q = __bfloat1622float2(qk[n][hf][0]), k = __bfloat1622float2(qk[n][hf][1]);
+      const float q0 = dq[n][2 * hf], q1 = dq[n][2 * hf + 1], r0 = dkr[n][2 * hf], r1 = dkr[n][2 * hf + 1];
+      const float c0 = dkc[n][2 * hf], c1 = dkc[n][2 * hf + 1];
       if (t < tc) {
-        const int64_t tk = pos.tok + t;
-        const float2 q = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.q + tk * p.q_ts + h * kK + i));
-        const float2 k = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.k + tk * p.k_ts + h * kK + i));
-        const float q0 = dq[n][2 * hf], q1 = dq[n][2 * hf + 1], r0 = dkr[n][2 * hf], r1 = dkr[n][2 * hf + 1];
-        const float c0 = dkc[n][2 * hf], c1 = dkc[n][2 * hf + 1];
         *reinterpret_cast<__nv_bfloat162*>(p.dq + tk * p.dq_ts + h * kK + i) = __floats2bfloat162_rn(q0, q1);
         *reinterpret_cast<__nv_bfloat162*>(p.dk + tk * p.dk_ts + h * kK + i) = __floats2bfloat162_rn(r0 + c0, r1 + c1);
-        g0 = fmaf(q.x, q0, k.x * (r0 - c0));
-        g1 = fmaf(q.y, q1, k.y * (r1 - c1));
       }
-      *reinterpret_cast<float2*>(&dgam[t][i]) = make_float2(g0, g1);
+      // rows behind the chunk: their gradients are zero
+      *reinterpret_cast<float2*>(&dgam[t][i]) = make_float2(fmaf(q.x, q0, k.x * (r0 - c0)), fmaf(q.y, q1, k.y * (r1 - c1)));
     }
   }
   __syncthreads();

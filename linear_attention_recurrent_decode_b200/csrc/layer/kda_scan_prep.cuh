@@ -213,20 +213,20 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   float* const hdr = reinterpret_cast<float*>(rec);
   auto scale_of = [&](PrepMax i) { return pow2_scale(__uint_as_float(sm.mx[i])); };
 
+  // v: 16-byte pieces, kept in registers until the scale is known
+  uint4 vraw[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = (tid + j * kPrepThreads) >> 4;
+    vraw[j] = *reinterpret_cast<const uint4*>(p.v + (pos.tok + (t < tc ? t : tc - 1)) * p.v_ts + h * kV + (tid & 15) * 8);
+  }
   // ---- 1. decay factors: thread = channel and sub-block
   const int ch = tid & (kK - 1), b = tid >> 7;
   SubFactors sf;
   float m_ku = 0.f, m_qu = 0.f, m_kd = 0.f;
   {
     float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
-#pragma unroll
-    for (int t = 0; t < kB; ++t) {
-      const int64_t tk = pos.tok + b * kB + t;
-      const bool in = b * kB + t < tc;
-      g[t] = in ? log_decay(__ldg(p.g + tk * p.g_ts + h * kK + ch)) : 0.f;
-      kv[t] = in ? __bfloat162float(p.k[tk * p.k_ts + h * kK + ch]) : 0.f;
-      qv[t] = in ? __bfloat162float(p.q[tk * p.q_ts + h * kK + ch]) : 0.f;
-    }
+    load_sub_block(p, pos.tok, tc, b, h * kK + ch, g, kv, qv);
     sf = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
@@ -241,13 +241,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     if (sf.exact) sm.exact[b] = 1;
     sm.end[b][ch] = sf.end;
   }
-  // v: 16-byte pieces, kept in registers until the scale is known
-  uint4 vraw[2];
   float m_v = 0.f;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int c = tid + j * kPrepThreads, t = c >> 4, pc = c & 15;
-    vraw[j] = t < tc ? *reinterpret_cast<const uint4*>(p.v + (pos.tok + t) * p.v_ts + h * kV + pc * 8) : make_uint4(0, 0, 0, 0);
+    if (((tid + j * kPrepThreads) >> 4) >= tc) vraw[j] = make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {vraw[j].x, vraw[j].y, vraw[j].z, vraw[j].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

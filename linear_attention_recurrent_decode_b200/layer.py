@@ -1,8 +1,11 @@
 """Binding of ``libkda_layer.so``: the operators of a KDA layer around the decode step.
 
 ``kda_scan`` / ``kda_scan_backward`` (``include/layer/kda_scan.h``) run the
-recurrence over long packed sequences and its gradients.  Like the rest of the
-package the functions only marshal torch tensors; there is no fallback.
+recurrence over long packed sequences and its gradients;
+``kda_qk_norm_rope`` / ``kda_qk_norm_rope_backward`` (``include/layer/kda_qk.h``)
+the per-head norm of its queries and keys with the position rotation.  Like the
+rest of the package the functions only marshal torch tensors; there is no
+fallback.
 """
 from __future__ import annotations
 
@@ -13,8 +16,8 @@ import threading
 
 import torch
 
-__all__ = ["kda_scan", "kda_scan_backward", "scan_workspace_bytes", "scan_error", "layer_library", "LAYER_LIBRARY_PATH",
-           "LAYER_SYMBOLS"]
+__all__ = ["kda_scan", "kda_scan_backward", "scan_workspace_bytes", "scan_error", "kda_qk_norm_rope", "kda_qk_norm_rope_backward",
+           "rope_frequencies", "layer_library", "LAYER_LIBRARY_PATH", "LAYER_SYMBOLS"]
 
 LAYER_LIBRARY_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda_layer.so")
 
@@ -38,11 +41,29 @@ class ScanGrads(ctypes.Structure):
                 ("d_initial_state", _P), ("saved", _I32)]
 
 
+class QkTensor(ctypes.Structure):
+    """ctypes mirror of ``kda_qk_tensor``."""
+    _fields_ = [("x", _P), ("x_row_stride", _I), ("y", _P), ("y_row_stride", _I), ("dy", _P), ("dy_row_stride", _I),
+                ("dx", _P), ("dx_row_stride", _I), ("weight", _P), ("dweight", _P), ("heads", _I)]
+
+
+class QkArgs(ctypes.Structure):
+    """ctypes mirror of ``kda_qk_args``."""
+    _fields_ = [("q", QkTensor), ("k", QkTensor), ("rows", _I), ("D", _I), ("rot", _I), ("positions", _P), ("inv_freq", _P),
+                ("positions_64", _I32), ("norm", _I32), ("interleaved", _I32), ("eps", _F), ("rope_scale", _F),
+                ("workspace", _P), ("workspace_bytes", _I)]
+
+
+QK_NORMS = {"none": 0, "l2": 1, "rms": 2}
+
 # Every symbol the headers under include/layer/ declare, with its ctypes signature.
 LAYER_SYMBOLS = {
     "kda_scan_workspace_bytes": ([_I, _I, _I32, _I, _I, _I, _I32], ctypes.c_int64),
     "kda_scan": ([ctypes.POINTER(ScanArgs), _P], ctypes.c_int),
     "kda_scan_backward": ([ctypes.POINTER(ScanArgs), ctypes.POINTER(ScanGrads), _P], ctypes.c_int),
+    "kda_qk_workspace_bytes": ([_I], ctypes.c_int64),
+    "kda_qk_norm_rope": ([ctypes.POINTER(QkArgs), _P], ctypes.c_int),
+    "kda_qk_norm_rope_backward": ([ctypes.POINTER(QkArgs), _P], ctypes.c_int),
 }
 
 _lock = threading.Lock()
@@ -254,3 +275,156 @@ def scan_error(workspace) -> int:
     """The error word of a workspace that the caller zeroed before the calls it watches: 1 if a kernel gave up a
     bounded wait.  Waits for the device's work in flight."""
     return int(workspace[:4].view(torch.int32).item())
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, trained_context: int | None = None,
+                     fast_turns: float = 32.0, slow_turns: float = 1.0, device=None):
+    """``(inv_freq, rope_scale)`` of a rotation of ``rot`` components: ``base ** (-2 i / rot)`` in float64.
+
+    ``factor`` > 1 stretches the positions for contexts that much longer than the model was trained on: without
+    ``trained_context`` every frequency is divided by it; with it only those that make fewer than ``slow_turns`` turns in
+    ``trained_context`` tokens, those that make more than ``fast_turns`` stay, a linear ramp over the pair index lies
+    between, and ``rope_scale`` is ``0.1 ln(factor) + 1`` (the ramped scaling published as YaRN)."""
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot must be even and >= 0, got {rot}")
+    if factor < 1.0 or base <= 1.0:
+        raise ValueError("factor must be >= 1 and base > 1")
+    freq = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    scale = 1.0
+    if factor > 1.0 and trained_context is None:
+        freq = freq / factor
+    elif factor > 1.0:
+        def pair_of(turns):  # the (fractional) pair that makes this many turns in the trained context
+            return rot * math.log(trained_context / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(pair_of(fast_turns)), 0), min(math.ceil(pair_of(slow_turns)), rot - 1)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - ramp) + freq / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    return (freq if device is None else freq.to(device)), scale
+
+
+def _qk_row_stride(t, name, lead, H, D, dev):
+    if t.dtype != torch.bfloat16 or t.get_device() != dev:
+        _on_device({name: t})
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() == 3 and t.shape == (*lead, H, D) and t.stride(2) == 1 and t.stride(1) == D:  # the usual case, cheaply
+        return t.stride(0) if lead[0] > 1 else H * D
+    return _row_stride(t, name, torch.bfloat16, lead, (H, D))
+
+
+def _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale):
+    """The arguments both calls share, the leading shape, and the current device."""
+    if not isinstance(q, torch.Tensor) or q.dim() < 3:
+        raise TypeError("q must be a torch.Tensor [..., heads, D]")
+    if norm not in QK_NORMS:
+        raise ValueError(f"norm must be one of {', '.join(QK_NORMS)}, got {norm!r}")
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if not q.is_cuda or q.get_device() != dev:
+        _on_device(dict(q=q))
+    lead, D = q.shape[:-2], q.shape[-1]
+    a = QkArgs()
+    a.rows = rows = math.prod(lead)
+    a.D, a.norm, a.eps, a.rope_scale, a.interleaved = D, QK_NORMS[norm], eps, rope_scale, bool(interleaved)
+    for name, x, w, t in (("q", q, q_weight, a.q), ("k", k, k_weight, a.k)):
+        if x is None:
+            if w is not None:
+                raise ValueError(f"{name}_weight without {name}")
+            continue
+        if not isinstance(x, torch.Tensor) or x.dim() != q.dim() or x.shape[:-2] != lead or x.shape[-1] != D:
+            raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, {D}]")
+        t.heads = x.shape[-2]
+        t.x, t.x_row_stride = x.data_ptr(), _qk_row_stride(x, name, lead, t.heads, D, dev)
+        if w is not None:
+            if not isinstance(w, torch.Tensor) or w.dtype != torch.bfloat16 or w.shape != (D,) or not w.is_contiguous():
+                raise TypeError(f"{name}_weight must be a contiguous bfloat16 [{D}] tensor")
+            if w.get_device() != dev:
+                _on_device({name + "_weight": w})
+            if norm == "none":
+                raise ValueError(f"{name}_weight needs a norm")
+            t.weight = w.data_ptr()
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise TypeError("inv_freq must be a contiguous float64 [rot / 2] tensor")
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+        if positions.dtype not in (torch.int32, torch.int64) or positions.shape != lead or not positions.is_contiguous():
+            raise TypeError(f"positions must be a contiguous int32 or int64 tensor of shape {tuple(lead)}")
+        if inv_freq.get_device() != dev or positions.get_device() != dev:
+            _on_device(dict(inv_freq=inv_freq, positions=positions))
+        a.rot = 2 * inv_freq.numel()
+        a.inv_freq, a.positions, a.positions_64 = inv_freq.data_ptr(), positions.data_ptr(), positions.dtype == torch.int64
+    elif positions is not None:
+        raise ValueError("positions need inv_freq")
+    return a, lead, D, dev
+
+
+def kda_qk_norm_rope(q, k=None, *, norm: str = "l2", eps: float = 1e-6, q_weight=None, k_weight=None, positions=None,
+                     inv_freq=None, interleaved: bool = False, rope_scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Per-head norm of queries and keys and the position rotation in one pass; returns ``(q, k)`` as the decode step,
+    the prefill and the scan take them (``k`` None if not given).
+
+    q ``[..., heads, D]``, k ``[..., k_heads, D]`` (bf16; rows may be strided views of one packed buffer).  ``norm``:
+    ``"l2"`` x / sqrt(sum x^2 + eps), ``"rms"`` x / sqrt(mean x^2 + eps), ``"none"``; ``q_weight`` / ``k_weight`` (bf16
+    ``[D]``) multiply after it.  ``inv_freq`` (float64 ``[rot / 2]``, :func:`rope_frequencies`) turns the first ``rot``
+    components of each head by ``positions`` (int32 or int64, the leading shape) in halves or ``interleaved`` pairs, times
+    ``rope_scale``.  Outputs are allocated if not given; ``q_out=q`` / ``k_out=k`` work in place."""
+    a, lead, D, dev = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale)
+    got = []
+    for name, x, y, t in (("q_out", q, q_out, a.q), ("k_out", k, k_out, a.k)):
+        if x is None:
+            if y is not None:
+                raise ValueError("k_out without k")
+        elif y is None:
+            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+            t.y, t.y_row_stride = y.data_ptr(), t.heads * D
+        else:
+            _on_device({name: y})
+            t.y, t.y_row_stride = y.data_ptr(), _row_stride(y, name, torch.bfloat16, lead, (t.heads, D))
+        got.append(y)
+    st = layer_library().kda_qk_norm_rope(ctypes.byref(a), _stream(stream))
+    if st:
+        _raise(st, "kda_qk_norm_rope")
+    return tuple(got)
+
+
+def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k=None, *, norm: str = "l2", eps: float = 1e-6, q_weight=None,
+                              k_weight=None, positions=None, inv_freq=None, interleaved: bool = False,
+                              rope_scale: float = 1.0, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of :func:`kda_qk_norm_rope` from those of its outputs: returns ``(dq, dk, d_q_weight, d_k_weight)``, the
+    last two fp32 ``[D]`` (None without the weight).  q, k and the options are the forward call's; ``dq`` / ``dk`` are
+    allocated if not given (``dq=d_q_out`` / ``dk=d_k_out`` work in place), and so is ``workspace`` (device uint8, 4096 D
+    bytes), used only with weights."""
+    a, lead, D, dev = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale)
+    got, dws = [], []
+    for name, x, dy, dx, w, t in (("q", q, d_q_out, dq, q_weight, a.q), ("k", k, d_k_out, dk, k_weight, a.k)):
+        dw = None
+        if x is None:
+            if dy is not None or dx is not None:
+                raise ValueError("gradients of k without k")
+        else:
+            if not isinstance(dy, torch.Tensor):
+                raise TypeError(f"d_{name}_out must be a torch.Tensor")
+            t.dy, t.dy_row_stride = dy.data_ptr(), _qk_row_stride(dy, f"d_{name}_out", lead, t.heads, D, dev)
+            if dx is None:
+                dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+                t.dx, t.dx_row_stride = dx.data_ptr(), t.heads * D
+            else:
+                _on_device({"d" + name: dx})
+                t.dx, t.dx_row_stride = dx.data_ptr(), _row_stride(dx, "d" + name, torch.bfloat16, lead, (t.heads, D))
+            if w is not None:
+                dw = torch.empty(D, dtype=torch.float32, device=x.device)
+                t.dweight = dw.data_ptr()
+        got.append(dx)
+        dws.append(dw)
+    if q_weight is not None or k_weight is not None:
+        if workspace is None:
+            workspace = torch.empty(max(layer_library().kda_qk_workspace_bytes(D), 16), dtype=torch.uint8, device=q.device)
+        else:
+            _on_device(dict(workspace=workspace))
+            if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+                raise TypeError("workspace must be a contiguous uint8 tensor")
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    st = layer_library().kda_qk_norm_rope_backward(ctypes.byref(a), _stream(stream))
+    if st:
+        _raise(st, "kda_qk_norm_rope_backward")
+    return (*got, *dws)
