@@ -28,7 +28,7 @@
  * strides); any other overlap is refused.
  *
  * Supported sizes: D a multiple of 8 from 8 to 256, rot a multiple of 16 from 0
- * to D, rows and heads >= 0.  Alignment: x, y, dy, dx, weight, workspace 16
+ * to D, rows >= 0, heads from 0 to 4096.  Alignment: x, y, dy, dx, weight, workspace 16
  * bytes and strides multiples of 8 elements; inv_freq, int64 positions 8, the
  * rest 4.
  *

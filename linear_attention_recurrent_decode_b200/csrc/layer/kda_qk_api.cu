@@ -33,8 +33,8 @@ kda_status common(const kda_qk_args& a, bool backward, ks::QkParams* p) {
   bool any = false, dw = false;
   for (int i = 0; i < 2; ++i) {
     int64_t items, width, elems;
-    if (t[i]->heads > 0x7fffffffLL / 4096 || !mul_ok(a.rows, t[i]->heads, &items) || !mul_ok(t[i]->heads, a.D, &width) ||
-        !mul_ok(items, a.D, &elems) || elems > INT64_MAX / 8)
+    if (t[i]->heads > ks::kMaxHeads || !mul_ok(a.rows, t[i]->heads, &items) || !mul_ok(t[i]->heads, a.D, &width) ||
+        !mul_ok(items, a.D, &elems) || elems >= (int64_t{1} << 51))
       return KDA_ERR_UNSUPPORTED;
     const int64_t rows = t[i]->heads > 0 ? a.rows : 0;
     any = any || (rows > 0);
@@ -56,6 +56,10 @@ kda_status common(const kda_qk_args& a, bool backward, ks::QkParams* p) {
     o.dw = backward ? t[i]->dweight : nullptr;
     o.items = items;
     o.heads = static_cast<int32_t>(t[i]->heads);
+    if (o.heads > 1) {  // ceil(2^n / heads)
+      o.div64 = ~uint64_t{0} / static_cast<uint64_t>(o.heads) + 1;
+      o.div32 = ~uint32_t{0} / static_cast<uint32_t>(o.heads) + 1;
+    }
   }
   if (a.rot > 0 && any) {
     if (a.positions == nullptr || a.inv_freq == nullptr) return KDA_ERR_INVALID_ARG;
@@ -117,7 +121,9 @@ int64_t split(ks::QkParams* p, int vpt) {
   }
   return span * (p->rot / 2) * static_cast<int64_t>(sizeof(float2));
 }
-// Heads a thread takes: four once that still leaves two tiles an SM, else one.
+// Heads a thread takes: the measured best for large calls (see the kernels) once that still leaves two tiles an SM,
+// else one, which spreads few heads over more SMs.
+constexpr int kForwardVpt = 4, kBackwardVpt = 2;
 int pick_vpt(ks::QkParams* p, int most) {
   split(p, most);
   return p->t[0].tiles + p->t[1].tiles >= 2 * sm_count() ? most : 1;
@@ -133,25 +139,33 @@ bool launch(F kernel, dim3 grid, int threads, int64_t smem, kda_stream_t stream,
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
 }
 
-template <int VPT>
-bool launch_forward(ks::QkRotate rot, unsigned grid, int64_t smem, kda_stream_t stream, const ks::QkParams& p) {
-  switch (rot) {
-    case ks::kQkNone: return launch(ks::kda_qk_forward_kernel<ks::kQkNone, VPT>, dim3(grid), ks::kQkThreads, smem, stream, p);
-    case ks::kQkHalves: return launch(ks::kda_qk_forward_kernel<ks::kQkHalves, VPT>, dim3(grid), ks::kQkThreads, smem, stream, p);
-    default: return launch(ks::kda_qk_forward_kernel<ks::kQkInterleaved, VPT>, dim3(grid), ks::kQkThreads, smem, stream, p);
+template <ks::QkRotate ROT, int LANES>
+bool launch_lanes(bool backward, int vpt, unsigned grid, int64_t smem, kda_stream_t stream, const ks::QkParams& p) {
+  if (backward) {
+    const int64_t red = p.t[0].dw || p.t[1].dw ? static_cast<int64_t>(ks::kQkThreads >> LANES) * p.D * 4 : 0;  // dw's sums
+    smem = smem > red ? smem : red;
+    return vpt == 1 ? launch(ks::kda_qk_backward_kernel<ROT, LANES, 1>, dim3(grid), ks::kQkThreads, smem, stream, p)
+                    : launch(ks::kda_qk_backward_kernel<ROT, LANES, kBackwardVpt>, dim3(grid), ks::kQkThreads, smem, stream, p);
+  }
+  return vpt == 1 ? launch(ks::kda_qk_forward_kernel<ROT, LANES, 1>, dim3(grid), ks::kQkThreads, smem, stream, p)
+                  : launch(ks::kda_qk_forward_kernel<ROT, LANES, kForwardVpt>, dim3(grid), ks::kQkThreads, smem, stream, p);
+}
+template <ks::QkRotate ROT>
+bool launch_rotate(bool backward, int vpt, unsigned grid, int64_t smem, kda_stream_t stream, const ks::QkParams& p) {
+  switch (p.lanes) {
+    case 0: return launch_lanes<ROT, 0>(backward, vpt, grid, smem, stream, p);
+    case 1: return launch_lanes<ROT, 1>(backward, vpt, grid, smem, stream, p);
+    case 2: return launch_lanes<ROT, 2>(backward, vpt, grid, smem, stream, p);
+    case 3: return launch_lanes<ROT, 3>(backward, vpt, grid, smem, stream, p);
+    case 4: return launch_lanes<ROT, 4>(backward, vpt, grid, smem, stream, p);
+    default: return launch_lanes<ROT, 5>(backward, vpt, grid, smem, stream, p);
   }
 }
-template <int VPT>
-bool launch_backward(ks::QkRotate rot, unsigned grid, int64_t smem, kda_stream_t stream, const ks::QkParams& p) {
-  switch (rot) {
-    case ks::kQkNone: return launch(ks::kda_qk_backward_kernel<ks::kQkNone, VPT>, dim3(grid), ks::kQkThreads, smem, stream, p);
-    case ks::kQkHalves: return launch(ks::kda_qk_backward_kernel<ks::kQkHalves, VPT>, dim3(grid), ks::kQkThreads, smem, stream, p);
-    default: return launch(ks::kda_qk_backward_kernel<ks::kQkInterleaved, VPT>, dim3(grid), ks::kQkThreads, smem, stream, p);
-  }
-}
-
-ks::QkRotate rotate_of(const kda_qk_args& a) {
-  return a.rot == 0 ? ks::kQkNone : (a.interleaved ? ks::kQkInterleaved : ks::kQkHalves);
+bool launch_qk(const kda_qk_args& a, bool backward, int vpt, int64_t grid, int64_t smem, kda_stream_t stream, const ks::QkParams& p) {
+  const unsigned n = static_cast<unsigned>(grid);
+  if (a.rot == 0) return launch_rotate<ks::kQkNone>(backward, vpt, n, smem, stream, p);
+  return a.interleaved ? launch_rotate<ks::kQkInterleaved>(backward, vpt, n, smem, stream, p)
+                       : launch_rotate<ks::kQkHalves>(backward, vpt, n, smem, stream, p);
 }
 
 }  // namespace
@@ -169,13 +183,10 @@ kda_status kda_qk_norm_rope(const kda_qk_args* args, kda_stream_t stream) {
   KDA_TRY(common(*args, false, &p));
   if (p.t[0].items + p.t[1].items == 0) return KDA_OK;
   KDA_TRY(check_device());
-  const int vpt = pick_vpt(&p, 4);
+  const int vpt = pick_vpt(&p, kForwardVpt);
   const int64_t smem = split(&p, vpt), grid = p.t[0].tiles + p.t[1].tiles;
   if (grid > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  const ks::QkRotate rot = rotate_of(*args);
-  const bool ok = vpt == 1 ? launch_forward<1>(rot, static_cast<unsigned>(grid), smem, stream, p)
-                           : launch_forward<4>(rot, static_cast<unsigned>(grid), smem, stream, p);
-  return ok ? KDA_OK : KDA_ERR_CUDA;
+  return launch_qk(*args, false, vpt, grid, smem, stream, p) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_qk_norm_rope_backward(const kda_qk_args* args, kda_stream_t stream) {
@@ -185,20 +196,16 @@ kda_status kda_qk_norm_rope_backward(const kda_qk_args* args, kda_stream_t strea
   const bool dw = p.t[0].dw != nullptr || p.t[1].dw != nullptr;
   if (p.t[0].items + p.t[1].items == 0 && !dw) return KDA_OK;
   KDA_TRY(check_device());
-  const int vpt = pick_vpt(&p, 2);
-  int64_t smem = split(&p, vpt);
-  // the blocks, six an SM at most (their registers), by the tensors' shares of the tiles
-  const int64_t most = 6 * sm_count() < ks::kQkMaxCtas - 2 ? 6 * sm_count() : ks::kQkMaxCtas - 2;
+  const int vpt = pick_vpt(&p, kBackwardVpt);
+  const int64_t smem = split(&p, vpt);
+  // as many blocks as run at once, by the tensors' shares of the tiles
+  const int64_t fit = ks::kQkBackwardCtas * sm_count(), most = fit < ks::kQkMaxCtas - 2 ? fit : ks::kQkMaxCtas - 2;
   const int64_t tiles = p.t[0].tiles + p.t[1].tiles;
   for (auto& t : p.t)
     t.ctas = static_cast<int32_t>(tiles <= most ? t.tiles
                                                 : (t.tiles == 0 ? 0 : 1 + static_cast<int64_t>(static_cast<double>(t.tiles) / tiles * (most - 2))));
-  const int64_t red = dw ? static_cast<int64_t>(ks::kQkThreads >> p.lanes) * p.D * static_cast<int64_t>(sizeof(float)) : 0;
-  if (red > smem) smem = red;
-  const unsigned grid = static_cast<unsigned>(p.t[0].ctas + p.t[1].ctas);
-  const ks::QkRotate rot = rotate_of(*args);
-  if (grid > 0 && !(vpt == 1 ? launch_backward<1>(rot, grid, smem, stream, p) : launch_backward<2>(rot, grid, smem, stream, p)))
-    return KDA_ERR_CUDA;
+  const int64_t grid = p.t[0].ctas + p.t[1].ctas;
+  if (grid > 0 && !launch_qk(*args, true, vpt, grid, smem, stream, p)) return KDA_ERR_CUDA;
   if (dw && !launch(ks::kda_qk_weight_kernel, dim3(static_cast<unsigned>((p.D + 31) / 32), 2), 1024, 0, stream, p)) return KDA_ERR_CUDA;
   return KDA_OK;
 }

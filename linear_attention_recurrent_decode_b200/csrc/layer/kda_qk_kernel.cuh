@@ -11,9 +11,15 @@
 // power of two of neighbouring lanes (unused ones idle for D = 96), sums and
 // the halves' partners go by shuffles.  A tile is 256 threads' heads, VPT each,
 // of one tensor; its rows' cos and sin are computed once, in shared memory, and
-// shared by all heads, while the loads are in flight.  VPT = 4 keeps four loads
-// in flight a thread; with few heads (fewer tiles than twice the SMs) VPT = 1
-// spreads them over more of the SMs.
+// shared by all heads, while the loads are in flight.
+//
+// Measured (B200, 16384 rows, D = 128): forward, 32 + 32 heads, 101 us, 5.3 TB/s
+// (0.81 of the measured copy rate), the instructions being the next bound (0.7
+// of the issue slots); four heads a thread and five blocks an SM against 115 us
+// for two heads.  Backward with weights, 32 + 8 heads, 144 us, 3.5 TB/s: two
+// heads a thread and three blocks an SM against 147 to 165 us for one, three or
+// four; loading the next tile ahead of computing one was slower (170 us, the
+// registers).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,6 +31,7 @@ namespace kdal {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkMaxCtas = 1024;  // of the backward pass: rows of its partial sums
+constexpr int kQkBackwardCtas = 3;  // an SM
 
 struct QkTensor {
   const __nv_bfloat16* x; int64_t x_ts;
@@ -34,8 +41,13 @@ struct QkTensor {
   float* dw;
   int64_t items;                           // rows * heads
   int64_t tiles;
+  uint64_t div64;                          // ceil(2^64 / heads) and ceil(2^32 / heads), 0 for one head: an item's row by
+  uint32_t div32;                          // a multiplication (exact: see kMaxHeads); a division cost 50 instructions a head
   int32_t heads, ctas;                     // ctas: blocks that share the tiles
 };
+// The quotient by multiplication is exact while n heads < 2^32 (or 2^64): n is below heads + 1024 in 32 bits, below 2^51
+// in 64.
+constexpr int kMaxHeads = 4096;
 struct QkParams {
   QkTensor t[2];
   const void* pos;
@@ -65,15 +77,19 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Sum over the 2^lanes neighbouring lanes of a head.
-__device__ __forceinline__ float head_sum(float x, int lanes) {
-  for (int o = 1; o < (1 << lanes); o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+// Sum over the 2^LANES neighbouring lanes of a head.
+template <int LANES>
+__device__ __forceinline__ float head_sum(float x) {
+#pragma unroll
+  for (int o = 1; o < (1 << LANES); o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// cos and sin of rows row0 .. row0 + span - 1, [span][rot / 2].  The angle is
+// cos and sin of rows row0 .. row0 + span - 1, [span][rot / 2], a row's pairs in the order [pair of pairs of a thread]
+// [thread][2], so that neighbouring lanes read neighbouring 16 bytes (in pair order they met in two of the banks).  The angle is
 // position * inv_freq in fp64, taken in half turns and reduced to one turn
 // there; cos and sin then see an argument exact to fp32.
+template <QkRotate ROT>
 __device__ __forceinline__ void qk_table(const QkParams& p, int64_t row0, int span, float2* tab) {
   const int half = p.rot >> 1;
   for (int e = threadIdx.x; e < span * half; e += kQkThreads) {
@@ -86,74 +102,91 @@ __device__ __forceinline__ void qk_table(const QkParams& p, int64_t row0, int sp
     u -= 2.0 * rint(0.5 * u);
     float s, c;
     sincospif(static_cast<float>(u), &s, &c);
-    tab[e] = make_float2(c * p.scale, s * p.scale);
+    constexpr int kLog = ROT == kQkHalves ? 3 : 2;  // pairs of a thread
+    const int at = ((((i & ((1 << kLog) - 1)) >> 1) * (half >> kLog) + (i >> kLog)) << 1) + (i & 1);
+    tab[r * half + at] = make_float2(c * p.scale, s * p.scale);
   }
 }
 
-// This thread's 8 components turned by the row's angles (cs: its row of the table); sign -1 turns back.
-template <QkRotate ROT>
-__device__ __forceinline__ void qk_rotate(const QkParams& p, const float2* cs, int l, float sign, float (&f)[8]) {
+// This thread's 8 components turned by the row's angles (cs: its row of the table), backwards if BACK.
+template <QkRotate ROT, bool BACK>
+__device__ __forceinline__ void qk_rotate(const QkParams& p, const float2* cs, int l, float (&f)[8]) {
   if constexpr (ROT == kQkInterleaved) {
     if (l * 8 >= p.rot) return;
+    const float4* const t4 = reinterpret_cast<const float4*>(cs) + l;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 t = cs[l * 4 + e];
-      const float s = sign * t.y, a = f[2 * e], b = f[2 * e + 1];
-      f[2 * e] = a * t.x - b * s;
-      f[2 * e + 1] = a * s + b * t.x;
+    for (int e = 0; e < 2; ++e) {
+      const float4 t = t4[e * (p.rot >> 3)];
+      const float a = f[4 * e], b = f[4 * e + 1], c = f[4 * e + 2], d = f[4 * e + 3];
+      const float s0 = BACK ? -t.y : t.y, s1 = BACK ? -t.w : t.w;
+      f[4 * e] = a * t.x - b * s0;
+      f[4 * e + 1] = a * s0 + b * t.x;
+      f[4 * e + 2] = c * t.z - d * s1;
+      f[4 * e + 3] = c * s1 + d * t.z;
     }
   } else if constexpr (ROT == kQkHalves) {
     const int hv = p.rot >> 4;  // threads of a half
     const bool first = l < hv, in = l < 2 * hv;
     const int lane = threadIdx.x & 31, from = in ? (first ? lane + hv : lane - hv) : lane;
-    float other[8];
+    const float sg = first == BACK ? 1.f : -1.f;
+    const float4* const t4 = reinterpret_cast<const float4*>(cs) + (first ? l : l - hv);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) other[e] = __shfl_sync(0xffffffffu, f[e], from);
-    if (!in) return;
-    const float sg = first ? -sign : sign;
-    const float2* const t = cs + (first ? l : l - hv) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = f[e] * t[e].x + sg * t[e].y * other[e];
+    for (int e = 0; e < 4; ++e) {
+      const float o0 = __shfl_sync(0xffffffffu, f[2 * e], from), o1 = __shfl_sync(0xffffffffu, f[2 * e + 1], from);
+      if (in) {
+        const float4 t = t4[e * hv];
+        f[2 * e] = fmaf(sg * t.y, o0, f[2 * e] * t.x);
+        f[2 * e + 1] = fmaf(sg * t.w, o1, f[2 * e + 1] * t.z);
+      }
+    }
   }
 }
 
-// The items of a tile that this thread takes part in.
-struct QkItem {
-  int64_t row;
-  int32_t r, head;  // row within the tile, head
-  bool in;
+// A thread's heads of a tile: the tile starts `rem` heads into row row0.
+template <int LANES, int VPT>
+struct QkTile {
+  static constexpr int kGroups = kQkThreads >> LANES;
+  int64_t row0;
+  int32_t rem, r[VPT], head[VPT];  // row within the tile, head
+  bool in[VPT];
+  __device__ __forceinline__ QkTile(const QkTensor& t, int64_t tile, int grp, bool used) {
+    const int64_t item0 = tile * (kGroups * VPT);
+    row0 = t.div64 ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(item0), t.div64)) : item0;
+    rem = static_cast<int32_t>(item0 - row0 * t.heads);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = grp + j * kGroups;
+      in[j] = used && item0 + i < t.items;
+      const uint32_t at = in[j] ? static_cast<uint32_t>(rem + i) : 0u;  // the table has no rows behind the last one
+      r[j] = static_cast<int32_t>(t.div32 ? __umulhi(at, t.div32) : at);
+      head[j] = static_cast<int32_t>(at) - r[j] * t.heads;
+    }
+  }
+  __device__ __forceinline__ int span(const QkTensor& t) const {
+    const uint32_t last = static_cast<uint32_t>(rem + kGroups * VPT - 1);
+    return static_cast<int>(t.div32 ? __umulhi(last, t.div32) : last) + 1;
+  }
 };
-__device__ __forceinline__ QkItem qk_item(const QkTensor& t, int64_t item0, int64_t row0, int rem, int i, bool used) {
-  QkItem it;
-  it.r = (rem + i) / t.heads;
-  it.head = rem + i - it.r * t.heads;
-  it.row = row0 + it.r;
-  it.in = used && item0 + i < t.items;
-  if (!it.in) it.r = 0;  // the table has no rows behind the last one
-  return it;
-}
 
-template <QkRotate ROT, int VPT>
-__global__ void __launch_bounds__(kQkThreads) kda_qk_forward_kernel(const __grid_constant__ QkParams p) {
+template <QkRotate ROT, int LANES, int VPT>
+__global__ void __launch_bounds__(kQkThreads, 5) kda_qk_forward_kernel(const __grid_constant__ QkParams p) {
   extern __shared__ __align__(16) float2 tab[];
   const int which = blockIdx.x >= p.t[0].tiles;
   const QkTensor& t = p.t[which];
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) - (which ? p.t[0].tiles : 0);
-  const int grp = threadIdx.x >> p.lanes, l = threadIdx.x & ((1 << p.lanes) - 1), groups = kQkThreads >> p.lanes;
-  const int64_t item0 = tile * (groups * VPT), row0 = item0 / t.heads;
-  const int rem = static_cast<int>(item0 - row0 * t.heads);
+  const int grp = threadIdx.x >> LANES, l = threadIdx.x & ((1 << LANES) - 1);
   const bool used = l * 8 < p.D;
+  const QkTile<LANES, VPT> it(t, static_cast<int64_t>(blockIdx.x) - (which ? p.t[0].tiles : 0), grp, used);
+  const __nv_bfloat16* const xb = t.x + it.row0 * t.x_ts + l * 8;
+  __nv_bfloat16* const yb = t.y + it.row0 * t.y_ts + l * 8;
   uint4 x[VPT];
-  QkItem it[VPT];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    it[j] = qk_item(t, item0, row0, rem, grp + j * groups, used);
-    x[j] = it[j].in ? *reinterpret_cast<const uint4*>(t.x + it[j].row * t.x_ts + it[j].head * p.D + l * 8) : make_uint4(0, 0, 0, 0);
-  }
+  for (int j = 0; j < VPT; ++j)
+    x[j] = it.in[j] ? *reinterpret_cast<const uint4*>(xb + it.r[j] * t.x_ts + it.head[j] * p.D) : make_uint4(0, 0, 0, 0);
   float w[8];
-  if (t.w != nullptr && used) unpack8(__ldg(reinterpret_cast<const uint4*>(t.w) + l), w);
+  const bool weighted = t.w != nullptr;
+  if (weighted && used) unpack8(__ldg(reinterpret_cast<const uint4*>(t.w) + l), w);
   if constexpr (ROT != kQkNone) {
-    qk_table(p, row0, (rem + groups * VPT - 1) / t.heads + 1, tab);
+    qk_table<ROT>(p, it.row0, it.span(t), tab);
     __syncthreads();
   }
 #pragma unroll
@@ -164,75 +197,76 @@ __global__ void __launch_bounds__(kQkThreads) kda_qk_forward_kernel(const __grid
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-      const float inv = rsqrtf(fmaf(head_sum(ss, p.lanes), p.inv_d, p.eps));
+      const float inv = rsqrtf(fmaf(head_sum<LANES>(ss), p.inv_d, p.eps));
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= inv;
-      if (t.w != nullptr) {
+      if (weighted) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= w[e];
       }
     }
-    qk_rotate<ROT>(p, tab + it[j].r * (p.rot >> 1), l, 1.f, f);
-    if (it[j].in) *reinterpret_cast<uint4*>(t.y + it[j].row * t.y_ts + it[j].head * p.D + l * 8) = pack8(f);
+    qk_rotate<ROT, false>(p, tab + it.r[j] * (p.rot >> 1), l, f);
+    if (it.in[j]) *reinterpret_cast<uint4*>(yb + it.r[j] * t.y_ts + it.head[j] * p.D) = pack8(f);
   }
 }
 
 // Blocks [0, t[0].ctas) walk q's tiles, the rest k's, so that a thread sums dw's contributions of its 8 components in
 // registers; a block then leaves one row of partial sums.
-template <QkRotate ROT, int VPT>
-__global__ void __launch_bounds__(kQkThreads) kda_qk_backward_kernel(const __grid_constant__ QkParams p) {
+template <QkRotate ROT, int LANES, int VPT>
+__global__ void __launch_bounds__(kQkThreads, kQkBackwardCtas) kda_qk_backward_kernel(const __grid_constant__ QkParams p) {
   extern __shared__ __align__(16) float2 tab[];
+  constexpr int kGroups = kQkThreads >> LANES;
   const int which = blockIdx.x >= p.t[0].ctas;
   const QkTensor& t = p.t[which];
-  const int grp = threadIdx.x >> p.lanes, l = threadIdx.x & ((1 << p.lanes) - 1), groups = kQkThreads >> p.lanes;
-  const bool used = l * 8 < p.D;
+  const int grp = threadIdx.x >> LANES, l = threadIdx.x & ((1 << LANES) - 1);
+  const bool used = l * 8 < p.D, weighted = t.w != nullptr;
   float w[8], dw[8] = {};
-  if (t.w != nullptr && used) unpack8(__ldg(reinterpret_cast<const uint4*>(t.w) + l), w);
+  if (weighted && used) unpack8(__ldg(reinterpret_cast<const uint4*>(t.w) + l), w);
   for (int64_t tile = static_cast<int64_t>(blockIdx.x) - (which ? p.t[0].ctas : 0); tile < t.tiles; tile += t.ctas) {
-    const int64_t item0 = tile * (groups * VPT), row0 = item0 / t.heads;
-    const int rem = static_cast<int>(item0 - row0 * t.heads);
+    const QkTile<LANES, VPT> it(t, tile, grp, used);
+    const __nv_bfloat16* const xb = t.x + it.row0 * t.x_ts + l * 8;
+    const __nv_bfloat16* const db = t.dy + it.row0 * t.dy_ts + l * 8;
+    __nv_bfloat16* const yb = t.y + it.row0 * t.y_ts + l * 8;
     uint4 x[VPT], dy[VPT];
-    QkItem it[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      it[j] = qk_item(t, item0, row0, rem, grp + j * groups, used);
       x[j] = dy[j] = make_uint4(0, 0, 0, 0);
-      if (it[j].in) {
-        if (p.norm) x[j] = *reinterpret_cast<const uint4*>(t.x + it[j].row * t.x_ts + it[j].head * p.D + l * 8);
-        dy[j] = *reinterpret_cast<const uint4*>(t.dy + it[j].row * t.dy_ts + it[j].head * p.D + l * 8);
+      if (it.in[j]) {
+        if (p.norm) x[j] = *reinterpret_cast<const uint4*>(xb + it.r[j] * t.x_ts + it.head[j] * p.D);
+        dy[j] = *reinterpret_cast<const uint4*>(db + it.r[j] * t.dy_ts + it.head[j] * p.D);
       }
     }
     if constexpr (ROT != kQkNone) {
-      qk_table(p, row0, (rem + groups * VPT - 1) / t.heads + 1, tab);
+      qk_table<ROT>(p, it.row0, it.span(t), tab);
       __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       float f[8], g[8];
       unpack8(dy[j], g);
-      qk_rotate<ROT>(p, tab + it[j].r * (p.rot >> 1), l, -1.f, g);
+      qk_rotate<ROT, true>(p, tab + it.r[j] * (p.rot >> 1), l, g);
       if (p.norm) {
         unpack8(x[j], f);
         float ss = 0.f, sg = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-        const float inv = rsqrtf(fmaf(head_sum(ss, p.lanes), p.inv_d, p.eps));
+        const float inv = rsqrtf(fmaf(head_sum<LANES>(ss), p.inv_d, p.eps));
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= inv;  // x^
-        if (t.w != nullptr) {
+        if (weighted) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (it[j].in) dw[e] = fmaf(g[e], f[e], dw[e]);
+            if (it.in[j]) dw[e] = fmaf(g[e], f[e], dw[e]);
             g[e] *= w[e];
           }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sg = fmaf(g[e], f[e], sg);
-        sg = head_sum(used ? sg : 0.f, p.lanes) * p.inv_d;
+        sg = head_sum<LANES>(used ? sg : 0.f) * p.inv_d;
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = inv * fmaf(-f[e], sg, g[e]);
       }
-      if (it[j].in) *reinterpret_cast<uint4*>(t.y + it[j].row * t.y_ts + it[j].head * p.D + l * 8) = pack8(g);
+      if (it.in[j]) *reinterpret_cast<uint4*>(yb + it.r[j] * t.y_ts + it.head[j] * p.D) = pack8(g);
     }
     if constexpr (ROT != kQkNone) __syncthreads();  // the table is rewritten
   }
@@ -245,7 +279,7 @@ __global__ void __launch_bounds__(kQkThreads) kda_qk_backward_kernel(const __gri
   __syncthreads();
   for (int d = threadIdx.x; d < p.D; d += kQkThreads) {
     float s = 0.f;
-    for (int i = 0; i < groups; ++i) s += red[i * p.D + d];
+    for (int i = 0; i < kGroups; ++i) s += red[i * p.D + d];
     p.partial[static_cast<int64_t>(blockIdx.x) * p.D + d] = s;
   }
 }

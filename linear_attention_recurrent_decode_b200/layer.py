@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -95,53 +96,77 @@ def _raise(status, where):
     raise KdaError(status, where)
 
 
-def _stream(stream):
-    from . import _stream_handle
-    return _stream_handle(stream)
+# The per-call path below is kept to a few microseconds: one comparison per tensor, the reason only on failure.
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
-def _on_device(tensors):
-    """The current device index; every given tensor must be on it."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
+def _device() -> int:
+    """The current device's index (-1 without CUDA: every tensor is then refused)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+
+
+def _on_stream(call):
+    """Runs a call given a ``stream`` with that stream current, so that what it allocates belongs to the stream too."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        from . import _stream_handle
+        handle = _stream_handle(stream).value or 0  # refuses another device's stream
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()):
+            return call(*args, **kwargs)
+    return run
+
+
+def _on_device(t, name, dev):
+    """Refuses a tensor that is not on the current device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev or not t.is_cuda:
         if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return dev
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
 
 
-def _row_stride(t, name, dtype, lead, inner):
-    """Row stride of a [*lead, *inner] tensor whose rows are evenly strided and dense inside."""
+def _row_stride(t, name, dtype, shape, lead, dev):
+    """Row stride of a tensor of this shape whose rows (over the first ``lead`` dimensions) are evenly strided and
+    dense inside."""
+    _on_device(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (*lead, *inner):
-        raise ValueError(f"{name} must have shape {(*lead, *inner)}, got {tuple(t.shape)}")
-    want = 1
-    for d in range(t.dim() - 1, len(lead) - 1, -1):
-        if t.shape[d] > 1 and t.stride(d) != want:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return math.prod(shape[lead:])
+    want, strides = 1, t.stride()
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] > 1 and strides[d] != want:
             raise ValueError(f"{name}: each row must be contiguous")
-        want *= t.shape[d]
+        want *= shape[d]
     # the innermost leading dimension longer than 1 sets the stride, the outer ones have to follow it
     rs, rows = None, 1
-    for d in range(len(lead) - 1, -1, -1):
-        if lead[d] > 1:
+    for d in range(lead - 1, -1, -1):
+        if shape[d] > 1:
             if rs is None:
-                rs = t.stride(d)
-            elif t.stride(d) != rs * rows:
+                rs = strides[d]
+            elif strides[d] != rs * rows:
                 raise ValueError(f"{name}: rows must be evenly strided")
-        rows *= lead[d]
+        rows *= shape[d]
     return want if rs is None else rs
 
 
-def _state(t, name, blocks, HV, K, V):
-    if t.dtype != torch.float32 or not t.is_contiguous():
+def _empty(x, shape=None, dtype=None):
+    """A contiguous tensor of x's (or this) shape and type on x's device."""
+    if shape is None:
+        return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+    return x.new_empty(shape, dtype=dtype)
+
+
+def _state(t, name, blocks, HV, K, V, dev):
+    _on_device(t, name, dev)
+    if t.dtype != _F32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 tensor")
-    if t.dim() != 4 or tuple(t.shape[1:]) != (HV, K, V) or (blocks is not None and t.shape[0] != blocks):
+    if t.dim() != 4 or t.shape[1:] != (HV, K, V) or (blocks is not None and t.shape[0] != blocks):
         raise ValueError(f"{name} must be [{'blocks' if blocks is None else blocks}, {HV}, {K}, {V}], got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -156,41 +181,44 @@ def scan_workspace_bytes(T: int, N: int, HV: int, K: int = 128, V: int = 128, *,
     return n
 
 
-def _scan_args(q, k, v, g, beta, initial_state, cu_seqlens, scale, workspace, training, slot_idx=None):
+def _scan_args(q, k, v, g, beta, cu_seqlens, scale, workspace, training):
+    """The arguments both calls share, the leading shape, (N, HV, K, V), the workspace and the current device."""
     if not isinstance(q, torch.Tensor) or not isinstance(v, torch.Tensor):
         raise TypeError("q and v must be torch.Tensors")
-    lead_dims = 1 if cu_seqlens is not None else 2
-    if q.dim() != lead_dims + 2 or v.dim() != lead_dims + 2:
+    n = 1 if cu_seqlens is not None else 2
+    if q.dim() != n + 2 or v.dim() != n + 2:
         raise ValueError("q, k, v must be [rows, HV, K|V] with cu_seqlens, [N, T, HV, K|V] without")
-    _on_device(dict(q=q, k=k, v=v, g=g, beta=beta, initial_state=initial_state, cu_seqlens=cu_seqlens, workspace=workspace,
-                    slot_idx=slot_idx))
-    lead, (HV, K), V = tuple(q.shape[:lead_dims]), q.shape[lead_dims:], v.shape[-1]
+    dev, qs, vs = _device(), q.shape, v.shape
+    lead, HV, K, V = qs[:n], qs[n], qs[n + 1], vs[n + 1]
+    a = ScanArgs()
     if cu_seqlens is not None:
+        _on_device(cu_seqlens, "cu_seqlens", dev)
         if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
             raise TypeError("cu_seqlens must be a contiguous int32 [N + 1] tensor")
         N, T = cu_seqlens.numel() - 1, lead[0]
+        a.cu_seqlens = cu_seqlens.data_ptr()
     else:
         N, T = lead
-    bf, f32 = torch.bfloat16, torch.float32
-    a = ScanArgs()
-    a.q, a.q_row_stride = q.data_ptr(), _row_stride(q, "q", bf, lead, (HV, K))
-    a.k, a.k_row_stride = k.data_ptr(), _row_stride(k, "k", bf, lead, (HV, K))
-    a.v, a.v_row_stride = v.data_ptr(), _row_stride(v, "v", bf, lead, (HV, V))
-    a.g, a.g_row_stride = g.data_ptr(), _row_stride(g, "g", f32, lead, (HV, K))
-    a.beta, a.beta_row_stride = beta.data_ptr(), _row_stride(beta, "beta", f32, lead, (HV,))
-    if cu_seqlens is not None:
-        a.cu_seqlens = cu_seqlens.data_ptr()
-    need = scan_workspace_bytes(T, N, HV, K, V, packed=cu_seqlens is not None, training=training)
+    a.q_row_stride = _row_stride(q, "q", _BF16, qs, n, dev)
+    a.k_row_stride = _row_stride(k, "k", _BF16, qs, n, dev)
+    a.v_row_stride = _row_stride(v, "v", _BF16, (*lead, HV, V), n, dev)
+    a.g_row_stride = _row_stride(g, "g", _F32, qs, n, dev)
+    a.beta_row_stride = _row_stride(beta, "beta", _F32, qs[:-1], n, dev)
+    a.q, a.k, a.v, a.g, a.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 tensor")
+        need = scan_workspace_bytes(T, N, HV, K, V, packed=cu_seqlens is not None, training=training)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
+    else:
+        _on_device(workspace, "workspace", dev)
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous uint8 tensor")
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     a.N, a.T, a.HV, a.K, a.V = N, T, HV, K, V
-    a.scale = float(1.0 / math.sqrt(K) if scale is None else scale)
-    return a, lead, (N, HV, K, V), workspace
+    a.scale = 1.0 / math.sqrt(K) if scale is None else scale
+    return a, lead, (N, HV, K, V), workspace, dev
 
 
+@_on_stream
 def kda_scan(q, k, v, g, beta, initial_state=None, *, cu_seqlens=None, slot_idx=None, final_state=None, out=None,
              scale: float | None = None, workspace=None, save: bool = False, stream=None):
     """The recurrence over whole sequences (``kda_scan`` of the C ABI); returns ``(out, final_state)``.
@@ -204,33 +232,36 @@ def kda_scan(q, k, v, g, beta, initial_state=None, *, cu_seqlens=None, slot_idx=
     updated in place unless another ``final_state`` pool is given; a slot outside it makes the sequence inactive (zero
     outputs).  ``workspace``: a device uint8 tensor of :func:`scan_workspace_bytes` bytes (allocated if not given);
     ``save=True`` (training size) keeps in it what :func:`kda_scan_backward` reads."""
-    a, lead, (N, HV, K, V), workspace = _scan_args(q, k, v, g, beta, initial_state, cu_seqlens, scale, workspace, save, slot_idx)
-    _on_device(dict(final_state=final_state, out=out))
+    a, lead, (N, HV, K, V), workspace, dev = _scan_args(q, k, v, g, beta, cu_seqlens, scale, workspace, save)
     blocks = N
     if slot_idx is not None:
         if initial_state is None:
             raise ValueError("slot_idx needs initial_state, the state pool")
-        if slot_idx.dtype != torch.int32 or tuple(slot_idx.shape) != (N,) or not slot_idx.is_contiguous():
+        _on_device(slot_idx, "slot_idx", dev)
+        _on_device(initial_state, "initial_state", dev)
+        if slot_idx.dtype != torch.int32 or slot_idx.shape != (N,) or not slot_idx.is_contiguous():
             raise TypeError(f"slot_idx must be a contiguous int32 [{N}] tensor")
         blocks = initial_state.shape[0]
         a.slot_idx, a.num_slots = slot_idx.data_ptr(), blocks
         if final_state is None:
             final_state = initial_state
     if final_state is None:
-        final_state = torch.empty((N, HV, K, V), dtype=torch.float32, device=q.device)
+        final_state = _empty(q, (N, HV, K, V), _F32)
     if initial_state is not None:
-        a.initial_state = _state(initial_state, "initial_state", blocks, HV, K, V)
-    a.final_state = _state(final_state, "final_state", blocks, HV, K, V)
+        a.initial_state = _state(initial_state, "initial_state", blocks, HV, K, V, dev)
+    a.final_state = _state(final_state, "final_state", blocks, HV, K, V, dev)
     if out is None:
-        out = torch.empty((*lead, HV, V), dtype=torch.bfloat16, device=q.device)
-    a.out, a.out_row_stride = out.data_ptr(), _row_stride(out, "out", torch.bfloat16, lead, (HV, V))
-    a.save = int(save)
-    st = layer_library().kda_scan(ctypes.byref(a), _stream(stream))
+        out = _empty(v)
+    a.out_row_stride = _row_stride(out, "out", _BF16, v.shape, len(lead), dev)
+    a.out = out.data_ptr()
+    a.save = bool(save)
+    st = layer_library().kda_scan(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _raise(st, "kda_scan")
     return out, final_state
 
 
+@_on_stream
 def kda_scan_backward(d_out, q, k, v, g, beta, initial_state=None, *, d_final_state=None, cu_seqlens=None,
                       scale: float | None = None, workspace=None, saved: bool = False, dq=None, dk=None, dv=None, dg=None,
                       dbeta=None, d_initial_state=None, stream=None):
@@ -243,32 +274,39 @@ def kda_scan_backward(d_out, q, k, v, g, beta, initial_state=None, *, d_final_st
     as they were."""
     if saved and workspace is None:
         raise ValueError("saved=True needs the forward call's workspace")
-    a, lead, (N, HV, K, V), workspace = _scan_args(q, k, v, g, beta, initial_state, cu_seqlens, scale, workspace, True)
-    _on_device(dict(d_out=d_out, d_final_state=d_final_state, dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta,
-                    d_initial_state=d_initial_state))
-    bf, f32 = torch.bfloat16, torch.float32
+    a, lead, (N, HV, K, V), workspace, dev = _scan_args(q, k, v, g, beta, cu_seqlens, scale, workspace, True)
+    n = len(lead)
     if initial_state is not None:
-        a.initial_state = _state(initial_state, "initial_state", N, HV, K, V)
+        a.initial_state = _state(initial_state, "initial_state", N, HV, K, V, dev)
     d = ScanGrads()
-    d.d_out, d.d_out_row_stride = d_out.data_ptr(), _row_stride(d_out, "d_out", bf, lead, (HV, V))
+    d.d_out_row_stride = _row_stride(d_out, "d_out", _BF16, v.shape, n, dev)
+    d.d_out = d_out.data_ptr()
     if d_final_state is not None:
-        d.d_final_state = _state(d_final_state, "d_final_state", N, HV, K, V)
-    got = []
-    for name, t, dtype, inner in (("dq", dq, bf, (HV, K)), ("dk", dk, bf, (HV, K)), ("dv", dv, bf, (HV, V)),
-                                  ("dg", dg, f32, (HV, K)), ("dbeta", dbeta, f32, (HV,))):
-        if t is None:
-            t = torch.empty((*lead, *inner), dtype=dtype, device=q.device)
-        setattr(d, name, t.data_ptr())
-        setattr(d, name + "_row_stride", _row_stride(t, name, dtype, lead, inner))
-        got.append(t)
+        d.d_final_state = _state(d_final_state, "d_final_state", N, HV, K, V, dev)
+    if dq is None:
+        dq = _empty(q)
+    if dk is None:
+        dk = _empty(q)
+    if dv is None:
+        dv = _empty(v)
+    if dg is None:
+        dg = _empty(g)
+    if dbeta is None:
+        dbeta = _empty(beta)
+    d.dq_row_stride = _row_stride(dq, "dq", _BF16, q.shape, n, dev)
+    d.dk_row_stride = _row_stride(dk, "dk", _BF16, q.shape, n, dev)
+    d.dv_row_stride = _row_stride(dv, "dv", _BF16, v.shape, n, dev)
+    d.dg_row_stride = _row_stride(dg, "dg", _F32, g.shape, n, dev)
+    d.dbeta_row_stride = _row_stride(dbeta, "dbeta", _F32, beta.shape, n, dev)
+    d.dq, d.dk, d.dv, d.dg, d.dbeta = dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr()
     if d_initial_state is None:
-        d_initial_state = torch.empty((N, HV, K, V), dtype=f32, device=q.device)
-    d.d_initial_state = _state(d_initial_state, "d_initial_state", N, HV, K, V)
-    d.saved = int(saved)
-    st = layer_library().kda_scan_backward(ctypes.byref(a), ctypes.byref(d), _stream(stream))
+        d_initial_state = _empty(q, (N, HV, K, V), _F32)
+    d.d_initial_state = _state(d_initial_state, "d_initial_state", N, HV, K, V, dev)
+    d.saved = bool(saved)
+    st = layer_library().kda_scan_backward(ctypes.byref(a), ctypes.byref(d), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _raise(st, "kda_scan_backward")
-    return (*got, d_initial_state)
+    return dq, dk, dv, dg, dbeta, d_initial_state
 
 
 def scan_error(workspace) -> int:
@@ -303,27 +341,16 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, tr
     return (freq if device is None else freq.to(device)), scale
 
 
-def _qk_row_stride(t, name, lead, H, D, dev):
-    if t.dtype != torch.bfloat16 or t.get_device() != dev:
-        _on_device({name: t})
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() == 3 and t.shape == (*lead, H, D) and t.stride(2) == 1 and t.stride(1) == D:  # the usual case, cheaply
-        return t.stride(0) if lead[0] > 1 else H * D
-    return _row_stride(t, name, torch.bfloat16, lead, (H, D))
-
-
 def _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale):
-    """The arguments both calls share, the leading shape, and the current device."""
+    """The arguments both calls share, the number of leading dimensions, D, and the current device."""
     if not isinstance(q, torch.Tensor) or q.dim() < 3:
         raise TypeError("q must be a torch.Tensor [..., heads, D]")
     if norm not in QK_NORMS:
         raise ValueError(f"norm must be one of {', '.join(QK_NORMS)}, got {norm!r}")
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    if not q.is_cuda or q.get_device() != dev:
-        _on_device(dict(q=q))
-    lead, D = q.shape[:-2], q.shape[-1]
+    dev, D, n = _device(), q.shape[-1], q.dim() - 2
+    lead = q.shape[:n]
     a = QkArgs()
-    a.rows = rows = math.prod(lead)
+    a.rows = math.prod(lead)
     a.D, a.norm, a.eps, a.rope_scale, a.interleaved = D, QK_NORMS[norm], eps, rope_scale, bool(interleaved)
     for name, x, w, t in (("q", q, q_weight, a.q), ("k", k, k_weight, a.k)):
         if x is None:
@@ -332,32 +359,32 @@ def _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleav
             continue
         if not isinstance(x, torch.Tensor) or x.dim() != q.dim() or x.shape[:-2] != lead or x.shape[-1] != D:
             raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, {D}]")
-        t.heads = x.shape[-2]
-        t.x, t.x_row_stride = x.data_ptr(), _qk_row_stride(x, name, lead, t.heads, D, dev)
+        t.x_row_stride = _row_stride(x, name, _BF16, x.shape, n, dev)
+        t.heads, t.x = x.shape[-2], x.data_ptr()
         if w is not None:
-            if not isinstance(w, torch.Tensor) or w.dtype != torch.bfloat16 or w.shape != (D,) or not w.is_contiguous():
+            _on_device(w, name + "_weight", dev)
+            if w.dtype != _BF16 or w.shape != (D,) or not w.is_contiguous():
                 raise TypeError(f"{name}_weight must be a contiguous bfloat16 [{D}] tensor")
-            if w.get_device() != dev:
-                _on_device({name + "_weight": w})
             if norm == "none":
                 raise ValueError(f"{name}_weight needs a norm")
             t.weight = w.data_ptr()
     if inv_freq is not None:
+        _on_device(inv_freq, "inv_freq", dev)
         if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise TypeError("inv_freq must be a contiguous float64 [rot / 2] tensor")
         if positions is None:
             raise ValueError("inv_freq needs positions")
+        _on_device(positions, "positions", dev)
         if positions.dtype not in (torch.int32, torch.int64) or positions.shape != lead or not positions.is_contiguous():
             raise TypeError(f"positions must be a contiguous int32 or int64 tensor of shape {tuple(lead)}")
-        if inv_freq.get_device() != dev or positions.get_device() != dev:
-            _on_device(dict(inv_freq=inv_freq, positions=positions))
         a.rot = 2 * inv_freq.numel()
         a.inv_freq, a.positions, a.positions_64 = inv_freq.data_ptr(), positions.data_ptr(), positions.dtype == torch.int64
     elif positions is not None:
         raise ValueError("positions need inv_freq")
-    return a, lead, D, dev
+    return a, n, D, dev
 
 
+@_on_stream
 def kda_qk_norm_rope(q, k=None, *, norm: str = "l2", eps: float = 1e-6, q_weight=None, k_weight=None, positions=None,
                      inv_freq=None, interleaved: bool = False, rope_scale: float = 1.0, q_out=None, k_out=None, stream=None):
     """Per-head norm of queries and keys and the position rotation in one pass; returns ``(q, k)`` as the decode step,
@@ -368,25 +395,26 @@ def kda_qk_norm_rope(q, k=None, *, norm: str = "l2", eps: float = 1e-6, q_weight
     ``[D]``) multiply after it.  ``inv_freq`` (float64 ``[rot / 2]``, :func:`rope_frequencies`) turns the first ``rot``
     components of each head by ``positions`` (int32 or int64, the leading shape) in halves or ``interleaved`` pairs, times
     ``rope_scale``.  Outputs are allocated if not given; ``q_out=q`` / ``k_out=k`` work in place."""
-    a, lead, D, dev = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale)
+    a, n, D, dev = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale)
     got = []
     for name, x, y, t in (("q_out", q, q_out, a.q), ("k_out", k, k_out, a.k)):
         if x is None:
             if y is not None:
                 raise ValueError("k_out without k")
         elif y is None:
-            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+            y = _empty(x)
             t.y, t.y_row_stride = y.data_ptr(), t.heads * D
         else:
-            _on_device({name: y})
-            t.y, t.y_row_stride = y.data_ptr(), _row_stride(y, name, torch.bfloat16, lead, (t.heads, D))
+            t.y_row_stride = _row_stride(y, name, _BF16, x.shape, n, dev)
+            t.y = y.data_ptr()
         got.append(y)
-    st = layer_library().kda_qk_norm_rope(ctypes.byref(a), _stream(stream))
+    st = layer_library().kda_qk_norm_rope(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _raise(st, "kda_qk_norm_rope")
     return tuple(got)
 
 
+@_on_stream
 def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k=None, *, norm: str = "l2", eps: float = 1e-6, q_weight=None,
                               k_weight=None, positions=None, inv_freq=None, interleaved: bool = False,
                               rope_scale: float = 1.0, dq=None, dk=None, workspace=None, stream=None):
@@ -394,7 +422,7 @@ def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k=None, *, norm: str = "l2", 
     last two fp32 ``[D]`` (None without the weight).  q, k and the options are the forward call's; ``dq`` / ``dk`` are
     allocated if not given (``dq=d_q_out`` / ``dk=d_k_out`` work in place), and so is ``workspace`` (device uint8, 4096 D
     bytes), used only with weights."""
-    a, lead, D, dev = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale)
+    a, n, D, dev = _qk_args(q, k, norm, eps, q_weight, k_weight, positions, inv_freq, interleaved, rope_scale)
     got, dws = [], []
     for name, x, dy, dx, w, t in (("q", q, d_q_out, dq, q_weight, a.q), ("k", k, d_k_out, dk, k_weight, a.k)):
         dw = None
@@ -402,29 +430,28 @@ def kda_qk_norm_rope_backward(d_q_out, d_k_out, q, k=None, *, norm: str = "l2", 
             if dy is not None or dx is not None:
                 raise ValueError("gradients of k without k")
         else:
-            if not isinstance(dy, torch.Tensor):
-                raise TypeError(f"d_{name}_out must be a torch.Tensor")
-            t.dy, t.dy_row_stride = dy.data_ptr(), _qk_row_stride(dy, f"d_{name}_out", lead, t.heads, D, dev)
+            t.dy_row_stride = _row_stride(dy, f"d_{name}_out", _BF16, x.shape, n, dev)
+            t.dy = dy.data_ptr()
             if dx is None:
-                dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+                dx = _empty(x)
                 t.dx, t.dx_row_stride = dx.data_ptr(), t.heads * D
             else:
-                _on_device({"d" + name: dx})
-                t.dx, t.dx_row_stride = dx.data_ptr(), _row_stride(dx, "d" + name, torch.bfloat16, lead, (t.heads, D))
+                t.dx_row_stride = _row_stride(dx, "d" + name, _BF16, x.shape, n, dev)
+                t.dx = dx.data_ptr()
             if w is not None:
-                dw = torch.empty(D, dtype=torch.float32, device=x.device)
+                dw = x.new_empty(D, dtype=_F32)
                 t.dweight = dw.data_ptr()
         got.append(dx)
         dws.append(dw)
     if q_weight is not None or k_weight is not None:
         if workspace is None:
-            workspace = torch.empty(max(layer_library().kda_qk_workspace_bytes(D), 16), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(max(layer_library().kda_qk_workspace_bytes(D), 16), dtype=torch.uint8)
         else:
-            _on_device(dict(workspace=workspace))
+            _on_device(workspace, "workspace", dev)
             if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
                 raise TypeError("workspace must be a contiguous uint8 tensor")
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    st = layer_library().kda_qk_norm_rope_backward(ctypes.byref(a), _stream(stream))
+    st = layer_library().kda_qk_norm_rope_backward(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(dev))
     if st:
         _raise(st, "kda_qk_norm_rope_backward")
     return (*got, *dws)
