@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "kda_layer_host.h"
+#include "kda_scan_chain.cuh"
 #include "kda_scan_grad.cuh"
 #include "kda_scan_prep.cuh"
 #include "layer/kda_scan.h"
@@ -13,12 +14,7 @@ namespace {
 using namespace kda_layer;
 namespace ks = kdal;
 
-template <int STRIPS>
-constexpr int kForwardSmem = static_cast<int>(sizeof(typename ks::ChainCfg<STRIPS>::Forward));
-template <int STRIPS>
-constexpr int kBackwardSmem = static_cast<int>(sizeof(typename ks::ChainCfg<STRIPS>::Backward));
-static_assert(kForwardSmem<4> <= 232448 && kBackwardSmem<4> <= 232448 && kForwardSmem<2> <= 232448 && kBackwardSmem<2> <= 232448,
-              "shared memory of an SM");
+constexpr int kChainSmem = static_cast<int>(sizeof(ks::ChainSmem));
 
 // Dynamic shared memory allowances, once per device.
 cudaError_t prepare_kernels() {
@@ -32,12 +28,8 @@ cudaError_t prepare_kernels() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
   allow(ks::kda_scan_prep_kernel, static_cast<int>(sizeof(ks::PrepSmem)));
-  allow(ks::kda_scan_forward_kernel<1>, kForwardSmem<1>);
-  allow(ks::kda_scan_forward_kernel<2>, kForwardSmem<2>);
-  allow(ks::kda_scan_forward_kernel<4>, kForwardSmem<4>);
-  allow(ks::kda_scan_backward_kernel<1>, kBackwardSmem<1>);
-  allow(ks::kda_scan_backward_kernel<2>, kBackwardSmem<2>);
-  allow(ks::kda_scan_backward_kernel<4>, kBackwardSmem<4>);
+  allow(ks::kda_scan_forward_kernel, kChainSmem);
+  allow(ks::kda_scan_backward_kernel, kChainSmem);
   allow(ks::kda_scan_grad_kernel, static_cast<int>(sizeof(ks::GradSmem)));
   if (e == cudaSuccess && bit) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -78,7 +70,7 @@ kda_status common(const kda_scan_args& a, bool training, ks::ScanParams* p, int6
   if (!mul_ok(a.N, packed ? 1 : a.T, rows)) return KDA_ERR_UNSUPPORTED;
   if (packed) *rows = a.T;
   if (!chunk_slots(a.N, a.T, packed, slots) || !workspace_bytes(a.N, a.T, packed, a.HV, training, &need) ||
-      !mul_ok(a.N, a.HV, &units) || units > 0x7fffffffLL / 8 || a.N > 0x7fffffffLL || *rows > INT64_MAX / (a.HV * ks::kK * 8))
+      !mul_ok(a.N, a.HV, &units) || units > 0x7fffffffLL || a.N > 0x7fffffffLL || *rows > INT64_MAX / (a.HV * ks::kK * 8))
     return KDA_ERR_UNSUPPORTED;
   if (packed && a.T > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;  // int32 offsets
   const int64_t hk = a.HV * ks::kK, hv = a.HV * ks::kV;
@@ -134,25 +126,9 @@ bool launch(F kernel, int64_t grid, int threads, int smem, kda_stream_t stream, 
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
 }
 
-// Strips of 16 value columns a CTA of the chain kernels takes: one while every
-// strip can have an SM of its own, more as the CTAs would otherwise queue.
-int chain_strips(int64_t units) { return units * 8 <= sm_count() ? 1 : (units * 4 <= sm_count() ? 2 : 4); }
-
-template <int STRIPS>
-bool launch_chain(bool forward, const ks::ScanParams& p, kda_stream_t stream) {
-  const int64_t grid = p.N * p.HV * (8 / STRIPS);
-  return forward ? launch(ks::kda_scan_forward_kernel<STRIPS>, grid, STRIPS * 128, kForwardSmem<STRIPS>, stream, p)
-                 : launch(ks::kda_scan_backward_kernel<STRIPS>, grid, STRIPS * 128, kBackwardSmem<STRIPS>, stream, p);
-}
-bool launch_chain(bool forward, const ks::ScanParams& p, kda_stream_t stream) {
-  const int strips = chain_strips(p.N * p.HV);
-  return strips == 1 ? launch_chain<1>(forward, p, stream)
-                     : (strips == 2 ? launch_chain<2>(forward, p, stream) : launch_chain<4>(forward, p, stream));
-}
-
 bool launch_forward(const ks::ScanParams& p, int64_t slots, kda_stream_t stream) {
   return launch(ks::kda_scan_prep_kernel, slots * p.HV, ks::kPrepThreads, sizeof(ks::PrepSmem), stream, p) &&
-         launch_chain(true, p, stream);
+         launch(ks::kda_scan_forward_kernel, p.N * p.HV, ks::kForwardThreads, kChainSmem, stream, p);
 }
 
 }  // namespace
@@ -240,7 +216,7 @@ kda_status kda_scan_backward(const kda_scan_args* args, const kda_scan_grads* gr
   p.dbeta = d.dbeta, p.dbeta_ts = d.dbeta_row_stride;
   p.d_init = d.d_initial_state;
   if (!d.saved && !launch_forward(p, slots, stream)) return KDA_ERR_CUDA;  // p.out is null: states only
-  if (!launch_chain(false, p, stream)) return KDA_ERR_CUDA;
+  if (!launch(ks::kda_scan_backward_kernel, a.N * a.HV, ks::kBackwardThreads, kChainSmem, stream, p)) return KDA_ERR_CUDA;
   return launch(ks::kda_scan_grad_kernel, slots * a.HV, ks::kGradThreads, sizeof(ks::GradSmem), stream, p) ? KDA_OK
                                                                                                           : KDA_ERR_CUDA;
 }

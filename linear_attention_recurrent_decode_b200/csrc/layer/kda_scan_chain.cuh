@@ -7,625 +7,560 @@
 //   dU = scale P^T dO + Ke dS1
 //   dS0 = Diag(exp(Gamma_C)) dS1 + scale Qt^T dO - Wr^T (beta dU).
 //
-// The value columns are independent: a strip is 16 of them, and a CTA walks the
-// chunks with one, two or four strips that share the chunk's tiles (a ring of
-// bulk copies).  A strip is four warps, one on each of the SM's schedulers,
-// because the chain's latency is what bounds it: one warp a strip, with no
-// exchange at all, measured 5.4 us a chunk forward and 7.3 us backward, against
-// 1.8 and 2.4 us here (one sequence, 8 heads).  Each warp keeps a quarter of the transposed
-// state, S^T [16 x 32 channels], in 16 accumulator registers a thread.  Per
-// chunk the warps of a strip exchange twice through shared memory: the sums
-// over their channels of S0^T Wr^T (each warp joins those of its 16 tokens),
-// then the resulting U^T as MMA fragments.  The accumulator layout of one
-// product is the A-operand layout of the next, so nothing is rearranged.
+// One CTA a sequence and head.  Everything is transposed so that the 128 value
+// columns are the M rows of the tensor cores' products and the lanes of tensor
+// memory: four threads a value column keep the state, 32 channels each, in fp32
+// registers.  Per chunk they write the state as an fp16 pair into
+// tensor memory (the A operand), read S0^T Wr^T back, write U^T there, and add
+// the read product U^T Ke to the decayed registers: the fp32 state itself never
+// passes through a product's accumulator, and rows never meet, but for the
+// scales, one per 32 of them.  The B operands are the record's tiles, straight
+// from bulk copies.
+//
+// Warps: 0-15 compute, 16 copies, 17 issues the products, 18-21 (forward) read
+// the outputs back.  A chunk's critical path is two products with a conversion
+// behind each; the outputs' products and read-back run beside it.
 #pragma once
 
 #include "kda_scan_common.cuh"
+#include "kda_umma.cuh"
 
 namespace kdal {
 
-constexpr int kStageBytes = 2 * Record::kPlane + Record::kHdr;  // 33 KB: two planes and a header
-constexpr int kDoPitch = 48;  // bytes per token row of a strip's 16 columns of dO (32 used)
+constexpr int kParts = 4;                    // threads of a value column
+constexpr int kComputeWarps = 4 * kParts;
+constexpr int kPartK = kK / kParts, kPartT = kC / kParts;  // a thread's channels and tokens
+constexpr uint32_t kTmemColumns = 512;
 
-// Exchange buffers of a strip.
-struct Strip {
-  float4 part[4][3][2][32];  // [from][to, without from][column tile of to's 16 tokens][lane]
-  uint4 u[4][2][32];         // U^T fragments per 16 tokens: hi, lo
-  uint4 s[4][2][32];         // forward: S^T fragments (hi) per 32 channels
+// Shared memory of both chains.  Wr, Ke and the header of two chunks, Qt and P of one.
+struct ChainSmem {
+  unsigned char wr[2][2 * Record::kPlane], ke[2][2 * Record::kPlane];
+  unsigned char qt[2 * Record::kPlane], p[kC * kC * 4];
+  unsigned char hdr[2][Record::kHdr];
+  float peak[4][kParts][4];      // [exchange][part][quarter of the value columns]
+  float sc_s[2][4], sc_u[2][4];  // by chunk parity, for the outputs
+  uint64_t full_wr[2], full_ke[2], full_hdr[2], full_qt, full_p, empty_hdr[2];
+  uint64_t state, rows, scales[2];  // written by the compute warps: the state, U (or dU), the scales
+  // Products done, by chunk parity: S0^T Wr^T (or dS1^T Ke^T), the state's with U; with Qt; forward: the outputs' with P.
+  // A tile's place is free again once the products that read it are.
+  uint64_t first[2], last[2], with_qt, out_done;
+  uint64_t out_free;                // forward: the outputs are read
+  uint64_t d_out;                   // backward: dO is written
+  uint64_t end;
+  uint32_t tmem;
 };
-struct StripBack {
-  float4 part[4][3][2][32];
-  uint4 u[4][2][32];
-  unsigned char dO[2][kC * kDoPitch];  // this chunk's and the next one's, [t][v] in fp16
-  float sc_u[4], sc_do[2][4];
-};
-struct StripScales {
-  float u[4], s[4];
-};
+static_assert(sizeof(ChainSmem) <= 232448, "shared memory of an SM");
 
-template <int STRIPS>
-struct ChainCfg {
-  static constexpr int kRing = STRIPS == 4 ? 4 : 5;
-  static constexpr int kAhead = kRing - 2;  // items copied ahead of the one in use
-  struct Common {
-    unsigned char stage[kRing][kStageBytes];
-    uint64_t full[kRing], empty[kRing];
-  };
-  struct Forward : Common {
-    Strip strip[STRIPS];
-    StripScales sc[STRIPS];
-  };
-  struct Backward : Common {
-    StripBack strip[STRIPS];
-  };
-};
-
-// What a stage holds: up to two pieces of a record.
-struct Piece {
-  int off0, bytes0, off1, bytes1;
-};
-// Forward: header and Wr; P (hi) and Qt (hi); header and Ke.
-// Backward: header and Ke; P; header and Qt; Wr.
-template <bool FWD>
-__device__ __forceinline__ Piece piece(int s) {
-  if constexpr (FWD) {
-    if (s == 0) return Piece{0, Record::kHdr, Record::kWr, 2 * Record::kPlane};
-    if (s == 1) return Piece{Record::kP, kC * kC * 2, Record::kQt, Record::kPlane};
-    return Piece{0, Record::kHdr, Record::kKe, 2 * Record::kPlane};
-  } else {
-    if (s == 0) return Piece{0, Record::kHdr, Record::kKe, 2 * Record::kPlane};
-    if (s == 1) return Piece{Record::kP, kC * kC * 4, 0, 0};
-    if (s == 2) return Piece{0, Record::kHdr, Record::kQt, 2 * Record::kPlane};
-    return Piece{Record::kWr, 2 * Record::kPlane, 0, 0};
+// A wait that remembers whether any gave up; from then on none waits, and the kernel runs to its end on whatever it has,
+// so that every barrier stays matched.  For whole warps `ok` is uniform.
+struct Waiter {
+  bool ok = true;
+  __device__ __forceinline__ void one(uint64_t* bar, int64_t phase) {  // a single thread
+    ok = ok && mbar_wait(bar, static_cast<uint32_t>(phase & 1));
   }
+  __device__ __forceinline__ void warp(uint64_t* bar, int64_t phase) {
+    one(bar, phase);
+    ok = __all_sync(0xffffffffu, ok);
+  }
+};
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
-// A warp's place in the ring.  One thread of the CTA also refills it: as it
-// comes to an item it starts the copy of the item kAhead further on, into the
-// stage that every warp released kRing - kAhead items ago.
-template <bool FWD, int STRIPS>
-struct Ring {
-  using Cfg = ChainCfg<STRIPS>;
-  static constexpr int kPer = FWD ? 3 : 4, kRing = Cfg::kRing;
-  const ScanParams& p;
-  typename Cfg::Common& sm;
-  const unsigned char* rec;  // of the next item to copy
-  int64_t step;              // to the next chunk's record
-  int32_t items, lane;
-  bool producer;
-  int32_t it = 0, stage = 0, phase = 0;  // the next item to release
-  int32_t put = 0, put_stage = 0, put_phase = 0, put_piece = 0;
-  bool ok = true;
-
-  __device__ __forceinline__ void fill() {
-    if (put >= items) return;
-    if (put >= kRing) ok = ok && mbar_wait(&sm.empty[put_stage], static_cast<uint32_t>(put_phase ^ 1));
-    if (!ok) return;
-    const Piece pc = piece<FWD>(put_piece);
-    mbar_expect(&sm.full[put_stage], static_cast<uint32_t>(pc.bytes0 + pc.bytes1));
-    bulk_load(sm.stage[put_stage], rec + pc.off0, static_cast<uint32_t>(pc.bytes0), &sm.full[put_stage]);
-    if (pc.bytes1)
-      bulk_load(sm.stage[put_stage] + pc.bytes0, rec + pc.off1, static_cast<uint32_t>(pc.bytes1), &sm.full[put_stage]);
-    ++put;
-    if (++put_stage == kRing) {
-      put_stage = 0;
-      put_phase ^= 1;
-    }
-    if (++put_piece == kPer) {
-      put_piece = 0;
-      rec += step;
-    }
-  }
-  __device__ __forceinline__ void start() {
-    if (producer)
-      for (int j = 0; j < Cfg::kAhead; ++j) fill();
-  }
-  // The current item, once it is there.  A warp whose wait gave up goes on without waiting, so that the strip's barriers
-  // stay matched; `ok` is uniform over the warp.
-  __device__ __forceinline__ const unsigned char* wait() {
-    if (producer) fill();
-    ok = ok && mbar_wait(&sm.full[stage], static_cast<uint32_t>(phase));
-    ok = __all_sync(0xffffffffu, ok);
-    return sm.stage[stage];
-  }
-  __device__ __forceinline__ void release() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.empty[stage]);
-    ++it;
-    if (++stage == kRing) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-  // After a wait that gave up: the CTA must not end with copies into it in flight.
-  __device__ __forceinline__ void abandon() {
-    if (lane == 0) set_error(p);
-    if (producer)
-      for (int32_t j = put > kRing ? put - kRing : 0; j < put; ++j)
-        mbar_wait(&sm.full[j % kRing], static_cast<uint32_t>((j / kRing) & 1));
-  }
-};
-
-template <typename Common>
-__device__ __forceinline__ void chain_init(Common& sm, int ring, int warps) {
+__device__ __forceinline__ void chain_init(ChainSmem& sm, int header_readers) {
+  if (threadIdx.x < 32) tmem_alloc(&sm.tmem, kTmemColumns);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ring; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], warps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.full_wr[i], 1);
+      mbar_init(&sm.full_ke[i], 1);
+      mbar_init(&sm.full_hdr[i], 1);
+      mbar_init(&sm.first[i], 1);
+      mbar_init(&sm.last[i], 1);
+      mbar_init(&sm.empty_hdr[i], header_readers);
+      mbar_init(&sm.scales[i], kComputeWarps);
     }
+    mbar_init(&sm.full_qt, 1);
+    mbar_init(&sm.full_p, 1);
+    mbar_init(&sm.with_qt, 1);
+    mbar_init(&sm.state, kComputeWarps);
+    mbar_init(&sm.rows, kComputeWarps);
+    mbar_init(&sm.d_out, kComputeWarps);
+    mbar_init(&sm.out_done, 1);
+    mbar_init(&sm.out_free, 4);
+    mbar_init(&sm.end, 1);
     mbar_fence_init();
   }
+  fence_before_sync();
   __syncthreads();
+  fence_after_sync();
 }
-// Barrier of a strip's four warps.
-__device__ __forceinline__ void strip_sync(int strip) { asm volatile("bar.sync %0, 128;" ::"r"(strip + 1) : "memory"); }
-
-__device__ __forceinline__ float max4(const float (&a)[4], float m) {
-  return fmaxf(fmaxf(fmaxf(fabsf(a[0]), fabsf(a[1])), fmaxf(fabsf(a[2]), fabsf(a[3]))), m);
+__device__ __forceinline__ void chain_exit(ChainSmem& sm) {
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x < 32) tmem_dealloc(sm.tmem, kTmemColumns);
 }
 
-// A 16 x 16 A-fragment pair to rows v0.. of a tile, columns c0..
-template <int COLS>
-__device__ __forceinline__ void store_frag(unsigned char* tile, int plane, int v0, int c0, int lane, const uint32_t (&ah)[4],
-                                           const uint32_t (&al)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t off = tile_off<COLS>(v0 + (lane >> 2) + (j & 1) * 8, c0 + (j >> 1) * 8 + 2 * (lane & 3));
-    *reinterpret_cast<uint32_t*>(tile + off) = ah[j];
-    *reinterpret_cast<uint32_t*>(tile + plane + off) = al[j];
+// The copies of every chunk's tiles, one thread; a tile's copy starts once the products of the tile before it in the
+// same place are complete.
+template <bool FWD>
+__device__ __forceinline__ void chain_copies(ChainSmem& sm, Waiter& w, const unsigned char* rec, int64_t step, int64_t chunks,
+                                             bool outputs) {
+  int64_t c = 0;
+  for (; c < chunks && w.ok; ++c, rec += step) {
+    const int b = static_cast<int>(c & 1);
+    auto put = [&](void* dst, int off, uint32_t bytes, uint64_t* full) {
+      if (!w.ok) return;
+      mbar_expect(full, bytes);
+      bulk_load(dst, rec + off, bytes, full);
+    };
+    if (c >= 2) w.one(&sm.empty_hdr[b], (c >> 1) - 1);
+    put(sm.hdr[b], 0, Record::kHdr, &sm.full_hdr[b]);
+    // Wr is read by the first product forwards, by the last backwards; Ke the other way round
+    if (c >= 2) w.one(&sm.first[b], (c >> 1) - 1);
+    if constexpr (FWD) put(sm.wr[b], Record::kWr, 2 * Record::kPlane, &sm.full_wr[b]);
+    else put(sm.ke[b], Record::kKe, 2 * Record::kPlane, &sm.full_ke[b]);
+    if (c >= 2) w.one(&sm.last[b], (c >> 1) - 1);
+    if constexpr (FWD) put(sm.ke[b], Record::kKe, 2 * Record::kPlane, &sm.full_ke[b]);
+    else put(sm.wr[b], Record::kWr, 2 * Record::kPlane, &sm.full_wr[b]);
+    if (!outputs) continue;
+    if (c >= 1) w.one(&sm.with_qt, c - 1);
+    put(sm.qt, Record::kQt, 2 * Record::kPlane, &sm.full_qt);
+    // P: backwards the product with it was issued ahead of the chunk's first
+    if (c >= 1) w.one(FWD ? &sm.out_done : &sm.first[b ^ 1], FWD ? c - 1 : (c - 1) >> 1);
+    put(sm.p, Record::kP, kC * kC * 4, &sm.full_p);
   }
-}
-__device__ __forceinline__ uint4 vec(const uint32_t (&a)[4]) { return make_uint4(a[0], a[1], a[2], a[3]); }
-__device__ __forceinline__ void unvec(uint4 v, uint32_t (&a)[4]) {
-  a[0] = v.x;
-  a[1] = v.y;
-  a[2] = v.z;
-  a[3] = v.w;
-}
-
-// 16 value columns x 32 channels of a [K][V] block in the accumulator layout: element (v, i).
-__device__ __forceinline__ void load_state(const float* blk, int v0, int i0, int lane, float (&s)[4][4]) {
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      s[n][e] = blk == nullptr ? 0.f : blk[(i0 + n * 8 + 2 * (lane & 3) + (e & 1)) * kV + v0 + (lane >> 2) + (e >> 1) * 8];
-}
-__device__ __forceinline__ void store_state(float* blk, int v0, int i0, int lane, const float (&s)[4][4]) {
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      blk[(i0 + n * 8 + 2 * (lane & 3) + (e & 1)) * kV + v0 + (lane >> 2) + (e >> 1) * 8] = s[n][e];
-}
-
-// [16 value columns x 16 tokens] of an accumulator pair, rounded to bf16, to rows (token, 16 values).
-__device__ __forceinline__ void store_out16(__nv_bfloat16* out, int64_t ts, int t0, int tc, int lane, const float (&c0)[4],
-                                            const float (&c1)[4], float f) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float(&c)[4] = j ? c1 : c0;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(c[0] * f, c[1] * f), hi = __floats2bfloat162_rn(c[2] * f, c[3] * f);
-    const uint32_t a = transpose8(*reinterpret_cast<const uint32_t*>(&lo)), b = transpose8(*reinterpret_cast<const uint32_t*>(&hi));
-    const int t = t0 + j * 8 + (lane >> 2);
-    if (t < tc) {
-      *reinterpret_cast<uint32_t*>(out + t * ts + 2 * (lane & 3)) = a;
-      *reinterpret_cast<uint32_t*>(out + t * ts + 8 + 2 * (lane & 3)) = b;
+  // After a wait that gave up: the CTA must not end with copies into it in flight.  The last copy into each place may be.
+  if (w.ok || c == 0) return;
+  --c;
+  for (int64_t d = c > 0 ? c - 1 : 0; d <= c; ++d) {
+    mbar_wait(&sm.full_hdr[d & 1], static_cast<uint32_t>((d >> 1) & 1));
+    mbar_wait(&sm.full_wr[d & 1], static_cast<uint32_t>((d >> 1) & 1));
+    mbar_wait(&sm.full_ke[d & 1], static_cast<uint32_t>((d >> 1) & 1));
+    if (outputs) {
+      mbar_wait(&sm.full_qt, static_cast<uint32_t>(d & 1));
+      mbar_wait(&sm.full_p, static_cast<uint32_t>(d & 1));
     }
   }
 }
 
-// The sums over a warp's 32 channels, S^T [16 x 32] B^T [32 x 64 tokens] with B a pair tile [t][i], in true units.
-__device__ __forceinline__ void channel_sums(uint32_t tile, int i0, int lane, const uint32_t (&ah)[2][4], const uint32_t (&al)[2][4],
-                                             float inv, float (&x)[8][4]) {
+// A quarter of a value column: the thread's channels of a [K][V] block.
+__device__ __forceinline__ void load_state(const float* blk, int v, int part, float (&s)[kPartK]) {
 #pragma unroll
-  for (int nb = 0; nb < 4; ++nb) {
-    uint32_t bh[2][4], bl[2][4];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      load_b<128>(tile, i0 + kk * 16, nb * 16, lane, bh[kk]);
-      load_b<128>(tile + Record::kPlane, i0 + kk * 16, nb * 16, lane, bl[kk]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[2 * nb][e] = x[2 * nb + 1][e] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      mma_pair(x[2 * nb], x[2 * nb + 1], ah[kk], bl[kk]);
-      mma_pair(x[2 * nb], x[2 * nb + 1], al[kk], bh[kk]);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) mma_pair(x[2 * nb], x[2 * nb + 1], ah[kk], bh[kk]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * nb][e] *= inv;
-      x[2 * nb + 1][e] *= inv;
-    }
-  }
+  for (int j = 0; j < kPartK; ++j) s[j] = blk == nullptr ? 0.f : blk[(part * kPartK + j) * kV + v];
 }
-// Hands each warp of the strip the sums of its 16 tokens.
-__device__ __forceinline__ void put_sums(float4 (&part)[4][3][2][32], int quarter, int lane, const float (&x)[8][4]) {
+__device__ __forceinline__ void store_state(float* blk, int v, int part, const float (&s)[kPartK]) {
 #pragma unroll
-  for (int to = 0; to < 4; ++to)
+  for (int j = 0; j < kPartK; ++j) blk[(part * kPartK + j) * kV + v] = s[j];
+}
+// The largest of `m` over a quarter's 32 value columns: the four warps that share them.
+__device__ __forceinline__ float quarter_max(ChainSmem& sm, int exchange, float m, int part, int quarter) {
+  m = warp_max(m);
+  sm.peak[exchange][part][quarter] = m;  // every lane the same value
+  asm volatile("bar.sync %0, 128;" ::"r"(quarter + 1) : "memory");
+  m = fmaxf(fmaxf(sm.peak[exchange][0][quarter], sm.peak[exchange][1][quarter]),
+            fmaxf(sm.peak[exchange][2][quarter], sm.peak[exchange][3][quarter]));
+  return m;
+}
+
+// x[n] sc as a pair, this thread's elements `first` .. of K: into tensor memory as the lane's A operand (hi, then lo), or
+// into the record's Core<kV> tile [v][element] with planes `plane` apart (apart from each other: the stores to the record
+// are issued while the products run).  With `f`, the elements times f[0 .. COUNT - 1] (shared memory).
+template <int K, bool TMEM, int COUNT>
+__device__ __forceinline__ void write_pair(uint32_t ta, unsigned char* tile, int plane, int v, int first, const float (&x)[COUNT], float sc,
+                                           const float* f = nullptr) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (to != quarter) {
-        const float(&c)[4] = x[2 * to + j];
-        part[quarter][to > quarter ? to - 1 : to][j][lane] = make_float4(c[0], c[1], c[2], c[3]);
+  for (int g = 0; g < COUNT / 16; ++g) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float2 fe = make_float2(sc, sc);
+      if (f != nullptr) {
+        const float2 y = *reinterpret_cast<const float2*>(f + g * 16 + 2 * e);
+        fe = make_float2(y.x * sc, y.y * sc);
       }
-}
-// This warp's tokens: its own sums and the other three warps', in a fixed order.
-__device__ __forceinline__ void take_sums(const float4 (&part)[4][3][2][32], int quarter, int lane, const float (&x)[8][4],
-                                          float (&own)[2][4]) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float4 c[4];
-#pragma unroll
-    for (int from = 0; from < 4; ++from) {
-      c[from] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (from != quarter) c[from] = part[from][quarter > from ? quarter - 1 : quarter][j][lane];
+      split2(x[g * 16 + 2 * e] * fe.x, x[g * 16 + 2 * e + 1] * fe.y, hi[e], lo[e]);
     }
+    if constexpr (TMEM) {
+      tmem_st(ta + first / 2 + g * 8, hi);
+      tmem_st(ta + K / 2 + first / 2 + g * 8, lo);
+    }
+    if constexpr (!TMEM) {
 #pragma unroll
-    for (int to = 0; to < 4; ++to)
-      if (to == quarter) {
-        const float(&m)[4] = x[2 * to + j];
-        c[to] = make_float4(m[0], m[1], m[2], m[3]);
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t off = Core<kV>::off(v, first + g * 16 + e * 8);
+        *reinterpret_cast<uint4*>(tile + off) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+        *reinterpret_cast<uint4*>(tile + plane + off) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
       }
-    own[j][0] = (c[0].x + c[1].x) + (c[2].x + c[3].x);
-    own[j][1] = (c[0].y + c[1].y) + (c[2].y + c[3].y);
-    own[j][2] = (c[0].z + c[1].z) + (c[2].z + c[3].z);
-    own[j][3] = (c[0].w + c[1].w) + (c[2].w + c[3].w);
-  }
-}
-// s += f U^T [16 x 16 tokens] B [16 tokens x 32 channels] with B a pair tile [t][i].
-template <bool PAIR>
-__device__ __forceinline__ void add_outer(uint32_t tile, int t0, int i0, int lane, const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                          float f, float (&s)[4][4]) {
-#pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    uint32_t bh[4], bl[4];
-    load_b_t<128>(tile, t0, i0 + nb * 16, lane, bh);
-    load_b_t<128>(tile + Record::kPlane, t0, i0 + nb * 16, lane, bl);
-    float x0[4] = {}, x1[4] = {};
-    mma_pair(x0, x1, ah, bl);
-    if constexpr (PAIR) mma_pair(x0, x1, al, bh);
-    mma_pair(x0, x1, ah, bh);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[2 * nb][e] = fmaf(x0[e], f, s[2 * nb][e]);
-      s[2 * nb + 1][e] = fmaf(x1[e], f, s[2 * nb + 1][e]);
     }
   }
 }
-// s = s Diag(exp(Gamma_C)) for the warp's channels.
-__device__ __forceinline__ void decay_state(const float* decay, int lane, float (&s)[4][4]) {
+// s = s d + f x, x read from tensor memory, d the channels' factors in shared memory.
+template <bool DECAY>
+__device__ __forceinline__ void add_product(uint32_t ta, const float* d, float f, float (&s)[kPartK]) {
+  uint32_t x[kPartK];
+  tmem_ld(ta, x);
+  tmem_wait_ld();
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const float2 d = *reinterpret_cast<const float2*>(decay + n * 8 + 2 * (lane & 3));
-    s[n][0] *= d.x;
-    s[n][1] *= d.y;
-    s[n][2] *= d.x;
-    s[n][3] *= d.y;
+  for (int j = 0; j < kPartK; j += 4) {
+    float4 dj = make_float4(1.f, 1.f, 1.f, 1.f);
+    if constexpr (DECAY) dj = *reinterpret_cast<const float4*>(d + j);
+    s[j] = fmaf(s[j], dj.x, __uint_as_float(x[j]) * f);
+    s[j + 1] = fmaf(s[j + 1], dj.y, __uint_as_float(x[j + 1]) * f);
+    s[j + 2] = fmaf(s[j + 2], dj.z, __uint_as_float(x[j + 2]) * f);
+    s[j + 3] = fmaf(s[j + 3], dj.w, __uint_as_float(x[j + 3]) * f);
   }
+}
+template <int N>
+__device__ __forceinline__ float abs_max(const float (&x)[N]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) m = fmaxf(m, fabsf(x[j]));
+  return m;
+}
+template <int N>
+__device__ __forceinline__ float abs_max(const float (&x)[N], const float* f) {  // of the products with f (shared memory)
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    const float4 y = *reinterpret_cast<const float4*>(f + j);
+    m = fmaxf(m, fmaxf(fmaxf(fabsf(x[j] * y.x), fabsf(x[j + 1] * y.y)), fmaxf(fabsf(x[j + 2] * y.z), fabsf(x[j + 3] * y.w))));
+  }
+  return m;
 }
 
-template <int STRIPS>
-__global__ void __launch_bounds__(STRIPS * 128, 1) kda_scan_forward_kernel(const __grid_constant__ ScanParams p) {
+// ---------------------------------------------------------------- forward
+// Columns of tensor memory.
+struct ForwardColumns {
+  static constexpr uint32_t kState = 0, kU = 128, kX = 192, kO1 = 256, kO2 = 320, kDelta = 384;
+};
+constexpr int kForwardThreads = (kComputeWarps + 6) * 32;
+
+__global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(const __grid_constant__ ScanParams p) {
+  using Col = ForwardColumns;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<typename ChainCfg<STRIPS>::Forward*>(smem_raw);
-  constexpr int kTiles = 8 / STRIPS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, strip = warp >> 2, quarter = warp & 3;
-  const int64_t unit = blockIdx.x / kTiles;
-  const int group = static_cast<int>(blockIdx.x - unit * kTiles) * STRIPS + strip;  // 16 value columns
-  const int64_t n = unit / p.HV, h = unit - n * p.HV;
+  ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
+  const int64_t n = blockIdx.x / p.HV, h = blockIdx.x - n * p.HV;
   int64_t start, len;
   seq_range(p, n, start, len);
-  const int32_t nch = static_cast<int32_t>((len + kC - 1) / kC);
-  const int64_t slot0 = first_slot(p, n, start), blk = state_block(p, n);
-  const int v0 = group * 16, i0 = quarter * 32, t0 = quarter * 16;
+  const int64_t chunks = (len + kC - 1) / kC, slot0 = first_slot(p, n, start), blk = state_block(p, n);
   if (blk < 0) {  // inactive: zero outputs
-    for (int64_t t = quarter * 32 + lane; t < len * 2; t += 128)
-      *reinterpret_cast<uint4*>(p.out + (start + (t >> 1)) * p.out_ts + h * kV + v0 + (t & 1) * 8) = make_uint4(0, 0, 0, 0);
+    for (int64_t t = threadIdx.x; t < len * 16; t += kForwardThreads)
+      *reinterpret_cast<uint4*>(p.out + (start + (t >> 4)) * p.out_ts + h * kV + (t & 15) * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
-  chain_init(sm, ChainCfg<STRIPS>::kRing, STRIPS * 4);
-  Strip& st = sm.strip[strip];
-  StripScales& sc = sm.sc[strip];
+  const bool outputs = p.out != nullptr;
+  chain_init(sm, outputs ? kComputeWarps + 4 : kComputeWarps);
   const int64_t sblk = (blk * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
   unsigned char* rec = record(p, slot0, h);
-  Ring<true, STRIPS> ring{p, sm, rec, step, nch * 3, lane, threadIdx.x == 0};
-  ring.start();
-  float s[4][4];
-  load_state(p.s_in == nullptr ? nullptr : p.s_in + sblk, v0, i0, lane, s);
-  for (int32_t c = 0; c < nch; ++c, rec += step) {
-    const int tc = static_cast<int>(len - static_cast<int64_t>(c) * kC < kC ? len - static_cast<int64_t>(c) * kC : kC);
-    float2 rt[2][2];  // Rt^T of this warp's tokens, needed after the first product
-    {
-      const float* const src = reinterpret_cast<const float*>(rec + Record::kRt) + (v0 + (lane >> 2)) * kC + t0 + 2 * (lane & 3);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  Waiter w;
+  if (warp < kComputeWarps) {
+    const int part = warp >> 2;
+    float s[kPartK];
+    load_state(p.s_in == nullptr ? nullptr : p.s_in + sblk, v, part, s);
+    for (int64_t c = 0; c < chunks; ++c, rec += step) {
+      const int b = static_cast<int>(c & 1);
+      const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
+      // ---- the state as a pair
+      const float sc_s = pow2_scale(quarter_max(sm, 0, abs_max(s), part, quarter));
+      fence_after_sync();
+      write_pair<kK, true>(mine + Col::kState, nullptr, 0, v, part * kPartK, s, sc_s);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sm.state, lane);
+      if (p.save) write_pair<kK, false>(0, rec + Record::kS, kV * kK * 2, v, part * kPartK, s, sc_s);
+      float r[kPartT];
+      {
+        const float4* const rt = reinterpret_cast<const float4*>(rec + Record::kRt) + part * (kPartT / 4) * kV + v;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        rt[j][0] = *reinterpret_cast<const float2*>(src + j * 8);
-        rt[j][1] = *reinterpret_cast<const float2*>(src + 8 * kC + j * 8);
+        for (int j = 0; j < kPartT / 4; ++j) {
+          const float4 x = rt[j * kV];
+          r[4 * j] = x.x;
+          r[4 * j + 1] = x.y;
+          r[4 * j + 2] = x.z;
+          r[4 * j + 3] = x.w;
+        }
+      }
+      w.warp(&sm.full_hdr[b], c >> 1);
+      // ---- r = Rt - S0 Wr, U = beta r
+      w.warp(&sm.first[b], c >> 1);
+      fence_after_sync();
+      {
+        const float f = -pow2_inv(sc_s) * pow2_inv(hdr[Record::kScWr]);
+        uint32_t x[kPartT];
+        tmem_ld(mine + Col::kX + part * kPartT, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < kPartT; ++j) r[j] = fmaf(__uint_as_float(x[j]), f, r[j]);
+      }
+      const float* const beta = hdr + Record::kBeta + part * kPartT;
+      const float sc_u = pow2_scale(quarter_max(sm, 1, abs_max(r, beta), part, quarter));
+      fence_after_sync();
+      write_pair<kC, true>(mine + Col::kU, nullptr, 0, v, part * kPartT, r, sc_u, beta);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sm.rows, lane);
+      if (part == 0 && lane == 0) {
+        sm.sc_s[b][quarter] = sc_s;
+        sm.sc_u[b][quarter] = sc_u;
+      }
+      warp_arrive(&sm.scales[b], lane);
+      if (p.save) {
+        const float sc_r = pow2_scale(quarter_max(sm, 2, abs_max(r), part, quarter));
+        write_pair<kC, false>(0, rec + Record::kR, Record::kPlane, v, part * kPartT, r, sc_r);
+        if (part == 0 && lane == 0) {
+          float* const sc = reinterpret_cast<float*>(rec + Record::kSc);
+          sc[Record::kScS + quarter] = sc_s;
+          sc[Record::kScR + quarter] = sc_r;
+        }
+      }
+      // ---- S1 = Diag(exp(Gamma_C)) S0 + Ke^T U
+      w.warp(&sm.last[b], c >> 1);
+      fence_after_sync();
+      add_product<true>(mine + Col::kDelta + part * kPartK, hdr + Record::kDecay + part * kPartK, pow2_inv(sc_u) * pow2_inv(hdr[Record::kScKe]), s);
+      fence_before_sync();
+      warp_arrive(&sm.empty_hdr[b], lane);
+    }
+    if (!w.ok) {
+      if (lane == 0) set_error(p);
+    } else if (p.s_out != nullptr) {
+      store_state(p.s_out + sblk, v, part, s);
+    }
+  } else if (warp == kComputeWarps) {
+    if (lane == 0) chain_copies<true>(sm, w, rec, step, chunks, outputs);
+    __syncwarp();
+  } else if (warp == kComputeWarps + 1) {
+    for (int64_t c = 0; c < chunks; ++c) {
+      const int b = static_cast<int>(c & 1);
+      w.warp(&sm.full_wr[b], c >> 1);
+      w.warp(&sm.state, c);
+      fence_after_sync();
+      umma_pairs<kC, kK, kC, false>(tmem + Col::kX, tmem + Col::kState, smem_addr(sm.wr[b]), Record::kPlane);
+      umma_commit(&sm.first[b]);
+      if (outputs) {
+        w.warp(&sm.full_qt, c);
+        if (c > 0) w.warp(&sm.out_free, c - 1);
+        fence_after_sync();
+        umma_pairs<kC, kK, kC, false>(tmem + Col::kO1, tmem + Col::kState, smem_addr(sm.qt), Record::kPlane);
+        umma_commit(&sm.with_qt);
+      }
+      w.warp(&sm.full_ke[b], c >> 1);
+      w.warp(&sm.rows, c);
+      fence_after_sync();
+      umma_pairs<kK, kC, kC, true>(tmem + Col::kDelta, tmem + Col::kU, smem_addr(sm.ke[b]), Record::kPlane);
+      umma_commit(&sm.last[b]);
+      if (outputs) {
+        w.warp(&sm.full_p, c);
+        umma_pairs<kC, kC, kC, false>(tmem + Col::kO2, tmem + Col::kU, smem_addr(sm.p), kC * kC * 2);
+        umma_commit(&sm.out_done);
       }
     }
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max4(s[j], m);
-    const float sc_s = pow2_scale(warp_max(m));
-    uint32_t ah[2][4], al[2][4];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      frag_a(s[2 * kk], s[2 * kk + 1], sc_s, ah[kk], al[kk]);
-      st.s[quarter][kk][lane] = vec(ah[kk]);
+    if (chunks > 0) {
+      umma_commit(&sm.end);
+      mbar_wait(&sm.end, 0);
     }
-    // ---- the sums of S0^T Wr^T over this warp's channels, to the warps of their tokens
-    float x[8][4];
-    const unsigned char* const wr = ring.wait();
-    const float* const hdr = reinterpret_cast<const float*>(wr);
-    const float sc_qt = hdr[Record::kScQt], sc_p = hdr[Record::kScP], sc_ke = hdr[Record::kScKe];
-    channel_sums(smem_addr(wr) + Record::kHdr, i0, lane, ah, al, pow2_inv(sc_s) * pow2_inv(hdr[Record::kScWr]), x);
-    put_sums(st.part, quarter, lane, x);
-    if (lane == 0) sc.s[quarter] = sc_s;
-    if (p.save) {
+    __syncwarp();
+    if (!w.ok && lane == 0) set_error(p);
+  } else if (outputs) {
+    // ---- O = scale (Qt S0 + P U): lanes are value columns; neighbours trade a token each, so that a thread stores two values
+    for (int64_t c = 0; c < chunks; ++c) {
+      const int b = static_cast<int>(c & 1);
+      const int tc = static_cast<int>(len - c * kC < kC ? len - c * kC : kC);
+      const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
+      w.warp(&sm.full_hdr[b], c >> 1);
+      w.warp(&sm.scales[b], c >> 1);
+      const float f1 = pow2_inv(sm.sc_s[b][quarter]) * pow2_inv(hdr[Record::kScQt]) * p.scale;
+      const float f2 = pow2_inv(sm.sc_u[b][quarter]) * pow2_inv(hdr[Record::kScP]) * p.scale;
+      warp_arrive(&sm.empty_hdr[b], lane);
+      w.warp(&sm.out_done, c);
+      fence_after_sync();
+      uint32_t y[kC / 2];  // two values of one token each
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
-        store_frag<128>(rec + Record::kS, kV * kK * 2, v0, i0 + kk * 16, lane, ah[kk], al[kk]);
-    }
-    float2 beta[2];
+      for (int g = 0; g < 4; ++g) {
+        uint32_t a[16], x[16];
+        tmem_ld(mine + Col::kO1 + g * 16, a);
+        tmem_ld(mine + Col::kO2 + g * 16, x);
+        tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) beta[j] = *reinterpret_cast<const float2*>(hdr + Record::kBeta + t0 + j * 8 + 2 * (lane & 3));
-    ring.release();
-    strip_sync(strip);
-    // ---- r^T and U^T of this warp's tokens
-    float r[2][4];
-    take_sums(st.part, quarter, lane, x, r);
-    float mr = 0.f, mu = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      r[j][0] = rt[j][0].x - r[j][0];
-      r[j][1] = rt[j][0].y - r[j][1];
-      r[j][2] = rt[j][1].x - r[j][2];
-      r[j][3] = rt[j][1].y - r[j][3];
-      mr = max4(r[j], mr);
-    }
-    float u[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[j][e] = r[j][e] * (e & 1 ? beta[j].y : beta[j].x);
-      mu = max4(u[j], mu);
-    }
-    {
-      const float sc_u = pow2_scale(warp_max(mu));
-      uint32_t uh[4], ul[4];
-      frag_a(u[0], u[1], sc_u, uh, ul);
-      st.u[quarter][0][lane] = vec(uh);
-      st.u[quarter][1][lane] = vec(ul);
-      if (lane == 0) sc.u[quarter] = sc_u;
-    }
-    // ---- O^T = scale (S0^T Qt^T + U^T P^T), this warp's tokens (one fp16 product: it is rounded to bf16)
-    const uint32_t a_p = smem_addr(ring.wait()), a_qt = a_p + kC * kC * 2;
-    float o[2][4] = {};
-#pragma unroll
-    for (int qd = 0; qd < 4; ++qd) {
-      float y[2][4] = {};
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        uint32_t a[4], b[4];
-        unvec(st.s[qd][kk][lane], a);
-        load_b<128>(a_qt, qd * 32 + kk * 16, t0, lane, b);
-        mma_pair(y[0], y[1], a, b);
+        for (int j = 0; j < 16; j += 2) {
+          const float o0 = fmaf(__uint_as_float(a[j]), f1, __uint_as_float(x[j]) * f2);
+          const float o1 = fmaf(__uint_as_float(a[j + 1]), f1, __uint_as_float(x[j + 1]) * f2);
+          const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? o0 : o1, 1);
+          const __nv_bfloat162 z = lane & 1 ? __floats2bfloat162_rn(got, o1) : __floats2bfloat162_rn(o0, got);
+          y[g * 8 + (j >> 1)] = *reinterpret_cast<const uint32_t*>(&z);
+        }
       }
-      const float f = pow2_inv(sc.s[qd]) * pow2_inv(sc_qt);
+      fence_before_sync();
+      warp_arrive(&sm.out_free, lane);  // ahead of the stores: the next chunk's products wait for it
+      __nv_bfloat16* const out = p.out + (start + c * kC) * p.out_ts + h * kV + (v & ~1);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] = fmaf(y[j][e], f, o[j][e]);
-    }
-    strip_sync(strip);
-    // ---- S1^T = S0^T Diag(exp(Gamma_C)) + U^T Ke
-    const bool out = p.out != nullptr;
-    uint32_t uh[4][4], ul[4][4];
-    float fu[4];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      unvec(st.u[kk][0][lane], uh[kk]);
-      unvec(st.u[kk][1][lane], ul[kk]);
-      fu[kk] = pow2_inv(sc.u[kk]);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      if (kk <= quarter) {
-        float y[2][4] = {};
-        uint32_t b[4];
-        load_b<64>(a_p, kk * 16, t0, lane, b);
-        mma_pair(y[0], y[1], uh[kk], b);
-        const float f = fu[kk] * pow2_inv(sc_p);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][e] = fmaf(y[j][e], f, o[j][e]);
-      }
-    ring.release();
-    const unsigned char* const ke = ring.wait();
-    decay_state(reinterpret_cast<const float*>(ke) + Record::kDecay + i0, lane, s);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      add_outer<true>(smem_addr(ke) + Record::kHdr, kk * 16, i0, lane, uh[kk], ul[kk], fu[kk] * pow2_inv(sc_ke), s);
-    ring.release();
-    if (out) store_out16(p.out + (start + static_cast<int64_t>(c) * kC) * p.out_ts + h * kV + v0, p.out_ts, t0, tc, lane, o[0], o[1], p.scale);
-    if (p.save) {
-      const float sc_r = pow2_scale(warp_max(mr));
-      uint32_t rh[4], rl[4];
-      frag_a(r[0], r[1], sc_r, rh, rl);
-      store_frag<64>(rec + Record::kR, Record::kPlane, v0, t0, lane, rh, rl);
-      if (lane == 0) {
-        float* const scales = reinterpret_cast<float*>(rec + Record::kSc);
-        scales[Record::kScS + group * 4 + quarter] = sc_s;
-        scales[Record::kScR + group * 4 + quarter] = sc_r;
+      for (int j = 0; j < kC / 2; ++j) {
+        const int t = 2 * j + (lane & 1);
+        if (t < tc) *reinterpret_cast<uint32_t*>(out + t * p.out_ts) = y[j];
       }
     }
+    if (!w.ok && lane == 0) set_error(p);
   }
-  if (!ring.ok) {  // a copy never came: the state is not written
-    ring.abandon();
-    return;
-  }
-  if (p.s_out != nullptr) store_state(p.s_out + sblk, v0, i0, lane, s);
+  chain_exit(sm);
 }
 
 // ---------------------------------------------------------------- backward
-template <int STRIPS>
-__global__ void __launch_bounds__(STRIPS * 128, 1) kda_scan_backward_kernel(const __grid_constant__ ScanParams p) {
+// dS1 as a pair and, once its product is done, the product with Wr share columns.
+struct BackwardColumns {
+  static constexpr uint32_t kState = 0, kDelta = 0, kDO = 128, kU = 160, kX1 = 224, kX2 = 288, kExtra = 352;
+};
+constexpr int kBackwardThreads = (kComputeWarps + 2) * 32;
+
+__global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(const __grid_constant__ ScanParams p) {
+  using Col = BackwardColumns;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  auto& sm = *reinterpret_cast<typename ChainCfg<STRIPS>::Backward*>(smem_raw);
-  constexpr int kTiles = 8 / STRIPS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, strip = warp >> 2, quarter = warp & 3;
-  const int64_t unit = blockIdx.x / kTiles;
-  const int group = static_cast<int>(blockIdx.x - unit * kTiles) * STRIPS + strip;
-  const int64_t n = unit / p.HV, h = unit - n * p.HV;
+  ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
+  const int64_t n = blockIdx.x / p.HV, h = blockIdx.x - n * p.HV;
   int64_t start, len;
   seq_range(p, n, start, len);
-  const int32_t nch = static_cast<int32_t>((len + kC - 1) / kC);
-  const int64_t slot0 = first_slot(p, n, start);
-  const int v0 = group * 16, i0 = quarter * 32, t0 = quarter * 16;
-  chain_init(sm, ChainCfg<STRIPS>::kRing, STRIPS * 4);
-  StripBack& st = sm.strip[strip];
+  const int64_t chunks = (len + kC - 1) / kC, slot0 = first_slot(p, n, start);
+  chain_init(sm, kComputeWarps);
   const int64_t sblk = (n * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
-  unsigned char* rec = record(p, slot0 + (nch > 0 ? nch - 1 : 0), h);
-  Ring<false, STRIPS> ring{p, sm, rec, -step, nch * 4, lane, threadIdx.x == 0};
-  ring.start();
-  float s[4][4];
-  load_state(p.d_final == nullptr ? nullptr : p.d_final + sblk, v0, i0, lane, s);
-
-  // dO, one 16-byte piece a thread (this warp: its 16 tokens), exact in fp16 after scaling: bf16 has 8 bits
-  const int dt = t0 + (lane >> 1), dh = lane & 1;
-  auto fetch = [&](int32_t c) {
-    const int64_t t = static_cast<int64_t>(c) * kC + dt;
-    return c >= 0 && t < len ? *reinterpret_cast<const uint4*>(p.d_out + (start + t) * p.d_out_ts + h * kV + v0 + dh * 8)
-                             : make_uint4(0, 0, 0, 0);
-  };
-  auto put_do = [&](uint4 raw, int buf) {
-    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float m = 0.f;
+  unsigned char* rec = record(p, slot0 + (chunks > 0 ? chunks - 1 : 0), h);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  Waiter w;
+  // i counts the chunks walked: i = 0 is the last chunk, and barriers' phases go by i
+  if (warp < kComputeWarps) {
+    const int part = warp >> 2;
+    float s[kPartK];
+    load_state(p.d_final == nullptr ? nullptr : p.d_final + sblk, v, part, s);
+    // dO^T: this thread's value column and tokens, exact in fp16 after scaling (bf16 has 8 bits)
+    unsigned short raw[kPartT];  // as loaded: packing them would wait for the loads
+    int64_t raw_t0 = 0;
+    auto fetch = [&](int64_t c) {
+      raw_t0 = c * kC + part * kPartT;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-    const float sc = pow2_scale(warp_max(m));
+      for (int j = 0; j < kPartT; ++j)
+        raw[j] = *reinterpret_cast<const unsigned short*>(p.d_out + (start + (raw_t0 + j < len ? raw_t0 + j : len - 1)) * p.d_out_ts + h * kV + v);
+    };
+    float sc_do = 1.f;
+    auto put = [&]() {
+      float y[kPartT], m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc, __uint_as_float(w[e] & 0xffff0000u) * sc));
-    *reinterpret_cast<uint4*>(st.dO[buf] + dt * kDoPitch + dh * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (lane == 0) st.sc_do[buf][quarter] = sc;
-  };
-  put_do(fetch(nch - 1), (nch - 1) & 1);
-  strip_sync(strip);
-
-  for (int32_t c = nch - 1; c >= 0; --c, rec -= step) {
-    const uint4 next_do = fetch(c - 1);
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max4(s[j], m);
-    const float sc_s = pow2_scale(warp_max(m));
-    uint32_t ah[2][4], al[2][4];
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      frag_a(s[2 * kk], s[2 * kk + 1], sc_s, ah[kk], al[kk]);
-      store_frag<128>(rec + Record::kDS, kV * kK * 2, v0, i0 + kk * 16, lane, ah[kk], al[kk]);
-    }
-    // ---- the sums of dS1^T Ke^T over this warp's channels, to the warps of their tokens
-    float x[8][4];
-    const unsigned char* const ke = ring.wait();
-    const float* const hdr = reinterpret_cast<const float*>(ke);
-    const float sc_p = hdr[Record::kScP], sc_qt = hdr[Record::kScQt], sc_wr = hdr[Record::kScWr];
-    channel_sums(smem_addr(ke) + Record::kHdr, i0, lane, ah, al, pow2_inv(sc_s) * pow2_inv(hdr[Record::kScKe]), x);
-    put_sums(st.part, quarter, lane, x);
-    float2 beta[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) beta[j] = *reinterpret_cast<const float2*>(hdr + Record::kBeta + t0 + j * 8 + 2 * (lane & 3));
-    ring.release();
-    // ---- scale dO^T P of this warp's tokens
-    uint32_t da[4][4];
-    float fd[4];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      ldsm4t(smem_addr(st.dO[c & 1]) + (kk * 16 + (lane & 7) + (lane >> 4) * 8) * kDoPitch + ((lane >> 3) & 1) * 16, da[kk]);
-      fd[kk] = pow2_inv(st.sc_do[c & 1][kk]) * p.scale;
-    }
-    const uint32_t a_p = smem_addr(ring.wait());
-    float du[2][4] = {};
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)  // t sub-block; P[t][s] is zero for s > t
-      if (kk >= quarter) {
-        uint32_t bh[4], bl[4];
-        load_b_t<64>(a_p, kk * 16, t0, lane, bh);
-        load_b_t<64>(a_p + kC * kC * 2, kk * 16, t0, lane, bl);
-        float y[2][4] = {};
-        mma_pair(y[0], y[1], da[kk], bl);
-        mma_pair(y[0], y[1], da[kk], bh);
-        const float f = fd[kk] * pow2_inv(sc_p);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) du[j][e] = fmaf(y[j][e], f, du[j][e]);
+      for (int j = 0; j < kPartT; ++j) {
+        y[j] = raw_t0 + j < len ? __uint_as_float(static_cast<uint32_t>(raw[j]) << 16) : 0.f;
+        m = fmaxf(m, fabsf(y[j]));
       }
-    ring.release();
-    strip_sync(strip);
-    // ---- dU^T of this warp's tokens; -beta dU^T to the strip
-    float own[2][4], m2 = 0.f;
-    take_sums(st.part, quarter, lane, x, own);
-    m = 0.f;
+      sc_do = pow2_scale(quarter_max(sm, 2, m, part, quarter));
+      uint32_t x[kPartT / 2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kPartT / 2; ++j)
+        x[j] = as_u32(__floats2half2_rn(y[2 * j] * sc_do, y[2 * j + 1] * sc_do));
+      fence_after_sync();
+      tmem_st(mine + Col::kDO + part * (kPartT / 2), x);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sm.d_out, lane);
+    };
+    if (chunks > 0) {
+      fetch(chunks - 1);
+      put();
+    }
+    for (int64_t i = 0; i < chunks; ++i, rec -= step) {
+      const int b = static_cast<int>(i & 1);
+      const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
+      // ---- dS1 as a pair
+      const float sc_s = pow2_scale(quarter_max(sm, 0, abs_max(s), part, quarter));
+      fence_after_sync();
+      write_pair<kK, true>(mine + Col::kState, nullptr, 0, v, part * kPartK, s, sc_s);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sm.state, lane);
+      write_pair<kK, false>(0, rec + Record::kDS, kV * kK * 2, v, part * kPartK, s, sc_s);
+      if (i + 1 < chunks) fetch(chunks - 2 - i);
+      // ---- decay, and scale Qt^T dO
+      w.warp(&sm.full_hdr[b], i >> 1);
+      w.warp(&sm.with_qt, i);
+      fence_after_sync();
+      const float f_do = pow2_inv(sc_do) * p.scale;
+      add_product<true>(mine + Col::kExtra + part * kPartK, hdr + Record::kDecay + part * kPartK, f_do * pow2_inv(hdr[Record::kScQt]), s);
+      // ---- dU = scale P^T dO + Ke dS1
+      w.warp(&sm.first[b], i >> 1);
+      fence_after_sync();
+      float du[kPartT];
+      {
+        const float f1 = f_do * pow2_inv(hdr[Record::kScP]), f2 = pow2_inv(sc_s) * pow2_inv(hdr[Record::kScKe]);
+        uint32_t x[kPartT], y[kPartT];
+        tmem_ld(mine + Col::kX1 + part * kPartT, x);
+        tmem_ld(mine + Col::kX2 + part * kPartT, y);
+        tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        du[j][e] += own[j][e];
-        own[j][e] = -du[j][e] * (e & 1 ? beta[j].y : beta[j].x);
+        for (int j = 0; j < kPartT; ++j) du[j] = fmaf(__uint_as_float(x[j]), f1, __uint_as_float(y[j]) * f2);
       }
-      m = max4(du[j], m);
-      m2 = max4(own[j], m2);
-    }
-    {
-      const float sc_u = pow2_scale(warp_max(m2));
-      uint32_t uh[4], ul[4];
-      frag_a(own[0], own[1], sc_u, uh, ul);
-      st.u[quarter][0][lane] = vec(uh);
-      st.u[quarter][1][lane] = vec(ul);
-      if (lane == 0) st.sc_u[quarter] = sc_u;
-    }
-    put_do(next_do, (c & 1) ^ 1);
-    // ---- dS0^T = dS1^T Diag(exp(Gamma_C)) + scale dO^T Qt - (beta dU)^T Wr
-    const unsigned char* const qt = ring.wait();
-    decay_state(reinterpret_cast<const float*>(qt) + Record::kDecay + i0, lane, s);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-      add_outer<false>(smem_addr(qt) + Record::kHdr, kk * 16, i0, lane, da[kk], da[kk], fd[kk] * pow2_inv(sc_qt), s);
-    ring.release();
-    strip_sync(strip);
-    const uint32_t a_wr = smem_addr(ring.wait());
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t uh[4], ul[4];
-      unvec(st.u[kk][0][lane], uh);
-      unvec(st.u[kk][1][lane], ul);
-      add_outer<true>(a_wr, kk * 16, i0, lane, uh, ul, pow2_inv(st.sc_u[kk]) * pow2_inv(sc_wr), s);
-    }
-    ring.release();
-    {
-      const float sc_du = pow2_scale(warp_max(m));
-      uint32_t uh[4], ul[4];
-      frag_a(du[0], du[1], sc_du, uh, ul);
-      store_frag<64>(rec + Record::kDU, Record::kPlane, v0, t0, lane, uh, ul);
-      if (lane == 0) {
-        float* const scales = reinterpret_cast<float*>(rec + Record::kSc);
-        scales[Record::kScDS + group * 4 + quarter] = sc_s;
-        scales[Record::kScDU + group * 4 + quarter] = sc_du;
+      const float* const beta = hdr + Record::kBeta + part * kPartT;
+      const float f_wr = -pow2_inv(hdr[Record::kScWr]);
+      const float sc_u = pow2_scale(quarter_max(sm, 1, abs_max(du, beta), part, quarter));
+      fence_after_sync();
+      write_pair<kC, true>(mine + Col::kU, nullptr, 0, v, part * kPartT, du, sc_u, beta);
+      warp_arrive(&sm.empty_hdr[b], lane);
+      tmem_wait_st();
+      fence_before_sync();
+      warp_arrive(&sm.rows, lane);
+      if (i + 1 < chunks) put();  // the products of this chunk's dO are complete
+      {
+        const float sc_du = pow2_scale(quarter_max(sm, 3, abs_max(du), part, quarter));
+        write_pair<kC, false>(0, rec + Record::kDU, Record::kPlane, v, part * kPartT, du, sc_du);
+        if (part == 0 && lane == 0) {
+          float* const sc = reinterpret_cast<float*>(rec + Record::kSc);
+          sc[Record::kScDS + quarter] = sc_s;
+          sc[Record::kScDU + quarter] = sc_du;
+        }
       }
+      // ---- dS0 = ... - Wr^T (beta dU)
+      w.warp(&sm.last[b], i >> 1);
+      fence_after_sync();
+      add_product<false>(mine + Col::kDelta + part * kPartK, nullptr, pow2_inv(sc_u) * f_wr, s);
+      fence_before_sync();
     }
+    if (!w.ok) {
+      if (lane == 0) set_error(p);
+    } else if (p.d_init != nullptr) {
+      store_state(p.d_init + sblk, v, part, s);
+    }
+  } else if (warp == kComputeWarps) {
+    if (lane == 0) chain_copies<false>(sm, w, rec, -step, chunks, true);
+    __syncwarp();
+  } else {
+    auto d_out_products = [&](int64_t i) {
+      w.warp(&sm.full_qt, i);
+      w.warp(&sm.d_out, i);
+      fence_after_sync();
+      umma_pairs<kK, kC, kC, true, true>(tmem + Col::kExtra, tmem + Col::kDO, smem_addr(sm.qt), Record::kPlane);
+      umma_commit(&sm.with_qt);
+      w.warp(&sm.full_p, i);
+      umma_pairs<kC, kC, kC, true, true>(tmem + Col::kX1, tmem + Col::kDO, smem_addr(sm.p), kC * kC * 2);
+    };
+    if (chunks > 0) d_out_products(0);
+    for (int64_t i = 0; i < chunks; ++i) {
+      const int b = static_cast<int>(i & 1);
+      w.warp(&sm.full_ke[b], i >> 1);
+      w.warp(&sm.state, i);
+      fence_after_sync();
+      umma_pairs<kC, kK, kC, false>(tmem + Col::kX2, tmem + Col::kState, smem_addr(sm.ke[b]), Record::kPlane);
+      umma_commit(&sm.first[b]);
+      w.warp(&sm.full_wr[b], i >> 1);
+      w.warp(&sm.rows, i);
+      fence_after_sync();
+      umma_pairs<kK, kC, kC, true>(tmem + Col::kDelta, tmem + Col::kU, smem_addr(sm.wr[b]), Record::kPlane);
+      umma_commit(&sm.last[b]);
+      if (i + 1 < chunks) d_out_products(i + 1);
+    }
+    if (chunks > 0) {
+      umma_commit(&sm.end);
+      mbar_wait(&sm.end, 0);
+    }
+    __syncwarp();
+    if (!w.ok && lane == 0) set_error(p);
   }
-  if (!ring.ok) {
-    ring.abandon();
-    return;
-  }
-  if (p.d_init != nullptr) store_state(p.d_init + sblk, v0, i0, lane, s);
+  chain_exit(sm);
 }
 
 }  // namespace kdal

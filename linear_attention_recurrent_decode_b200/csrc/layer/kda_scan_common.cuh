@@ -45,22 +45,22 @@ struct Record {
   static constexpr int kScWr = 192, kScKe = 193, kScQt = 194, kScP = 195, kScY = 196;
   // byte offsets
   static constexpr int kHdr = 1024;
-  static constexpr int kPlane = kC * kK * 2;       // 16 KB: a [64][128] (or [128][64]) plane
-  static constexpr int kP = kHdr;                  // P   [t][s] hi, lo (8 KB each)
-  static constexpr int kQt = kP + kC * kC * 4;     // Qt  [t][i] hi, lo
-  static constexpr int kWr = kQt + 2 * kPlane;     // Wr  [t][i] hi, lo
-  static constexpr int kKe = kWr + 2 * kPlane;     // Ke  [t][i] hi, lo
-  static constexpr int kRt = kKe + 2 * kPlane;     // Rt^T [v][t] fp32
+  static constexpr int kPlane = kC * kK * 2;       // 16 KB: a plane of 64 x 128 elements
+  // pairs hi, lo of Core tiles; [rows][columns]
+  static constexpr int kP = kHdr;                  // P   [t][s], 8 KB a plane
+  static constexpr int kQt = kP + kC * kC * 4;     // Qt  [t][i]
+  static constexpr int kWr = kQt + 2 * kPlane;     // Wr  [t][i]
+  static constexpr int kKe = kWr + 2 * kPlane;     // Ke  [t][i]
+  static constexpr int kRt = kKe + 2 * kPlane;     // Rt^T fp32, [t / 4][v][4]
   static constexpr int64_t kForward = kRt + kV * kC * 4;
-  static constexpr int kY = static_cast<int>(kForward);  // beta_t Y [t][s] hi, lo
-  static constexpr int kS = kY + kC * kC * 4;      // S0^T [v][i] hi, lo (32 KB each)
-  static constexpr int kR = kS + kV * kK * 4;      // r^T  [v][t] hi, lo
-  static constexpr int kDS = kR + 2 * kPlane;      // dS1^T [v][i] hi, lo
-  static constexpr int kDU = kDS + kV * kK * 4;    // dU^T [v][t] hi, lo
-  // Scales of the last four, floats [8][4] each: per 16 value columns and per
-  // quarter of the channels (S, dS) or of the tokens (r, dU).
+  static constexpr int kY = static_cast<int>(kForward);  // beta_t Y [t][s]
+  static constexpr int kS = kY + kC * kC * 4;      // S0^T [v][i], 32 KB a plane
+  static constexpr int kR = kS + kV * kK * 4;      // r^T  [v][t]
+  static constexpr int kDS = kR + 2 * kPlane;      // dS1^T [v][i]
+  static constexpr int kDU = kDS + kV * kK * 4;    // dU^T [v][t]
+  // Scales of the last four, floats [4] each: per 32 value columns.
   static constexpr int kSc = kDU + 2 * kPlane;
-  static constexpr int kScS = 0, kScR = 32, kScDS = 64, kScDU = 96, kScBytes = 512;
+  static constexpr int kScS = 0, kScR = 4, kScDS = 8, kScDU = 12, kScBytes = 64;
   static constexpr int64_t kTraining = kSc + kScBytes;
 };
 constexpr int64_t kWsHeader = 256;  // word 0: the error word

@@ -20,7 +20,7 @@
 // 1 (see SubFactors), and no product is formed twice.
 #pragma once
 
-#include "kda_scan_chain.cuh"
+#include "kda_scan_common.cuh"
 
 namespace kdal {
 
@@ -55,6 +55,33 @@ struct GradPairs {  // over s0 .. dO once those are dead
 static_assert(sizeof(GradPairs) <= offsetof(GradSmem, emu), "the factors fit over the operand tiles");
 static_assert(2 * sizeof(float) * kC * kDP <= kV * kK * 4, "dP and dA fit over S0");
 static_assert(sizeof(GradSmem) <= 232448, "shared memory of an SM");
+
+// A 16 x 16 A-fragment pair to rows v0.. of a tile, columns c0..
+template <class L>
+__device__ __forceinline__ void store_frag(unsigned char* tile, int plane, int v0, int c0, int lane, const uint32_t (&ah)[4],
+                                           const uint32_t (&al)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t off = L::off(v0 + (lane >> 2) + (j & 1) * 8, c0 + (j >> 1) * 8 + 2 * (lane & 3));
+    *reinterpret_cast<uint32_t*>(tile + off) = ah[j];
+    *reinterpret_cast<uint32_t*>(tile + plane + off) = al[j];
+  }
+}
+// [16 value columns x 16 tokens] of an accumulator pair, rounded to bf16, to rows (token, 16 values).
+__device__ __forceinline__ void store_out16(__nv_bfloat16* out, int64_t ts, int t0, int tc, int lane, const float (&c0)[4],
+                                            const float (&c1)[4], float f) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float(&c)[4] = j ? c1 : c0;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(c[0] * f, c[1] * f), hi = __floats2bfloat162_rn(c[2] * f, c[3] * f);
+    const uint32_t a = transpose8(*reinterpret_cast<const uint32_t*>(&lo)), b = transpose8(*reinterpret_cast<const uint32_t*>(&hi));
+    const int t = t0 + j * 8 + (lane >> 2);
+    if (t < tc) {
+      *reinterpret_cast<uint32_t*>(out + t * ts + 2 * (lane & 3)) = a;
+      *reinterpret_cast<uint32_t*>(out + t * ts + 8 + 2 * (lane & 3)) = b;
+    }
+  }
+}
 
 // Direct sums inside sub-block b (its decays are out of the factors' range):
 // one accumulator element (t, i), pairs from the log-decays between them.
@@ -166,7 +193,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc, __uint_as_float(w[e] & 0xffff0000u) * sc));
-      *reinterpret_cast<uint4*>(sm.dO + off128(t, pc * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(sm.dO + Rows128::off(t, pc * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   const float sc_do = pow2_scale(__uint_as_float(sm.mx_do));
@@ -190,23 +217,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       uint32_t dh[4], dl[4];
       for (int kk = 3; kk >= nb; --kk) {     // s sub-block; Y[s][t] is zero for t >= s
         uint32_t bh[4], bl[4];
-        load_a<64>(a_ds, v0, kk * 16, lane, dh);
-        load_a<64>(a_ds + Record::kPlane, v0, kk * 16, lane, dl);
-        load_b_t<64>(a_y, kk * 16, nb * 16, lane, bh);
-        load_b_t<64>(a_y + kC * kC * 2, kk * 16, nb * 16, lane, bl);
+        load_a<Core<kV>>(a_ds, v0, kk * 16, lane, dh);
+        load_a<Core<kV>>(a_ds + Record::kPlane, v0, kk * 16, lane, dl);
+        load_b_t<Core<kC>>(a_y, kk * 16, nb * 16, lane, bh);
+        load_b_t<Core<kC>>(a_y + kC * kC * 2, kk * 16, nb * 16, lane, bl);
         float x[2][4] = {};
         mma_pair(x[0], x[1], dh, bl);
         mma_pair(x[0], x[1], dl, bh);
         mma_pair(x[0], x[1], dh, bh);
-        const float f = pow2_inv(sm.sc[Record::kScDU + grp * 4 + kk]) * pow2_inv(sm.hdr[Record::kScY]);
+        const float f = pow2_inv(sm.sc[Record::kScDU + (grp >> 1)]) * pow2_inv(sm.hdr[Record::kScY]);
         add_scaled(acc[0], x[0], f);
         add_scaled(acc[1], x[1], f);
       }
       // dh, dl now hold the sub-block's own dU
-      const float inv = pow2_inv(sm.sc[Record::kScDU + grp * 4 + nb]), inv_r = pow2_inv(sm.sc[Record::kScR + grp * 4 + nb]);
+      const float inv = pow2_inv(sm.sc[Record::kScDU + (grp >> 1)]), inv_r = pow2_inv(sm.sc[Record::kScR + (grp >> 1)]);
       uint32_t rh[4], rl[4];
-      load_a<64>(a_r, v0, nb * 16, lane, rh);
-      load_a<64>(a_r + Record::kPlane, v0, nb * 16, lane, rl);
+      load_a<Core<kV>>(a_r, v0, nb * 16, lane, rh);
+      load_a<Core<kV>>(a_r + Record::kPlane, v0, nb * 16, lane, rl);
       float m = 0.f, db[4] = {0.f, 0.f, 0.f, 0.f};  // tokens nb 16 + 2 (lane & 3) + {0, 1, 8, 9}
 #pragma unroll
       for (int j = 0; j < 4; ++j) {  // fragment register j: rows + (j & 1) 8, columns + (j >> 1) 8
@@ -229,7 +256,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       const float sc = pow2_scale(warp_max(m));
       if (lane == 0) sm.sc_dr[grp][nb] = sc;
       frag_a(acc[0], acc[1], sc, dh, dl);
-      store_frag<64>(sm.dr, Record::kPlane, v0, nb * 16, lane, dh, dl);
+      store_frag<Core<kV>>(sm.dr, Record::kPlane, v0, nb * 16, lane, dh, dl);
       store_out16(dv, p.dv_ts, nb * 16, tc, lane, acc[0], acc[1], 1.f);
     }
   }
@@ -247,21 +274,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   }
 
   // ---- 2. dQt = scale dO S0^T and dKt = -dR S0^T: warp = 16 tokens x 32 channels, a partial sum per 16 value columns
-  const int I = warp & 3, i4 = warp >> 2, i0 = i4 * 32;
+  const int I = warp & 3, i0 = (warp >> 2) * 32;
   float dq[4][4] = {}, dkr[4][4] = {};
 #pragma unroll 2
   for (int g = 0; g < 8; ++g) {
     uint32_t a[4], ah[4], al[4];
-    load_a<128>(a_do, I * 16, g * 16, lane, a);
-    load_a_t<64>(a_dr, I * 16, g * 16, lane, ah);
-    load_a_t<64>(a_dr + Record::kPlane, I * 16, g * 16, lane, al);
-    const float inv_s = pow2_inv(sm.sc[Record::kScS + g * 4 + i4]);
+    load_a<Rows128>(a_do, I * 16, g * 16, lane, a);
+    load_a_t<Core<kV>>(a_dr, I * 16, g * 16, lane, ah);
+    load_a_t<Core<kV>>(a_dr + Record::kPlane, I * 16, g * 16, lane, al);
+    const float inv_s = pow2_inv(sm.sc[Record::kScS + (g >> 1)]);
     const float fq = inv_s * (pow2_inv(sc_do) * p.scale), fk = -inv_s * pow2_inv(sm.sc_dr[g][I]);
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
       uint32_t bh[4], bl[4];
-      load_b_t<128>(a_s0, g * 16, i0 + nb * 16, lane, bh);
-      load_b_t<128>(a_s0 + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
+      load_b_t<Core<kV>>(a_s0, g * 16, i0 + nb * 16, lane, bh);
+      load_b_t<Core<kV>>(a_s0 + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
       float x[2][4] = {}, y[2][4] = {};
       mma_pair(x[0], x[1], a, bl);
       mma_pair(y[0], y[1], ah, bl);
@@ -279,35 +306,45 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     if (tid == 0) set_error(p);
     return;
   }
-  // ---- 3. exp(Gamma_C) sum_v S0 dS1 per channel: thread = two channels of 16 value columns ...
-  float e0 = 0.f, e1 = 0.f;
+  // ---- 3. exp(Gamma_C) sum_v S0 dS1: warp = eight channels, lanes over the value columns; lane e < 8 keeps channel e's
+  float e_sum = 0.f;
   {
-    const int i = (tid & 63) * 2, g = tid >> 6;
-#pragma unroll 4
-    for (int v = g * 16; v < g * 16 + 16; ++v) {
-      const uint32_t off = off128(v, i);
-      const float2 s = join2(*reinterpret_cast<const uint32_t*>(sm.s0 + off), *reinterpret_cast<const uint32_t*>(sm.s0 + kV * kK * 2 + off));
-      const float2 d = join2(*reinterpret_cast<const uint32_t*>(sm.ds + off), *reinterpret_cast<const uint32_t*>(sm.ds + kV * kK * 2 + off));
-      e0 = fmaf(s.x, d.x, e0);
-      e1 = fmaf(s.y, d.y, e1);
+    float x[8] = {};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t off = Core<kV>::off(q * 32 + lane, warp * 8);
+      const uint4 sh = *reinterpret_cast<const uint4*>(sm.s0 + off), sl = *reinterpret_cast<const uint4*>(sm.s0 + kV * kK * 2 + off);
+      const uint4 dh = *reinterpret_cast<const uint4*>(sm.ds + off), dl = *reinterpret_cast<const uint4*>(sm.ds + kV * kK * 2 + off);
+      const float inv = pow2_inv(sm.sc[Record::kScS + q]) * pow2_inv(sm.sc[Record::kScDS + q]);
+      const uint32_t a[4] = {sh.x, sh.y, sh.z, sh.w}, al[4] = {sl.x, sl.y, sl.z, sl.w};
+      const uint32_t d[4] = {dh.x, dh.y, dh.z, dh.w}, ld[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 s = join2(a[e], al[e]), ds = join2(d[e], ld[e]);
+        x[2 * e] = fmaf(s.x * ds.x, inv, x[2 * e]);
+        x[2 * e + 1] = fmaf(s.y * ds.y, inv, x[2 * e + 1]);
+      }
     }
-    const float inv = pow2_inv(sm.sc[Record::kScS + g * 4 + (i >> 5)]) * pow2_inv(sm.sc[Record::kScDS + g * 4 + (i >> 5)]);
-    e0 *= inv * sm.hdr[Record::kDecay + i];
-    e1 *= inv * sm.hdr[Record::kDecay + i + 1];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
+      if (lane == e) e_sum = x[e] * sm.hdr[Record::kDecay + warp * 8 + e];
+    }
   }
   // ---- 4. dKe = (beta r) dS1^T
   float dkc[4][4] = {};
 #pragma unroll 2
   for (int g = 0; g < 8; ++g) {
     uint32_t ah[4], al[4];
-    load_a_t<64>(a_r, I * 16, g * 16, lane, ah);
-    load_a_t<64>(a_r + Record::kPlane, I * 16, g * 16, lane, al);
-    const float f = pow2_inv(sm.sc[Record::kScR + g * 4 + I]) * pow2_inv(sm.sc[Record::kScDS + g * 4 + i4]);
+    load_a_t<Core<kV>>(a_r, I * 16, g * 16, lane, ah);
+    load_a_t<Core<kV>>(a_r + Record::kPlane, I * 16, g * 16, lane, al);
+    const float f = pow2_inv(sm.sc[Record::kScR + (g >> 1)]) * pow2_inv(sm.sc[Record::kScDS + (g >> 1)]);
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb) {
       uint32_t bh[4], bl[4];
-      load_b_t<128>(a_ds, g * 16, i0 + nb * 16, lane, bh);
-      load_b_t<128>(a_ds + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
+      load_b_t<Core<kV>>(a_ds, g * 16, i0 + nb * 16, lane, bh);
+      load_b_t<Core<kV>>(a_ds + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
       float x[2][4] = {};
       mma_pair(x[0], x[1], ah, bl);
       mma_pair(x[0], x[1], al, bh);
@@ -335,12 +372,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll 2
     for (int g = 0; g < 8; ++g) {
       uint32_t a[4], ah[4], al[4], bh[4], bl[4];
-      load_a<128>(a_do, ti * 16, g * 16, lane, a);
-      load_a_t<64>(a_dr, ti * 16, g * 16, lane, ah);
-      load_a_t<64>(a_dr + Record::kPlane, ti * 16, g * 16, lane, al);
-      load_b_t<64>(a_r, g * 16, si * 16, lane, bh);
-      load_b_t<64>(a_r + Record::kPlane, g * 16, si * 16, lane, bl);
-      const float inv_r = pow2_inv(sm.sc[Record::kScR + g * 4 + si]);
+      load_a<Rows128>(a_do, ti * 16, g * 16, lane, a);
+      load_a_t<Core<kV>>(a_dr, ti * 16, g * 16, lane, ah);
+      load_a_t<Core<kV>>(a_dr + Record::kPlane, ti * 16, g * 16, lane, al);
+      load_b_t<Core<kV>>(a_r, g * 16, si * 16, lane, bh);
+      load_b_t<Core<kV>>(a_r + Record::kPlane, g * 16, si * 16, lane, bl);
+      const float inv_r = pow2_inv(sm.sc[Record::kScR + (g >> 1)]);
       const float fp = inv_r * (pow2_inv(sc_do) * p.scale), fa = -inv_r * pow2_inv(sm.sc_dr[g][ti]);
       float x[2][4] = {}, y[2][4] = {};
       mma_pair(x[0], x[1], a, bl);
@@ -472,9 +509,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   // ---- 8. dq, dk; dg by a sum from the chunk's end
   float (*const dgam)[kGP] = pr.up;
   float (*const keb)[kK] = reinterpret_cast<float (*)[kK]>(&pr.ku[0][0]);  // [4 row blocks x 8 rows][128]
-  float (*const ev)[kK] = reinterpret_cast<float (*)[kK]>(&pr.qu[0][0]);   // [8][128]
-  ev[tid >> 6][(tid & 63) * 2] = e0;
-  ev[tid >> 6][(tid & 63) * 2 + 1] = e1;
+  float* const ev = &pr.qu[0][0];  // [128]
+  if (lane < 8) ev[warp * 8 + lane] = e_sum;
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
 #pragma unroll
@@ -500,9 +536,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
     for (int t = kB - 1; t >= 0; --t) sum += dgam[sub * kB + t][ch];
     sm.tail[sub][ch] = sum;
-    float acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) acc += ev[w][ch];
+    float acc = ev[ch];
 #pragma unroll 8
     for (int w = 0; w < 32; ++w) acc += keb[w][ch];
     __syncthreads();

@@ -178,16 +178,29 @@ __device__ __forceinline__ void solve_below(PrepSmem& sm, int r0, int c0, int la
   __syncwarp();
 }
 
+// Elements s0 .. s0 + 7 of row t of a lower triangular matrix stored by blocks of 16 (nothing above the diagonal blocks).
+__device__ __forceinline__ void read_row(const float (&m)[kC][kAP], int t, int s0, float (&x)[8]) {
+  const bool in = (s0 >> 4) <= (t >> 4);
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(&m[t][s0 + e]);
+    x[e] = in ? v.x : 0.f;
+    x[e + 1] = in ? v.y : 0.f;
+    x[e + 2] = in ? v.z : 0.f;
+    x[e + 3] = in ? v.w : 0.f;
+  }
+}
+
 // 16 x 16 of a product over the 128 channels of two pair tiles [row][i].
 __device__ __forceinline__ void pair_product(uint32_t row_tile, int m0, uint32_t col_tile, int n0, int lane, float (&out)[2][4]) {
   float hi[2][2][4] = {}, lo[2][4] = {};
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     uint32_t ah[4], al[4], bh[4], bl[4];
-    load_a<128>(row_tile, m0, kk * 16, lane, ah);
-    load_a<128>(row_tile + kHalfPlane, m0, kk * 16, lane, al);
-    load_b<128>(col_tile, kk * 16, n0, lane, bh);
-    load_b<128>(col_tile + kHalfPlane, kk * 16, n0, lane, bl);
+    load_a<Core<32>>(row_tile, m0, kk * 16, lane, ah);
+    load_a<Core<32>>(row_tile + kHalfPlane, m0, kk * 16, lane, al);
+    load_b<Core<32>>(col_tile, kk * 16, n0, lane, bh);
+    load_b<Core<32>>(col_tile + kHalfPlane, kk * 16, n0, lane, bl);
     mma_pair(lo[0], lo[1], ah, bl);
     mma_pair(lo[0], lo[1], al, bh);
     mma_pair(hi[kk & 1][0], hi[kk & 1][1], ah, bh);
@@ -320,12 +333,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       dst[t][s] = s < t + kind ? x : 0.f;
     }
   }
-  // ---- 4. tiles of the decayed rows, over the factors: Qt and Ke to the record, the others to shared memory
+  // ---- 4. tiles of the decayed rows, over the factors: Qt and Ke to the record, the others to shared memory;
+  // warp = eight channels, lane = token (and the one 32 further on)
   {
+    const int i0 = warp * 8;
     float ku[2][8], qu[2][8], kd[2][8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = tid + j * kPrepThreads, t = c >> 4, i0 = (c & 15) * 8;
+      const int t = j * 32 + lane;
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
         *reinterpret_cast<float4*>(&ku[j][e]) = *reinterpret_cast<const float4*>(&sm.f.ku[t][i0 + e]);
@@ -340,25 +355,24 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
 #pragma unroll
       for (int e = 0; e < 4; ++e) split2(x[2 * e] * f[2 * e] * sc, x[2 * e + 1] * f[2 * e + 1] * sc, h[e], l[e]);
       *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      if (lo != nullptr) *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+      *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
     };
     auto get = [&](const float* src, float (&f)[8]) {
       *reinterpret_cast<float4*>(&f[0]) = *reinterpret_cast<const float4*>(src);
       *reinterpret_cast<float4*>(&f[4]) = *reinterpret_cast<const float4*>(src + 4);
     };
-    const float sc_v = scale_of(kMxV);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = tid + j * kPrepThreads, t = c >> 4, i0 = (c & 15) * 8, tb = t / kB;  // tb: 0, 1 and then 2, 3
-      const uint32_t off = off128(t, i0);
+      const int t = j * 32 + lane, tb = t / kB;  // tb: 0, 1 and then 2, 3
+      const uint32_t off = Core<kC>::off(t, i0);
       float f[8];
       get(&sm.up[tb][i0], f);
       put(sm.t.kt, sm.t.kt + Record::kPlane, off, ku[j], f, scale_of(kMxKt));
-      put(rec + Record::kQt, p.save ? rec + Record::kQt + Record::kPlane : nullptr, off, qu[j], f, scale_of(kMxQt));
+      put(rec + Record::kQt, rec + Record::kQt + Record::kPlane, off, qu[j], f, scale_of(kMxQt));
       get(&sm.dn[tb][i0], f);
       put(rec + Record::kKe, rec + Record::kKe + Record::kPlane, off, kd[j], f, scale_of(kMxKe));
       get(&sm.x32[tb][i0], f);
-      const uint32_t off32 = off128(t & 31, i0), off16 = off128((t >> 5) * kB + (t & 15), i0);
+      const uint32_t off32 = Core<32>::off(lane, i0), off16 = Core<32>::off(j * kB + (lane & 15), i0);
       if (j == 1) {
         put(sm.t.r32[0], sm.t.r32[0] + kHalfPlane, off32, ku[j], f, scale_of(kMxR32K));
         put(sm.t.r32[1], sm.t.r32[1] + kHalfPlane, off32, qu[j], f, scale_of(kMxR32Q));
@@ -372,12 +386,17 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       } else {
         put(sm.t.c16, sm.t.c16 + kHalfPlane, off16, kd[j], f, scale_of(kMxC16));
       }
+    }
+    const float sc_v = scale_of(kMxV);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = tid + j * kPrepThreads;
       const uint32_t w[4] = {vraw[j].x, vraw[j].y, vraw[j].z, vraw[j].w};
       uint32_t vh[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         vh[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc_v, __uint_as_float(w[e] & 0xffff0000u) * sc_v));
-      *reinterpret_cast<uint4*>(sm.vt + off) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+      *reinterpret_cast<uint4*>(sm.vt + Rows128::off(c >> 4, (c & 15) * 8)) = make_uint4(vh[0], vh[1], vh[2], vh[3]);
     }
   }
   __syncthreads();
@@ -440,15 +459,14 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     const float sc_p = scale_of(kMxP);
     if (w == 0) hdr[Record::kScP] = sc_p;
     for (int c = w; c < kC * kC / 8; c += kPrepThreads - 128) {
-      const int t = c >> 3, s0 = (c & 7) * 8;
-      const bool in = (s0 >> 4) <= (t >> 4);
+      const int t = c & 63, s0 = (c >> 6) * 8;
+      float x[8];
+      read_row(sm.pm, t, s0, x);
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        split2(in ? sm.pm[t][s0 + 2 * e] * sc_p : 0.f, in ? sm.pm[t][s0 + 2 * e + 1] * sc_p : 0.f, hi[e], lo[e]);
-      *reinterpret_cast<uint4*>(rec + Record::kP + off64(t, s0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (p.save)
-        *reinterpret_cast<uint4*>(rec + Record::kP + kC * kC * 2 + off64(t, s0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      for (int e = 0; e < 4; ++e) split2(x[2 * e] * sc_p, x[2 * e + 1] * sc_p, hi[e], lo[e]);
+      *reinterpret_cast<uint4*>(rec + Record::kP + Core<kC>::off(t, s0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(rec + Record::kP + kC * kC * 2 + Core<kC>::off(t, s0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
   __syncthreads();
@@ -457,22 +475,24 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   const float sc_m = pow2_scale(fmaxf(1.f, y_beta)), sc_y = pow2_scale(y_beta), sc_v = scale_of(kMxV), sc_kt = scale_of(kMxKt);
   unsigned char* const mt = reinterpret_cast<unsigned char*>(&sm.pm[0][0]);
   {
-    const int t = tid >> 3, s0 = (tid & 7) * 8;
-    const bool in = (s0 >> 4) <= (t >> 4);
+    const int t = tid & 63, s0 = (tid >> 6) * 8;
     const float bt = sm.beta[t];
+    float x[8];
+    read_row(sm.y, t, s0, x);
     uint32_t hi[4], lo[4], yh[4], yl[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int s = s0 + 2 * e;
-      const float y0 = in ? sm.y[t][s] : 0.f, y1 = in ? sm.y[t][s + 1] : 0.f;
-      split2(((t == s ? 1.f : 0.f) - y0 * sm.beta[s]) * sc_m, ((t == s + 1 ? 1.f : 0.f) - y1 * sm.beta[s + 1]) * sc_m, hi[e], lo[e]);
-      split2(y0 * bt * sc_y, y1 * bt * sc_y, yh[e], yl[e]);
+      split2(((t == s ? 1.f : 0.f) - x[2 * e] * sm.beta[s]) * sc_m, ((t == s + 1 ? 1.f : 0.f) - x[2 * e + 1] * sm.beta[s + 1]) * sc_m,
+             hi[e], lo[e]);
+      split2(x[2 * e] * bt * sc_y, x[2 * e + 1] * bt * sc_y, yh[e], yl[e]);
     }
-    *reinterpret_cast<uint4*>(mt + off64(t, s0)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(mt + kC * kC * 2 + off64(t, s0)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    const uint32_t off = Core<kC>::off(t, s0);
+    *reinterpret_cast<uint4*>(mt + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(mt + kC * kC * 2 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (p.save) {
-      *reinterpret_cast<uint4*>(rec + Record::kY + off64(t, s0)) = make_uint4(yh[0], yh[1], yh[2], yh[3]);
-      *reinterpret_cast<uint4*>(rec + Record::kY + kC * kC * 2 + off64(t, s0)) = make_uint4(yl[0], yl[1], yl[2], yl[3]);
+      *reinterpret_cast<uint4*>(rec + Record::kY + off) = make_uint4(yh[0], yh[1], yh[2], yh[3]);
+      *reinterpret_cast<uint4*>(rec + Record::kY + kC * kC * 2 + off) = make_uint4(yl[0], yl[1], yl[2], yl[3]);
     }
   }
   __syncthreads();
@@ -487,9 +507,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     float hi[2][4] = {}, lo[2][4] = {};
     for (int kk = 0; kk <= nb; ++kk) {  // s sub-blocks up to it
       uint32_t av[4], bh[4], bl[4];
-      load_a_t<128>(vt_a, g16, kk * 16, lane, av);
-      load_b<64>(mt_a, kk * 16, nb * 16, lane, bh);
-      load_b<64>(mt_a + kC * kC * 2, kk * 16, nb * 16, lane, bl);
+      load_a_t<Rows128>(vt_a, g16, kk * 16, lane, av);
+      load_b<Core<kC>>(mt_a, kk * 16, nb * 16, lane, bh);
+      load_b<Core<kC>>(mt_a + kC * kC * 2, kk * 16, nb * 16, lane, bl);
       mma_pair(lo[0], lo[1], av, bl);
       mma_pair(hi[0], hi[1], av, bh);
     }
@@ -499,7 +519,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
-        *reinterpret_cast<float2*>(rt + (v0 + hf * 8) * kC + t0 + n * 8) =
+        *reinterpret_cast<float2*>(rt + ((t0 + n * 8) >> 2) * (kV * 4) + (v0 + hf * 8) * 4 + (t0 & 3)) =
             make_float2((hi[n][2 * hf] + lo[n][2 * hf]) * inv, (hi[n][2 * hf + 1] + lo[n][2 * hf + 1]) * inv);
   }
   // ---- 9. Wr = M Kt: warp = 16 key channels, the same token sub-blocks
@@ -511,10 +531,10 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     float hi[2][4] = {}, lo[2][4] = {};
     for (int kk = 0; kk <= mb; ++kk) {
       uint32_t ah[4], al[4], bh[4], bl[4];
-      load_b_t<128>(kt_a, kk * 16, g16, lane, bh);
-      load_b_t<128>(kt_a + Record::kPlane, kk * 16, g16, lane, bl);
-      load_a<64>(mt_a, mb * 16, kk * 16, lane, ah);
-      load_a<64>(mt_a + kC * kC * 2, mb * 16, kk * 16, lane, al);
+      load_b_t<Core<kC>>(kt_a, kk * 16, g16, lane, bh);
+      load_b_t<Core<kC>>(kt_a + Record::kPlane, kk * 16, g16, lane, bl);
+      load_a<Core<kC>>(mt_a, mb * 16, kk * 16, lane, ah);
+      load_a<Core<kC>>(mt_a + kC * kC * 2, mb * 16, kk * 16, lane, al);
       mma_pair(lo[0], lo[1], ah, bl);
       mma_pair(lo[0], lo[1], al, bh);
       mma_pair(hi[0], hi[1], ah, bh);
@@ -539,7 +559,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t hi, lo;
         split2(acc[u][n][2 * hf] * sc_wr, acc[u][n][2 * hf + 1] * sc_wr, hi, lo);
-        const uint32_t off = off128((u ? 3 - first : first) * 16 + hf * 8 + (lane >> 2), g16 + n * 8 + 2 * (lane & 3));
+        const uint32_t off = Core<kC>::off((u ? 3 - first : first) * 16 + hf * 8 + (lane >> 2), g16 + n * 8 + 2 * (lane & 3));
         *reinterpret_cast<uint32_t*>(sm.t.kt + off) = hi;
         *reinterpret_cast<uint32_t*>(sm.t.kt + Record::kPlane + off) = lo;
       }

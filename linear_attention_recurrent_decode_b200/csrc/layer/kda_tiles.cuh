@@ -68,21 +68,28 @@ __device__ __forceinline__ float2 join2(uint32_t hi, uint32_t lo) {
 }
 
 // ---------------------------------------------------------------- tiles
-// Byte offset of element (r, c) of a 16-bit tile with 128 or 64 columns: rows
-// of 256 or 128 bytes whose 16-byte pieces are permuted by the row (XOR with
-// its low three bits), so that eight rows of one column block lie in different
-// banks.  The same image is kept in global memory: a tile is one bulk copy.
-__device__ __forceinline__ uint32_t off128(int r, int c) {
-  return static_cast<uint32_t>(r * 256 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) * 2)));
-}
-__device__ __forceinline__ uint32_t off64(int r, int c) {
-  return static_cast<uint32_t>(r * 128 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) * 2)));
-}
-template <int COLS>
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-  if constexpr (COLS == 128) return off128(r, c);
-  else return off64(r, c);
-}
+// Byte offsets of element (r, c) of a 16-bit tile.
+//
+// Core: 16-byte pieces of eight columns, the pieces of one column block
+// contiguous over the ROWS rows.  Eight rows of a piece are one core matrix of
+// the tensor cores' unswizzled shared-memory layout, so the same tile serves as
+// an operand with its rows as the product's columns (K-major) and, transposed,
+// with its rows contracted (MN-major), and as an ldmatrix source without bank
+// conflicts; a warp whose lanes own rows writes it in whole lines.  The image in
+// global memory is the same: a tile is one bulk copy.
+template <int ROWS>
+struct Core {
+  static constexpr int kBlock = ROWS * 16;  // bytes from one column block to the next
+  static __device__ __forceinline__ uint32_t off(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * kBlock + r * 16 + (c & 7) * 2);
+  }
+};
+// Rows of 256 bytes whose 16-byte pieces are permuted by the row: for tiles written a row of 16-byte pieces at a time.
+struct Rows128 {
+  static __device__ __forceinline__ uint32_t off(int r, int c) {
+    return static_cast<uint32_t>(r * 256 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) * 2)));
+  }
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -93,23 +100,23 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 // A fragment (16 x 16 at (m0, k0)) of a tile stored [m][k] or [k][m].
-template <int COLS>
+template <class L>
 __device__ __forceinline__ void load_a(uint32_t tile, int m0, int k0, int lane, uint32_t (&a)[4]) {
-  ldsm4(tile + tile_off<COLS>(m0 + (lane & 15), k0 + (lane >> 4) * 8), a);
+  ldsm4(tile + L::off(m0 + (lane & 15), k0 + (lane >> 4) * 8), a);
 }
-template <int COLS>
+template <class L>
 __device__ __forceinline__ void load_a_t(uint32_t tile, int m0, int k0, int lane, uint32_t (&a)[4]) {
-  ldsm4t(tile + tile_off<COLS>(k0 + (lane & 7) + (lane >> 4) * 8, m0 + ((lane >> 3) & 1) * 8), a);
+  ldsm4t(tile + L::off(k0 + (lane & 7) + (lane >> 4) * 8, m0 + ((lane >> 3) & 1) * 8), a);
 }
 // B fragments of two 8-column tiles (16 x 16 at (k0, n0); b[0..1] columns n0..,
 // b[2..3] columns n0 + 8..) of a tile stored [n][k] or [k][n].
-template <int COLS>
+template <class L>
 __device__ __forceinline__ void load_b(uint32_t tile, int k0, int n0, int lane, uint32_t (&b)[4]) {
-  ldsm4(tile + tile_off<COLS>(n0 + (lane & 7) + (lane >> 4) * 8, k0 + ((lane >> 3) & 1) * 8), b);
+  ldsm4(tile + L::off(n0 + (lane & 7) + (lane >> 4) * 8, k0 + ((lane >> 3) & 1) * 8), b);
 }
-template <int COLS>
+template <class L>
 __device__ __forceinline__ void load_b_t(uint32_t tile, int k0, int n0, int lane, uint32_t (&b)[4]) {
-  ldsm4t(tile + tile_off<COLS>(k0 + (lane & 15), n0 + (lane >> 4) * 8), b);
+  ldsm4t(tile + L::off(k0 + (lane & 15), n0 + (lane >> 4) * 8), b);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -185,12 +192,5 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* mbar, uint32_t parity) {
 }
 // Orders this thread's ordinary shared-memory accesses before later bulk copies into the same bytes.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 }  // namespace kdal
