@@ -57,8 +57,9 @@
  * copies are bounded, and one that ever gives up stores 1 there and leaves
  * results undefined; the library never clears it.
  *
- * Execution: kda_scan enqueues 2 kernels, kda_scan_backward 2 (4 with saved =
- * 0) on `stream`; no host synchronisation; can be captured in a CUDA graph.
+ * Execution: kda_scan enqueues 2 kernels (4 where long sequences of few heads
+ * are walked in segments), kda_scan_backward 2 (4), and those of the forward pass
+ * before them with saved = 0, on `stream`; no host synchronisation; can be captured in a CUDA graph.
  * Results do not depend on the launch's timing (no atomics on data).
  *
  * Errors: as in kda_decode.h, nothing is enqueued unless KDA_OK is returned.

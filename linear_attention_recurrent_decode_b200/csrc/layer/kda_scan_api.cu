@@ -6,6 +6,7 @@
 #include "kda_layer_host.h"
 #include "kda_scan_chain.cuh"
 #include "kda_scan_grad.cuh"
+#include "kda_scan_join.cuh"
 #include "kda_scan_prep.cuh"
 #include "layer/kda_scan.h"
 
@@ -30,6 +31,8 @@ cudaError_t prepare_kernels() {
   allow(ks::kda_scan_prep_kernel, static_cast<int>(sizeof(ks::PrepSmem)));
   allow(ks::kda_scan_forward_kernel, kChainSmem);
   allow(ks::kda_scan_backward_kernel, kChainSmem);
+  allow(ks::kda_scan_join_kernel<false>, static_cast<int>(sizeof(ks::JoinSmem)));
+  allow(ks::kda_scan_join_kernel<true>, static_cast<int>(sizeof(ks::JoinSmem)));
   allow(ks::kda_scan_grad_kernel, static_cast<int>(sizeof(ks::GradSmem)));
   if (e == cudaSuccess && bit) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -41,11 +44,39 @@ bool chunk_slots(int64_t N, int64_t T, bool packed, int64_t* slots) {
   return mul_ok(N, T / ks::kC + (T % ks::kC != 0), slots);
 }
 
-bool workspace_bytes(int64_t N, int64_t T, bool packed, int64_t HV, bool training, int64_t* bytes) {
-  int64_t slots, recs;
-  return chunk_slots(N, T, packed, &slots) && mul_ok(slots, HV, &recs) && recs <= 0x7fffffffLL &&
-         mul_ok(recs, training ? ks::Record::kTraining : ks::Record::kForward, bytes) &&
-         !__builtin_add_overflow(*bytes, ks::kWsHeader, bytes);
+// Chunks of a segment, 0 for none, and the segment slots of the call.  Segments are for calls whose sequences and heads
+// leave half the SMs idle or more, with room for a sequence of 24 chunks (below, walking it twice and joining cost what
+// the segments save); as long as the first of the two walks, two blocks a segment, then fills the SMs once, and at least
+// 8 chunks.  Measured (8192 tokens, 8 heads): see the table of the chain's times in kda_scan_chain.cuh.
+constexpr int64_t kSms = 148;
+bool segments(int64_t N, int64_t T, bool packed, int64_t HV, int32_t* seg_chunks, int64_t* slots) {
+  const int64_t total = packed ? T / ks::kC : (T + ks::kC - 1) / ks::kC;  // the longest sequence's chunks at most
+  *seg_chunks = 0;
+  *slots = N;
+  int64_t units;
+  if (!mul_ok(N, HV, &units)) return false;
+  if (units * 2 >= kSms || total < 24) return true;
+  const int64_t all = (packed ? total : total * N) * HV;
+  int64_t len = (2 * all + kSms - 1) / kSms;
+  len = len < 8 ? 8 : len;
+  if (len > 0x7fffffff) return false;
+  *seg_chunks = static_cast<int32_t>(len);
+  *slots = packed ? total / len + N : N * ((total + len - 1) / len);
+  return true;
+}
+
+bool workspace_bytes(int64_t N, int64_t T, bool packed, int64_t HV, bool training, int64_t* bytes, int64_t* records = nullptr) {
+  int64_t slots, recs, seg_slots, seg_bytes = 0;
+  int32_t seg_chunks;
+  if (!chunk_slots(N, T, packed, &slots) || !mul_ok(slots, HV, &recs) || recs > 0x7fffffffLL ||
+      !mul_ok(recs, training ? ks::Record::kTraining : ks::Record::kForward, bytes) || __builtin_add_overflow(*bytes, ks::kWsHeader, bytes) ||
+      !segments(N, T, packed, HV, &seg_chunks, &seg_slots))
+    return false;
+  if (records) *records = *bytes;
+  if (seg_chunks > 0 && (!mul_ok(seg_slots, HV, &seg_bytes) || seg_bytes > 0x7fffffffLL / 2 ||
+                         !mul_ok(seg_bytes, 2 * ks::kK * ks::kV * static_cast<int64_t>(sizeof(float)), &seg_bytes)))
+    return false;
+  return !__builtin_add_overflow(*bytes, seg_bytes, bytes);
 }
 
 kda_status check_rows(const void* p, int64_t stride, int64_t width, int64_t rows, uintptr_t align, int64_t mult) {
@@ -62,14 +93,14 @@ kda_status check_rows(const void* p, int64_t stride, int64_t width, int64_t rows
   } while (0)
 
 // Checks what both calls share and fills the kernels' parameters.
-kda_status common(const kda_scan_args& a, bool training, ks::ScanParams* p, int64_t* slots, int64_t* rows) {
+kda_status common(const kda_scan_args& a, bool training, ks::ScanParams* p, int64_t* slots, int64_t* seg_slots, int64_t* rows) {
   if (a.N < 0 || a.T < 0 || a.HV < 0 || a.workspace_bytes < 0 || a.num_slots < 0) return KDA_ERR_INVALID_ARG;
   if (a.HV < 1 || a.K != ks::kK || a.V != ks::kV) return KDA_ERR_UNSUPPORTED;
   const bool packed = a.cu_seqlens != nullptr;
-  int64_t need, units;
+  int64_t need, units, records;
   if (!mul_ok(a.N, packed ? 1 : a.T, rows)) return KDA_ERR_UNSUPPORTED;
   if (packed) *rows = a.T;
-  if (!chunk_slots(a.N, a.T, packed, slots) || !workspace_bytes(a.N, a.T, packed, a.HV, training, &need) ||
+  if (!chunk_slots(a.N, a.T, packed, slots) || !workspace_bytes(a.N, a.T, packed, a.HV, training, &need, &records) ||
       !mul_ok(a.N, a.HV, &units) || units > 0x7fffffffLL || a.N > 0x7fffffffLL || *rows > INT64_MAX / (a.HV * ks::kK * 8))
     return KDA_ERR_UNSUPPORTED;
   if (packed && a.T > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;  // int32 offsets
@@ -99,6 +130,12 @@ kda_status common(const kda_scan_args& a, bool training, ks::ScanParams* p, int6
   p->seq_chunks = static_cast<int32_t>(packed ? 0 : (a.T + ks::kC - 1) / ks::kC);
   p->scale = a.scale;
   p->save = training;
+  segments(a.N, a.T, packed, a.HV, &p->seg_chunks, seg_slots);
+  if (p->seg_chunks > 0) {
+    p->seq_segs = static_cast<int32_t>(packed ? 0 : (p->seq_chunks + p->seg_chunks - 1) / p->seg_chunks);
+    p->seg_state = reinterpret_cast<float*>(p->ws + records);
+    p->seg_map = p->seg_state + *seg_slots * a.HV * ks::kK * ks::kV;
+  }
   return KDA_OK;
 }
 
@@ -126,9 +163,29 @@ bool launch(F kernel, int64_t grid, int threads, int smem, kda_stream_t stream, 
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
 }
 
-bool launch_forward(const ks::ScanParams& p, int64_t slots, kda_stream_t stream) {
-  return launch(ks::kda_scan_prep_kernel, slots * p.HV, ks::kPrepThreads, sizeof(ks::PrepSmem), stream, p) &&
-         launch(ks::kda_scan_forward_kernel, p.N * p.HV, ks::kForwardThreads, kChainSmem, stream, p);
+constexpr int kJoinGroups = ks::kV / ks::kJoinCols;
+
+bool launch_forward(ks::ScanParams p, int64_t slots, int64_t seg_slots, kda_stream_t stream) {
+  if (!launch(ks::kda_scan_prep_kernel, slots * p.HV, ks::kPrepThreads, sizeof(ks::PrepSmem), stream, p)) return false;
+  if (p.seg_chunks > 0) {
+    p.transitions = 1;
+    if (!launch(ks::kda_scan_forward_kernel, seg_slots * p.HV * 2, ks::kForwardThreads, kChainSmem, stream, p) ||
+        !launch(ks::kda_scan_join_kernel<false>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, sizeof(ks::JoinSmem), stream, p))
+      return false;
+    p.transitions = 0;
+  }
+  return launch(ks::kda_scan_forward_kernel, seg_slots * p.HV, ks::kForwardThreads, kChainSmem, stream, p);
+}
+bool launch_backward(ks::ScanParams p, int64_t slots, int64_t seg_slots, kda_stream_t stream) {
+  if (p.seg_chunks > 0) {
+    p.transitions = 1;
+    if (!launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kBackwardThreads, kChainSmem, stream, p) ||
+        !launch(ks::kda_scan_join_kernel<true>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, sizeof(ks::JoinSmem), stream, p))
+      return false;
+    p.transitions = 0;
+  }
+  return launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kBackwardThreads, kChainSmem, stream, p) &&
+         launch(ks::kda_scan_grad_kernel, slots * p.HV, ks::kGradThreads, sizeof(ks::GradSmem), stream, p);
 }
 
 }  // namespace
@@ -147,8 +204,8 @@ kda_status kda_scan(const kda_scan_args* args, kda_stream_t stream) {
   const kda_scan_args& a = *args;
   if (a.N == 0 && a.T >= 0 && a.HV >= 1 && a.K == ks::kK && a.V == ks::kV) return KDA_OK;  // no sequence
   ks::ScanParams p;
-  int64_t slots, rows;
-  KDA_TRY(common(a, a.save != 0, &p, &slots, &rows));
+  int64_t slots, seg_slots, rows;
+  KDA_TRY(common(a, a.save != 0, &p, &slots, &seg_slots, &rows));
   const int64_t hv = a.HV * ks::kV, state = a.HV * ks::kK * ks::kV;
   KDA_TRY(check_rows(a.out, a.out_row_stride, hv, rows, 16, 8));
   const Inputs in = inputs_of(a, rows);
@@ -168,7 +225,7 @@ kda_status kda_scan(const kda_scan_args* args, kda_stream_t stream) {
   p.slot_idx = a.slot_idx;
   p.num_slots = a.num_slots;
   p.out = static_cast<__nv_bfloat16*>(a.out), p.out_ts = a.out_row_stride;
-  return launch_forward(p, slots, stream) ? KDA_OK : KDA_ERR_CUDA;
+  return launch_forward(p, slots, seg_slots, stream) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_scan_backward(const kda_scan_args* args, const kda_scan_grads* grads, kda_stream_t stream) {
@@ -178,8 +235,8 @@ kda_status kda_scan_backward(const kda_scan_args* args, const kda_scan_grads* gr
   if (a.N == 0 && a.T >= 0 && a.HV >= 1 && a.K == ks::kK && a.V == ks::kV) return KDA_OK;
   if (a.slot_idx != nullptr) return KDA_ERR_INVALID_ARG;
   ks::ScanParams p;
-  int64_t slots, rows;
-  KDA_TRY(common(a, true, &p, &slots, &rows));
+  int64_t slots, seg_slots, rows;
+  KDA_TRY(common(a, true, &p, &slots, &seg_slots, &rows));
   const int64_t hk = a.HV * ks::kK, hv = a.HV * ks::kV, state = hk * ks::kV;
   KDA_TRY(check_rows(d.d_out, d.d_out_row_stride, hv, rows, 16, 8));
   KDA_TRY(check_rows(d.dq, d.dq_row_stride, hk, rows, 16, 8));
@@ -215,10 +272,8 @@ kda_status kda_scan_backward(const kda_scan_args* args, const kda_scan_grads* gr
   p.dg = d.dg, p.dg_ts = d.dg_row_stride;
   p.dbeta = d.dbeta, p.dbeta_ts = d.dbeta_row_stride;
   p.d_init = d.d_initial_state;
-  if (!d.saved && !launch_forward(p, slots, stream)) return KDA_ERR_CUDA;  // p.out is null: states only
-  if (!launch(ks::kda_scan_backward_kernel, a.N * a.HV, ks::kBackwardThreads, kChainSmem, stream, p)) return KDA_ERR_CUDA;
-  return launch(ks::kda_scan_grad_kernel, slots * a.HV, ks::kGradThreads, sizeof(ks::GradSmem), stream, p) ? KDA_OK
-                                                                                                          : KDA_ERR_CUDA;
+  if (!d.saved && !launch_forward(p, slots, seg_slots, stream)) return KDA_ERR_CUDA;  // p.out is null: states only
+  return launch_backward(p, slots, seg_slots, stream) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

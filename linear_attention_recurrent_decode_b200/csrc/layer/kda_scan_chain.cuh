@@ -17,6 +17,14 @@
 // scales, one per 32 of them.  The B operands are the record's tiles, straight
 // from bulk copies.
 //
+// Long sequences of few heads would leave most SMs idle.  They are cut into
+// segments: a segment's end state is linear in its start state, S -> M S + E.  A
+// first call walks every segment from zero (E) and, with no values, from the
+// identity (the matrix M, whose columns are 128 more value columns); a small
+// kernel joins the segments in order, and a second call walks them all from
+// their right starts.  That is three times the work in (1 / segments) of the
+// time.  Backwards the transition is M's transpose.
+//
 // Warps: 0-15 compute, 16 copies, 17 issues the products, 18-21 (forward) read
 // the outputs back.  A chunk's critical path is two products with a conversion
 // behind each; the outputs' products and read-back run beside it.
@@ -48,6 +56,7 @@ struct ChainSmem {
   uint64_t d_out;                   // backward: dO is written
   uint64_t end;
   uint32_t tmem;
+  int64_t seq;
 };
 static_assert(sizeof(ChainSmem) <= 232448, "shared memory of an SM");
 
@@ -241,25 +250,41 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
-  const int64_t n = blockIdx.x / p.HV, h = blockIdx.x - n * p.HV;
-  int64_t start, len;
-  seq_range(p, n, start, len);
-  const int64_t chunks = (len + kC - 1) / kC, slot0 = first_slot(p, n, start), blk = state_block(p, n);
+  // the transitions' call: E and M of a segment in neighbouring blocks
+  const int64_t unit = p.transitions ? blockIdx.x >> 1 : blockIdx.x, slot = unit / p.HV, h = unit - slot * p.HV;
+  const bool map = p.transitions && (blockIdx.x & 1);
+  const Segment seg = locate_segment(p, slot, &sm.seq);
+  if (seg.segs == 0) return;
+  const bool last = seg.seg == seg.segs - 1;
+  // The last segment's end is not a start; M is for the segments behind the first (the last's for the backward pass).
+  if (p.transitions && (map ? seg.seg == 0 || (last && !p.save) : last)) return;
+  const int64_t n = seg.n, start = seg.start + seg.first * kC, len = seg.len - seg.first * kC, chunks = seg.chunks;
+  const int64_t blk = state_block(p, n);
   if (blk < 0) {  // inactive: zero outputs
-    for (int64_t t = threadIdx.x; t < len * 16; t += kForwardThreads)
-      *reinterpret_cast<uint4*>(p.out + (start + (t >> 4)) * p.out_ts + h * kV + (t & 15) * 8) = make_uint4(0, 0, 0, 0);
+    if (!p.transitions) {
+      const int64_t rows = len < chunks * kC ? len : chunks * kC;
+      for (int64_t t = threadIdx.x; t < rows * 16; t += kForwardThreads)
+        *reinterpret_cast<uint4*>(p.out + (start + (t >> 4)) * p.out_ts + h * kV + (t & 15) * 8) = make_uint4(0, 0, 0, 0);
+    }
     return;
   }
-  const bool outputs = p.out != nullptr;
+  const bool outputs = p.out != nullptr && !p.transitions, save = p.save && !p.transitions;
   chain_init(sm, outputs ? kComputeWarps + 4 : kComputeWarps);
-  const int64_t sblk = (blk * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
-  unsigned char* rec = record(p, slot0, h);
+  const int64_t sblk = (blk * p.HV + h) * kK * kV, gblk = (slot * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
+  unsigned char* rec = record(p, first_slot(p, n, seg.start) + seg.first, h);
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   Waiter w;
   if (warp < kComputeWarps) {
     const int part = warp >> 2;
     float s[kPartK];
-    load_state(p.s_in == nullptr ? nullptr : p.s_in + sblk, v, part, s);
+    // a segment's start: the first's is the call's, the others' the end of the one before (zero for their E)
+    const float* const from = seg.seg == 0 ? (p.s_in == nullptr ? nullptr : p.s_in + sblk)
+                                           : (p.transitions ? nullptr : p.seg_state + gblk - p.HV * kK * kV);
+    load_state(from, v, part, s);
+    if (map) {
+#pragma unroll
+      for (int j = 0; j < kPartK; ++j) s[j] = part * kPartK + j == v ? 1.f : 0.f;
+    }
     for (int64_t c = 0; c < chunks; ++c, rec += step) {
       const int b = static_cast<int>(c & 1);
       const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
@@ -270,13 +295,13 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
       tmem_wait_st();
       fence_before_sync();
       warp_arrive(&sm.state, lane);
-      if (p.save) write_pair<kK, false>(0, rec + Record::kS, kV * kK * 2, v, part * kPartK, s, sc_s);
+      if (save) write_pair<kK, false>(0, rec + Record::kS, kV * kK * 2, v, part * kPartK, s, sc_s);
       float r[kPartT];
       {
         const float4* const rt = reinterpret_cast<const float4*>(rec + Record::kRt) + part * (kPartT / 4) * kV + v;
 #pragma unroll
         for (int j = 0; j < kPartT / 4; ++j) {
-          const float4 x = rt[j * kV];
+          const float4 x = map ? make_float4(0.f, 0.f, 0.f, 0.f) : rt[j * kV];
           r[4 * j] = x.x;
           r[4 * j + 1] = x.y;
           r[4 * j + 2] = x.z;
@@ -307,7 +332,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
         sm.sc_u[b][quarter] = sc_u;
       }
       warp_arrive(&sm.scales[b], lane);
-      if (p.save) {
+      if (save) {
         const float sc_r = pow2_scale(quarter_max(sm, 2, abs_max(r), part, quarter));
         write_pair<kC, false>(0, rec + Record::kR, Record::kPlane, v, part * kPartT, r, sc_r);
         if (part == 0 && lane == 0) {
@@ -325,7 +350,9 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
     }
     if (!w.ok) {
       if (lane == 0) set_error(p);
-    } else if (p.s_out != nullptr) {
+    } else if (p.transitions) {
+      store_state((map ? p.seg_map : p.seg_state) + gblk, v, part, s);
+    } else if (last && p.s_out != nullptr) {
       store_state(p.s_out + sblk, v, part, s);
     }
   } else if (warp == kComputeWarps) {
@@ -418,20 +445,23 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
-  const int64_t n = blockIdx.x / p.HV, h = blockIdx.x - n * p.HV;
-  int64_t start, len;
-  seq_range(p, n, start, len);
-  const int64_t chunks = (len + kC - 1) / kC, slot0 = first_slot(p, n, start);
+  const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  const Segment seg = locate_segment(p, slot, &sm.seq);
+  if (seg.segs == 0 || (p.transitions && seg.seg == 0)) return;
+  const int64_t n = seg.n, start = seg.start + seg.first * kC, len = seg.len - seg.first * kC, chunks = seg.chunks;
   chain_init(sm, kComputeWarps);
-  const int64_t sblk = (n * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
-  unsigned char* rec = record(p, slot0 + (chunks > 0 ? chunks - 1 : 0), h);
+  const int64_t sblk = (n * p.HV + h) * kK * kV, gblk = (slot * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
+  unsigned char* rec = record(p, first_slot(p, n, seg.start) + seg.first + (chunks > 0 ? chunks - 1 : 0), h);
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   Waiter w;
   // i counts the chunks walked: i = 0 is the last chunk, and barriers' phases go by i
   if (warp < kComputeWarps) {
     const int part = warp >> 2;
     float s[kPartK];
-    load_state(p.d_final == nullptr ? nullptr : p.d_final + sblk, v, part, s);
+    // a segment's end: the last's is the call's, the others' the start of the one behind (zero for their transition)
+    const float* const from = seg.seg == seg.segs - 1 ? (p.d_final == nullptr ? nullptr : p.d_final + sblk)
+                                                      : (p.transitions ? nullptr : p.seg_state + gblk + p.HV * kK * kV);
+    load_state(from, v, part, s);
     // dO^T: this thread's value column and tokens, exact in fp16 after scaling (bf16 has 8 bits)
     unsigned short raw[kPartT];  // as loaded: packing them would wait for the loads
     int64_t raw_t0 = 0;
@@ -474,7 +504,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
       tmem_wait_st();
       fence_before_sync();
       warp_arrive(&sm.state, lane);
-      write_pair<kK, false>(0, rec + Record::kDS, kV * kK * 2, v, part * kPartK, s, sc_s);
+      if (!p.transitions) write_pair<kK, false>(0, rec + Record::kDS, kV * kK * 2, v, part * kPartK, s, sc_s);
       if (i + 1 < chunks) fetch(chunks - 2 - i);
       // ---- decay, and scale Qt^T dO
       w.warp(&sm.full_hdr[b], i >> 1);
@@ -505,7 +535,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
       fence_before_sync();
       warp_arrive(&sm.rows, lane);
       if (i + 1 < chunks) put();  // the products of this chunk's dO are complete
-      {
+      if (!p.transitions) {
         const float sc_du = pow2_scale(quarter_max(sm, 3, abs_max(du), part, quarter));
         write_pair<kC, false>(0, rec + Record::kDU, Record::kPlane, v, part * kPartT, du, sc_du);
         if (part == 0 && lane == 0) {
@@ -522,7 +552,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
     }
     if (!w.ok) {
       if (lane == 0) set_error(p);
-    } else if (p.d_init != nullptr) {
+    } else if (p.transitions) {
+      store_state(p.seg_state + gblk, v, part, s);
+    } else if (seg.seg == 0 && p.d_init != nullptr) {
       store_state(p.d_init + sblk, v, part, s);
     }
   } else if (warp == kComputeWarps) {

@@ -24,6 +24,11 @@ struct ScanParams {
   int32_t N, seq_chunks;    // seq_chunks: ceil(T / C) of the dense form
   float scale;
   int32_t save;             // the forward call keeps what the backward pass reads
+  // Segments of a sequence's chunks, walked side by side (see kda_scan_chain.cuh); seg_chunks 0: none.
+  int32_t seg_chunks, seq_segs;  // chunks of a segment; segments of a sequence of the dense form
+  int32_t transitions;      // the chain call computes the segments' transitions instead of the results
+  float* seg_state;         // [segment slots, HV, K, V] states at the segments' ends (or starts, backwards)
+  float* seg_map;           // [segment slots, HV, K, K] transition matrices
   // backward
   const __nv_bfloat16* d_out; int64_t d_out_ts;
   const float* d_final;     // [N, HV, K, V] or null
@@ -124,6 +129,46 @@ __device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot, Ch
   }
   __syncthreads();
   return *sh;
+}
+
+// A CTA's part of a sequence: `chunks` chunks from `first` on, segment `seg` of `segs`.  The segment slots of sequence n
+// start at cu[n] / (C seg_chunks) + n, like the chunk slots.
+struct Segment {
+  int64_t n, start, len;    // the sequence
+  int64_t first, chunks;
+  int64_t seg, segs;        // segs 0: no such segment
+};
+__device__ __forceinline__ int64_t first_segment(const ScanParams& p, int64_t n, int64_t start) {
+  return p.cu == nullptr ? n * p.seq_segs : start / (static_cast<int64_t>(kC) * p.seg_chunks) + n;
+}
+__device__ __forceinline__ Segment segment_of(const ScanParams& p, int64_t n, int64_t slot) {
+  Segment s;
+  s.n = n;
+  seq_range(p, n, s.start, s.len);
+  const int64_t chunks = (s.len + kC - 1) / kC;
+  if (p.seg_chunks == 0) {
+    s.seg = 0, s.segs = 1, s.first = 0, s.chunks = chunks;
+    return s;
+  }
+  s.segs = chunks == 0 ? 1 : (chunks + p.seg_chunks - 1) / p.seg_chunks;
+  s.seg = slot - first_segment(p, n, s.start);
+  s.first = s.seg * p.seg_chunks;
+  s.chunks = chunks - s.first < p.seg_chunks ? chunks - s.first : p.seg_chunks;
+  if (s.seg < 0 || s.seg >= s.segs) s.segs = 0;
+  return s;
+}
+// The segment of a slot (all threads of the block call it; `sh` is shared).
+__device__ __forceinline__ Segment locate_segment(const ScanParams& p, int64_t slot, int64_t* sh) {
+  if (p.seg_chunks == 0) return segment_of(p, slot, slot);
+  if (p.cu == nullptr) return segment_of(p, slot / p.seq_segs, slot);
+  if (threadIdx.x == 0) *sh = -1;
+  __syncthreads();
+  for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x)
+    if (segment_of(p, n, slot).segs) *sh = n;
+  __syncthreads();
+  Segment s{};
+  if (*sh >= 0) s = segment_of(p, *sh, slot);
+  return s;
 }
 
 // ---------------------------------------------------------------- decays

@@ -12,8 +12,13 @@ Tolerances, from the arithmetic and the number formats:
   results' largest value by less than a factor of 4 (half the square root of the 128 terms, as the largest of many
   results is 2 or more standard deviations): 96 2^-22 = 2.3e-5 of the largest value.  The recurrence contracts
   (decays at most 1, |k| at most 1, beta in [0, 1]), so errors of earlier chunks do not grow.  SCAN_REL = 2.5e-5.
+* An element far below its tile's largest is held within 2^-39 of that largest (the pair's low half ends there), not
+  within 2^-22 of itself.  Decays make such elements: where everything at the start has been forgotten, results fall to
+  any size while their operands' tiles do not, and are off by up to 2^-39 of the products that forgot them.  With at most
+  8 such products in a chunk: FLOOR = 2^-36 of the largest input (values, states, gradients), absolute.
 * dg is a difference of sums over the rest of the chunk (64 tokens, random signs: a factor of 8) of q dq + k (dk_row -
-  dk_column): DG_REL = 8 SCAN_REL.
+  dk_column): DG_REL = 8 SCAN_REL of the largest value, and of the terms |q dq| + |k dk|, whose difference may vanish
+  (for a single token from a zero state it does, exactly).
 * The norm and rotation: sums of D <= 256 squares in fp32, a reciprocal square root (2 ulp), cos and sin (2 ulp) and a
   handful of products: below 32 ulp = 2^-19 of the head's largest value.  QK_REL = 2^-19; the weights' gradients, sums
   of fp32 products in fp32 and fp64, within 2^-19 of the sum of the terms' magnitudes.
@@ -25,18 +30,19 @@ import torch
 BF16_HALF_STEP = 2.0 ** -8
 SCAN_REL = 2.5e-5
 DG_REL = 8 * SCAN_REL
+FLOOR = 2.0 ** -36
 QK_REL = 2.0 ** -19
 
 
-def check(got, ref, rel, what, half_step=0.0):
-    """|got - ref| <= half_step |ref| + rel max|ref|, element by element."""
+def check(got, ref, rel, what, half_step=0.0, floor=0.0):
+    """|got - ref| <= half_step |ref| + rel max|ref| + floor, element by element."""
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     got, ref = got.double(), ref.double()
     assert bool(torch.isfinite(got).all()), f"{what}: non-finite values"
     if ref.numel() == 0:
         return
     # the rounding is of the computed value, itself within rel max|ref| of ref
-    bound = half_step * ref.abs() + (1 + half_step) * rel * ref.abs().max()
+    bound = half_step * ref.abs() + (1 + half_step) * (rel * ref.abs().max() + floor)
     over = (got - ref).abs() - bound
     assert float(over.max()) <= 0, (f"{what}: {int((over > 0).sum())} of {ref.numel()} elements off, worst by "
                                     f"{float(over.max()):.3e}, largest reference {float(ref.abs().max()):.3e}")

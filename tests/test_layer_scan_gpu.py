@@ -54,23 +54,26 @@ def double(*xs):
 
 def check_scan(out, final, q, k, v, g, beta, state, cu, scale):
     ro, rs = ref.scan(*double(q, k, v, g, beta), state.double(), cu, scale)
+    floor = ref.FLOOR * max(float(x.abs().max()) for x in (v, state) if x.numel())
     for n in range(len(cu) - 1):  # a sequence's results are held to its own magnitude
         a, b = int(cu[n]), int(cu[n + 1])
         if b > a:
-            ref.check(out[a:b], ro[a:b], ref.SCAN_REL, f"out of sequence {n}", ref.BF16_HALF_STEP)
-        ref.check(final[n], rs[n], ref.SCAN_REL, f"state of sequence {n}")
+            ref.check(out[a:b], ro[a:b], ref.SCAN_REL, f"out of sequence {n}", ref.BF16_HALF_STEP, floor * scale)
+        ref.check(final[n], rs[n], ref.SCAN_REL, f"state of sequence {n}", floor=floor)
 
 
 LENGTHS = [
     ([1], 1), ([2], 3), ([16], 2), ([17, 15, 1], 2), ([63, 64, 65], 2), ([128], 1), ([129, 0, 31], 2), ([0, 5, 0, 0, 70, 0], 1),
     ([100, 1, 219], 4), ([7] * 40, 3), ([300, 200], 16), ([90] * 8, 20),
 ]
+# walked in segments of 8 chunks: one to five of them, the last from one token to full
+LONG = [([64 * 24], 2), ([1600], 1), ([64 * 16 + 1, 0, 500, 64 * 8], 2), ([2100, 1, 70], 1)]
 
 
-@pytest.mark.parametrize("lens,H", LENGTHS)
+@pytest.mark.parametrize("lens,H", LENGTHS + LONG)
 @pytest.mark.parametrize("with_state", [False, True])
 def test_scan_lengths(lens, H, with_state, cuda_device):
-    q, k, v, g, beta, cu = inputs(lens, H, seed=len(lens) + H)
+    q, k, v, g, beta, cu = inputs(lens, H, "mild" if (lens, H) in LONG else "softplus", seed=len(lens) + H)
     state = states(len(lens), H, 5) if with_state else None
     out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu)
     check_scan(out, final, q, k, v, g, beta, state if with_state else torch.zeros_like(final), cu.tolist(), K ** -0.5)
@@ -177,6 +180,25 @@ def test_scan_slots(cuda_device):
         assert torch.equal(other[s], pool[s]) if s in (4, 0, 2) else bool((other[s] == 3).all())
 
 
+def test_scan_slots_of_long_sequences(cuda_device):
+    """In place through segments, with an inactive sequence among them; and the dense form's segments."""
+    H, lens = 2, [1300, 900, 600]
+    q, k, v, g, beta, cu = inputs(lens, H, "mild", seed=32)
+    pool, c = states(4, H, 8), cu.tolist()
+    slots = torch.tensor([3, -1, 0], dtype=torch.int32, device=cuda_device)
+    before = pool.clone()
+    out, _ = kda.kda_scan(q, k, v, g, beta, pool, cu_seqlens=cu, slot_idx=slots)
+    for n, s in ((0, 3), (2, 0)):
+        a, b = c[n], c[n + 1]
+        check_scan(out[a:b], pool[s:s + 1], q[a:b], k[a:b], v[a:b], g[a:b], beta[a:b], before[s:s + 1], [0, b - a], K ** -0.5)
+    assert bool((out[c[1]:c[2]] == 0).all()) and torch.equal(pool[1:3], before[1:3])
+    T = 1700  # two sequences of 27 chunks
+    q, k, v, g, beta, cu = inputs([T] * 2, 1, "mild", seed=33)
+    state = states(2, 1, 4)
+    out, final = kda.kda_scan(*(x.view(2, T, *x.shape[1:]) for x in (q, k, v, g, beta)), state)
+    check_scan(out.view(2 * T, 1, V), final, q, k, v, g, beta, state, cu.tolist(), K ** -0.5)
+
+
 def test_scan_bad_offsets_stay_in_bounds(cuda_device):
     """Offsets that decrease or leave the rows are clamped: an error in them cannot reach other memory."""
     q, k, v, g, beta, _ = inputs([100], 2, seed=41)
@@ -186,6 +208,13 @@ def test_scan_bad_offsets_stay_in_bounds(cuda_device):
     kda.kda_scan(q, k, v, g, beta, cu_seqlens=cu, out=out)
     torch.cuda.synchronize()
     assert bool((guard[:100] == 5).all()) and bool((guard[200:] == 5).all())
+    # with segments
+    q, k, v, g, beta, _ = inputs([2000], 1, seed=42)
+    cu = torch.tensor([1990, 0, 2000, 3, 2 ** 31 - 1], dtype=torch.int32, device=cuda_device)
+    guard = torch.full((2200, 1, V), 5.0, dtype=torch.bfloat16, device=cuda_device)
+    kda.kda_scan(q, k, v, g, beta, cu_seqlens=cu, out=guard[100:2100])
+    torch.cuda.synchronize()
+    assert bool((guard[:100] == 5).all()) and bool((guard[2100:] == 5).all())
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
@@ -208,20 +237,26 @@ def test_scan_nan_stays_in_its_sequence_and_head(bad, cuda_device):
         assert torch.equal(a[m], b[m]), name
 
 
-def check_gradients(got, want, cu):
+def check_gradients(got, want, cu, q, k, d_out, d_final):
+    """Each sequence's gradients to their own magnitude.  Values and states are of the order of 1 here, so the largest input
+    of the gradients' recurrence is that of d_out and d_final."""
+    floor = ref.FLOOR * max(float(d_out.abs().max()), 0.0 if d_final is None else float(d_final.abs().max()))
     for name, a, b in zip(GRADS, got, want):
         rel = ref.DG_REL if name == "dg" else ref.SCAN_REL
         step = ref.BF16_HALF_STEP if name in ("dq", "dk", "dv") else 0.0
         for n in range(len(cu) - 1):
             lo, hi = (n, n + 1) if name == "dstate" else (int(cu[n]), int(cu[n + 1]))
             if hi > lo:
-                ref.check(a[lo:hi], b[lo:hi], rel, f"{name} of sequence {n}", step)
+                terms = 0.0
+                if name == "dg":
+                    terms = rel * float((q[lo:hi].double() * want[0][lo:hi]).abs().max() + (k[lo:hi].double() * want[1][lo:hi]).abs().max())
+                ref.check(a[lo:hi], b[lo:hi], rel, f"{name} of sequence {n}", step, floor + terms)
 
 
-@pytest.mark.parametrize("lens,H", [x for x in LENGTHS if sum(x[0]) * x[1] < 4000])
+@pytest.mark.parametrize("lens,H", [x for x in LENGTHS if sum(x[0]) * x[1] < 4000] + LONG)
 @pytest.mark.parametrize("with_state", [False, True])
 def test_scan_gradients_lengths(lens, H, with_state, cuda_device):
-    q, k, v, g, beta, cu = inputs(lens, H, seed=61 + H)
+    q, k, v, g, beta, cu = inputs(lens, H, "mild" if (lens, H) in LONG else "softplus", seed=61 + H)
     N, c = len(lens), cu.tolist()
     d_out = torch.randn(sum(lens), H, V, device=cuda_device, generator=torch.Generator(device=cuda_device).manual_seed(1)).bfloat16()
     state = states(N, H, 5) if with_state else None
@@ -234,7 +269,7 @@ def test_scan_gradients_lengths(lens, H, with_state, cuda_device):
     again = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)
     for name, a, b in zip(GRADS, got, again):
         assert torch.equal(a, b), f"{name}: computed from the saved pass and anew"
-    check_gradients(got, want[2:], c)
+    check_gradients(got, want[2:], c, q, k, d_out, d_final)
 
 
 @pytest.mark.parametrize("decay", ["softplus", "mild", "none", "strong", "mixed", "growing"])
@@ -253,7 +288,7 @@ def test_scan_gradients_decays_and_edges(decay, edge, cuda_device):
     state, d_final, c = states(2, 2, 6), states(2, 2, 7), cu.tolist()
     want = ref.scan_gradients(q, k, v, g, beta, state, c, 0.7, d_out, d_final)
     got = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu, scale=0.7)
-    check_gradients(got, want[2:], c)
+    check_gradients(got, want[2:], c, q, k, d_out, d_final)
 
 
 def test_scan_gradients_against_differences(cuda_device):
