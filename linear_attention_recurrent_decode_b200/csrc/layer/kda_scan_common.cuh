@@ -237,25 +237,51 @@ __device__ __forceinline__ SubFactors sub_factors(const float (&g)[kB], float (&
   return f;
 }
 
-// The log-decays, keys and queries of sub-block b's 16 tokens in channel `col` (a head's column), zeros behind the
-// chunk.  Every load is issued ahead of any use and without a branch (rows behind the chunk read its last one): as
-// conditional loads they ran one after the other, 17000 cycles against 4000.
-__device__ __forceinline__ void load_sub_block(const ScanParams& p, int64_t tok, int tc, int b, int64_t col, float (&g)[kB],
-                                               float (&k)[kB], float (&q)[kB]) {
-  __nv_bfloat16 kr[kB], qr[kB];
-#pragma unroll
-  for (int t = 0; t < kB; ++t) {
-    const int64_t tk = tok + (b * kB + t < tc ? b * kB + t : tc - 1);
-    g[t] = __ldg(p.g + tk * p.g_ts + col);
-    kr[t] = p.k[tk * p.k_ts + col];
-    qr[t] = p.q[tk * p.q_ts + col];
+// A chunk's log-decays, keys and queries as they lie in memory, in shared memory.
+struct RawRows {
+  float g[kC][kK];
+  __nv_bfloat16 k[kC][kK], q[kC][kK];
+};
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Starts the copies of the chunk's rows (rows behind its end: its last one's).  Asynchronous copies need no registers:
+// loaded into registers by the threads that use them, 48 values each, they came in batches, 8900 cycles against 3500.
+template <int THREADS>
+__device__ __forceinline__ void fetch_rows(const ScanParams& p, int64_t tok, int tc, int64_t h, float (*g)[kK], __nv_bfloat16 (*k)[kK],
+                                           __nv_bfloat16 (*q)[kK]) {
+  const int tid = threadIdx.x;
+  for (int e = tid; e < kC * kK / 8; e += THREADS) {
+    const int t = e >> 4, i = (e & 15) * 8;
+    const int64_t row = tok + (t < tc ? t : tc - 1);
+    cp_async16(&k[t][i], p.k + row * p.k_ts + h * kK + i);
+    cp_async16(&q[t][i], p.q + row * p.q_ts + h * kK + i);
   }
+  if (((reinterpret_cast<uintptr_t>(p.g) & 15) | (p.g_ts & 3)) == 0) {
+    for (int e = tid; e < kC * kK / 4; e += THREADS) {
+      const int t = e >> 5, i = (e & 31) * 4;
+      cp_async16(&g[t][i], p.g + (tok + (t < tc ? t : tc - 1)) * p.g_ts + h * kK + i);
+    }
+  } else {  // g may lie on any 4 bytes
+    for (int e = tid; e < kC * kK; e += THREADS) {
+      const int t = e >> 7, i = e & (kK - 1);
+      cp_async4(&g[t][i], p.g + (tok + (t < tc ? t : tc - 1)) * p.g_ts + h * kK + i);
+    }
+  }
+}
+// Sub-block b's 16 tokens in channel ch, zeros behind the chunk.
+__device__ __forceinline__ void read_sub_block(const float (*gs)[kK], const __nv_bfloat16 (*ks)[kK], const __nv_bfloat16 (*qs)[kK], int tc,
+                                               int b, int ch, float (&g)[kB], float (&k)[kB], float (&q)[kB]) {
 #pragma unroll
   for (int t = 0; t < kB; ++t) {
     const bool in = b * kB + t < tc;
-    g[t] = in ? log_decay(g[t]) : 0.f;
-    k[t] = in ? __bfloat162float(kr[t]) : 0.f;
-    q[t] = in ? __bfloat162float(qr[t]) : 0.f;
+    g[t] = in ? log_decay(gs[b * kB + t][ch]) : 0.f;
+    k[t] = in ? __bfloat162float(ks[b * kB + t][ch]) : 0.f;
+    q[t] = in ? __bfloat162float(qs[b * kB + t][ch]) : 0.f;
   }
 }
 

@@ -364,7 +364,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       dkc[n][3] *= b1;
     }
   }
-  __syncthreads();  // every warp is done with S0 (and with the sums over it)
+  __syncthreads();  // every warp is done with S0 and dS1
+  // The raw rows over dS1, for step 6.
+  RawRows& raw = *reinterpret_cast<RawRows*>(sm.ds);
+  static_assert(sizeof(RawRows) <= sizeof(sm.ds), "the raw rows fit");
+  fetch_rows<kGradThreads>(p, pos.tok, tc, h, raw.g, raw.k, raw.q);
   // ---- 5. dP and dA over S0, 16 x 16 a warp (none above the diagonal)
   if (const int ti = warp >> 2, si = warp & 3; si <= ti) {
     const int t = ti * 16 + (lane >> 2), s = si * 16 + 2 * (lane & 3);
@@ -401,12 +405,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         pr.da[tt][ss] = ss < tt ? ca[n][e] * b : 0.f;
       }
   }
-  __syncthreads();  // every warp is done with the operand tiles
+  cp_async_wait_all();
+  __syncthreads();  // every warp is done with the operand tiles, the raw rows are there
   // ---- 6. decay factors
   const int ch = tid & (kK - 1), sub = tid >> 7;
   {
     float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
-    load_sub_block(p, pos.tok, tc, sub, h * kK + ch, g, kv, qv);
+    read_sub_block(raw.g, raw.k, raw.q, tc, sub, ch, g, kv, qv);
+    __syncthreads();  // the factors go over them
     const SubFactors f = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
@@ -461,6 +467,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       scale_cols(dkr, &sm.erd[J][col]);
     }
   }
+  __nv_bfloat162 qk[4][2][2];  // q and k again, at this thread's elements (rows behind the chunk: the last one's)
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int64_t tk = pos.tok + (row + hf * 8 < tc ? row + hf * 8 : tc - 1);
+      qk[n][hf][0] = *reinterpret_cast<const __nv_bfloat162*>(p.q + tk * p.q_ts + h * kK + col + n * 8);
+      qk[n][hf][1] = *reinterpret_cast<const __nv_bfloat162*>(p.k + tk * p.k_ts + h * kK + col + n * 8);
+    }
   for (int J = kNB - 1; J >= I; --J) {  // column blocks: later tokens
     scale_cols(dkc, &(J > I ? sm.eru : sm.erd)[J][col]);
     if (J == I && exact) break;
@@ -495,15 +510,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         dkr[n][e] += d.y;
         dkc[n][e] += d.z;
       }
-    }
-  __nv_bfloat162 qk[4][2][2];  // q and k again, at this thread's elements (rows behind the chunk: the last one's)
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int64_t tk = pos.tok + (row + hf * 8 < tc ? row + hf * 8 : tc - 1);
-      qk[n][hf][0] = *reinterpret_cast<const __nv_bfloat162*>(p.q + tk * p.q_ts + h * kK + col + n * 8);
-      qk[n][hf][1] = *reinterpret_cast<const __nv_bfloat162*>(p.k + tk * p.k_ts + h * kK + col + n * 8);
     }
   __syncthreads();  // the factors are dead: the decays' gradients go over them
   // ---- 8. dq, dk; dg by a sum from the chunk's end

@@ -23,10 +23,6 @@ struct JoinSmem {
   float s[kK][kJoinCols];
 };
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-
 template <bool BACK>
 __global__ void __launch_bounds__(kJoinThreads) kda_scan_join_kernel(const __grid_constant__ ScanParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];

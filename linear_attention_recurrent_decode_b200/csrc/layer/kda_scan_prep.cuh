@@ -53,13 +53,16 @@ enum PrepMax { kMxV, kMxKt, kMxQt, kMxKe, kMxR32K, kMxR32Q, kMxC32, kMxR16K, kMx
 
 struct PrepSmem {
   union {
-    PrepFactors f;
+    struct {
+      PrepFactors f;
+      __nv_bfloat16 q[kC][kK];          // the raw queries
+    };
     PrepTiles t;
   };
   unsigned char vt[Record::kPlane];     // V tile [t][v]
   float a[kC][kAP];                     // A
   float pm[kC][kAP];                    // P; then the tile M
-  float y[kC][kAP];                     // Y
+  float y[kC][kAP];                     // Y; a, pm and y first hold the raw log-decays and keys
   Sum end[kNB][kK];                     // log-decay of a sub-block
   float up[kNB][kK], dn[kNB][kK];       // to Kt and Qt, to Ke
   float x32[kNB][kK], x16[kNB][kK];     // to the tiles r32 or c32, r16 or c16
@@ -69,6 +72,8 @@ struct PrepSmem {
   ChunkPos pos;
 };
 static_assert(2 * kC * kC * 2 <= sizeof(float) * kC * kAP, "the M tile fits into pm");
+static_assert(offsetof(PrepSmem, y) - offsetof(PrepSmem, a) >= sizeof(float) * kC * kK && sizeof(float) * kC * kAP >= 2 * kC * kK,
+              "the raw rows fit");
 static_assert(sizeof(PrepSmem) <= 232448, "shared memory of an SM");
 
 __device__ __forceinline__ void block_max(uint32_t* slot, float m, int lane) {
@@ -131,11 +136,12 @@ __device__ __forceinline__ void tf32_b(F f, int lane, uint32_t (&h)[2], uint32_t
 // Y's block of ROWS rows from r0 under its diagonal blocks, columns c0 .. c0 + 7 of the ROWS columns from r0 - ROWS:
 //   Y21 = (I - Y2 diag(beta2)) A21 (I - diag(beta1) Y1).
 // One warp; it reads and writes these columns alone (and finished diagonal blocks).
+// Returns the largest magnitude this thread wrote.
 template <int ROWS>
-__device__ __forceinline__ void solve_below(PrepSmem& sm, int r0, int c0, int lane) {
+__device__ __forceinline__ float solve_below(PrepSmem& sm, int r0, int c0, int lane) {
   constexpr int kM = ROWS / 16;
   const int k0 = r0 - ROWS, r = lane >> 2, c = lane & 3, first = (c0 - k0) / 8;
-  float x[kM][4];
+  float x[kM][4], largest = 0.f;
 #pragma unroll
   for (int m = 0; m < kM; ++m) {
     float lo[4] = {}, hi[4] = {};
@@ -174,8 +180,11 @@ __device__ __forceinline__ void solve_below(PrepSmem& sm, int r0, int c0, int la
 #pragma unroll
   for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sm.y[r0 + m * 16 + r + (e >> 1) * 8][c0 + 2 * c + (e & 1)] = x[m][e];
-  __syncwarp();
+    for (int e = 0; e < 4; ++e) {
+      sm.y[r0 + m * 16 + r + (e >> 1) * 8][c0 + 2 * c + (e & 1)] = x[m][e];
+      largest = fmaxf(largest, fabsf(x[m][e]));
+    }
+  return largest;
 }
 
 // Elements s0 .. s0 + 7 of row t of a lower triangular matrix stored by blocks of 16 (nothing above the diagonal blocks).
@@ -226,6 +235,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   float* const hdr = reinterpret_cast<float*>(rec);
   auto scale_of = [&](PrepMax i) { return pow2_scale(__uint_as_float(sm.mx[i])); };
 
+  float (*const graw)[kK] = reinterpret_cast<float (*)[kK]>(&sm.a[0][0]);
+  __nv_bfloat16 (*const kraw)[kK] = reinterpret_cast<__nv_bfloat16 (*)[kK]>(&sm.y[0][0]);
+  fetch_rows<kPrepThreads>(p, pos.tok, tc, h, graw, kraw, sm.q);
   // v: 16-byte pieces, kept in registers until the scale is known
   uint4 vraw[2];
 #pragma unroll
@@ -239,7 +251,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   float m_ku = 0.f, m_qu = 0.f, m_kd = 0.f;
   {
     float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
-    load_sub_block(p, pos.tok, tc, b, h * kK + ch, g, kv, qv);
+    cp_async_wait_all();
+    __syncthreads();
+    read_sub_block(graw, kraw, sm.q, tc, b, ch, g, kv, qv);
     sf = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
@@ -426,6 +440,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
 
   // ---- 6. Y = A (I + diag(beta) A)^-1: four warps, the diagonal blocks by substitution, then pairs of blocks
   if (warp < 4) {
+    float m = 0.f;
     if (lane < kB) {
       const int r0 = warp * kB;
       float x[kB];
@@ -438,16 +453,15 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
         for (int r = s + 1; r < kB; ++r) x[r] = fmaf(sm.a[r0 + r][r0 + s], w, x[r]);
       }
 #pragma unroll
-      for (int r = 0; r < kB; ++r) sm.y[r0 + r][r0 + lane] = x[r];
+      for (int r = 0; r < kB; ++r) {
+        sm.y[r0 + r][r0 + lane] = x[r];
+        m = fmaxf(m, fabsf(x[r]));
+      }
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
-    solve_below<16>(sm, 16 + (warp >> 1) * 32, (warp >> 1) * 32 + (warp & 1) * 8, lane);
+    m = fmaxf(m, solve_below<16>(sm, 16 + (warp >> 1) * 32, (warp >> 1) * 32 + (warp & 1) * 8, lane));
     asm volatile("bar.sync 1, 128;" ::: "memory");
-    solve_below<32>(sm, 32, warp * 8, lane);
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    float m = 0.f;
-    for (int e = tid; e < kC * kC; e += 128)
-      if (((e >> 4) & 3) <= (e >> 10)) m = fmaxf(m, fabsf(sm.y[e >> 6][e & 63]));
+    m = fmaxf(m, solve_below<32>(sm, 32, warp * 8, lane));
     block_max(&sm.mx[kMxY], m, lane);
   } else {  // the other warps: P to the record
     const int w = tid - 128;
