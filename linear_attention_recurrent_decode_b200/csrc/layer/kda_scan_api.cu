@@ -31,8 +31,6 @@ cudaError_t prepare_kernels() {
   allow(ks::kda_scan_prep_kernel, static_cast<int>(sizeof(ks::PrepSmem)));
   allow(ks::kda_scan_forward_kernel, kChainSmem);
   allow(ks::kda_scan_backward_kernel, kChainSmem);
-  allow(ks::kda_scan_join_kernel<false>, static_cast<int>(sizeof(ks::JoinSmem)));
-  allow(ks::kda_scan_join_kernel<true>, static_cast<int>(sizeof(ks::JoinSmem)));
   allow(ks::kda_scan_grad_kernel, static_cast<int>(sizeof(ks::GradSmem)));
   if (e == cudaSuccess && bit) ready.fetch_or(bit, std::memory_order_relaxed);
   return e;
@@ -170,7 +168,7 @@ bool launch_forward(ks::ScanParams p, int64_t slots, int64_t seg_slots, kda_stre
   if (p.seg_chunks > 0) {
     p.transitions = 1;
     if (!launch(ks::kda_scan_forward_kernel, seg_slots * p.HV * 2, ks::kForwardThreads, kChainSmem, stream, p) ||
-        !launch(ks::kda_scan_join_kernel<false>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, sizeof(ks::JoinSmem), stream, p))
+        !launch(ks::kda_scan_join_kernel<false>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, 0, stream, p))
       return false;
     p.transitions = 0;
   }
@@ -180,7 +178,7 @@ bool launch_backward(ks::ScanParams p, int64_t slots, int64_t seg_slots, kda_str
   if (p.seg_chunks > 0) {
     p.transitions = 1;
     if (!launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kBackwardThreads, kChainSmem, stream, p) ||
-        !launch(ks::kda_scan_join_kernel<true>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, sizeof(ks::JoinSmem), stream, p))
+        !launch(ks::kda_scan_join_kernel<true>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, 0, stream, p))
       return false;
     p.transitions = 0;
   }
