@@ -254,13 +254,16 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
   const int64_t unit = p.transitions ? blockIdx.x >> 1 : blockIdx.x, slot = unit / p.HV, h = unit - slot * p.HV;
   const bool map = p.transitions && (blockIdx.x & 1);
   const Segment seg = locate_segment(p, slot, &sm.seq);
-  if (seg.segs == 0) return;
   const bool last = seg.seg == seg.segs - 1;
-  // The last segment's end is not a start; M is for the segments behind the first (the last's for the backward pass).
-  if (p.transitions && (map ? seg.seg == 0 || (last && !p.save) : last)) return;
+  // The last segment's end is nobody's start, and the first's start is known: it has no use for M.
+  if (seg.segs == 0 || (p.transitions && (last || (map && seg.seg == 0)))) {
+    wait_upstream();
+    return;
+  }
   const int64_t n = seg.n, start = seg.start + seg.first * kC, len = seg.len - seg.first * kC, chunks = seg.chunks;
   const int64_t blk = state_block(p, n);
   if (blk < 0) {  // inactive: zero outputs
+    wait_upstream();
     if (!p.transitions) {
       const int64_t rows = len < chunks * kC ? len : chunks * kC;
       for (int64_t t = threadIdx.x; t < rows * 16; t += kForwardThreads)
@@ -273,6 +276,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
   const int64_t sblk = (blk * p.HV + h) * kK * kV, gblk = (slot * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
   unsigned char* rec = record(p, first_slot(p, n, seg.start) + seg.first, h);
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  wait_upstream();
   Waiter w;
   if (warp < kComputeWarps) {
     const int part = warp >> 2;
@@ -446,7 +450,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
   const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  wait_upstream();  // this may be its call's first kernel
   const Segment seg = locate_segment(p, slot, &sm.seq);
+  // The first segment's start gradient is the result itself, and nobody's end.
   if (seg.segs == 0 || (p.transitions && seg.seg == 0)) return;
   const int64_t n = seg.n, start = seg.start + seg.first * kC, len = seg.len - seg.first * kC, chunks = seg.chunks;
   chain_init(sm, kComputeWarps);

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   if (tid < kNB) sm.exact[tid] = 0;
   const ChunkPos pos = locate(p, slot, &sm.pos);
   const int tc = pos.tc;
+  wait_upstream();
   if (tc == 0) return;
   __syncthreads();
   const unsigned char* const rec = record(p, slot, h);

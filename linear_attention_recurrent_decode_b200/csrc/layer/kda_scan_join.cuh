@@ -9,8 +9,9 @@
 // steps' latency bounds it: each element of a matrix is used once per CTA, so the
 // fragments of the tf32 products (pairs, three products: fp32 accuracy) go from
 // global memory straight to registers, a step ahead, and only the columns pass
-// through shared memory.  Measured: 1.6 us a step, against 5 us for fp32 products
-// with the matrix staged in shared memory.
+// through shared memory.  Measured: 3 us a step (its
+// loads' latency), against 5 us for fp32 products with the matrix staged in
+// shared memory.
 #pragma once
 
 #include "kda_scan_common.cuh"
@@ -30,6 +31,7 @@ __global__ void __launch_bounds__(kJoinThreads, 1) kda_scan_join_kernel(const __
   int64_t start, len;
   seq_range(p, n, start, len);
   const int64_t chunks = (len + kC - 1) / kC, segs = (chunks + p.seg_chunks - 1) / p.seg_chunks;
+  wait_upstream();
   if (segs < 3 || state_block(p, n) < 0) return;
   const int64_t slot0 = first_segment(p, n, start), steps = segs - 2, first = BACK ? segs - 2 : 1;
   auto block = [&](int64_t g) { return ((slot0 + g) * p.HV + h) * kK * kV; };

@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  wait_upstream();
   if (tid < kMxCount) sm.mx[tid] = 0;
   if (tid < kNB) sm.exact[tid] = 0;
   const ChunkPos pos = locate(p, slot, &sm.pos);
