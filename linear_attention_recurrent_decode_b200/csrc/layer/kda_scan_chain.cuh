@@ -56,7 +56,6 @@ struct ChainSmem {
   uint64_t d_out;                   // backward: dO is written
   uint64_t end;
   uint32_t tmem;
-  int64_t seq;
 };
 static_assert(sizeof(ChainSmem) <= 232448, "shared memory of an SM");
 
@@ -251,9 +250,10 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
   // the transitions' call: E and M of a segment in neighbouring blocks
-  const int64_t unit = p.transitions ? blockIdx.x >> 1 : blockIdx.x, slot = unit / p.HV, h = unit - slot * p.HV;
+  int64_t slot, h;
+  slot_and_head(p, p.transitions ? blockIdx.x >> 1 : blockIdx.x, slot, h);
   const bool map = p.transitions && (blockIdx.x & 1);
-  const Segment seg = locate_segment(p, slot, &sm.seq);
+  const Segment seg = locate_segment(p, slot);
   const bool last = seg.seg == seg.segs - 1;
   // The last segment's end is nobody's start, and the first's start is known: it has no use for M.
   if (seg.segs == 0 || (p.transitions && (last || (map && seg.seg == 0)))) {
@@ -449,9 +449,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, quarter = warp & 3, v = quarter * 32 + lane;
-  const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  int64_t slot, h;
+  slot_and_head(p, blockIdx.x, slot, h);
   wait_upstream();  // this may be its call's first kernel
-  const Segment seg = locate_segment(p, slot, &sm.seq);
+  const Segment seg = locate_segment(p, slot);
   // The first segment's start gradient is the result itself, and nobody's end.
   if (seg.segs == 0 || (p.transitions && seg.seg == 0)) return;
   const int64_t n = seg.n, start = seg.start + seg.first * kC, len = seg.len - seg.first * kC, chunks = seg.chunks;

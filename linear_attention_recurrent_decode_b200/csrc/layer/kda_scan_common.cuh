@@ -59,7 +59,9 @@ struct Record {
   static constexpr int kRt = kKe + 2 * kPlane;     // Rt^T fp32, [t / 4][v][4]
   static constexpr int64_t kForward = kRt + kV * kC * 4;
   static constexpr int kY = static_cast<int>(kForward);  // beta_t Y [t][s]
-  static constexpr int kS = kY + kC * kC * 4;      // S0^T [v][i], 32 KB a plane
+  static constexpr int kDn = kY + kC * kC * 4;     // fp32 [4][128]: from k dn to Ke, per sub-block and channel
+  static constexpr int kDnBytes = kNB * kK * 4;
+  static constexpr int kS = kDn + kDnBytes;        // S0^T [v][i], 32 KB a plane
   static constexpr int kR = kS + kV * kK * 4;      // r^T  [v][t]
   static constexpr int kDS = kR + 2 * kPlane;      // dS1^T [v][i]
   static constexpr int kDU = kDS + kV * kK * 4;    // dU^T [v][t]
@@ -104,31 +106,43 @@ struct ChunkPos {
   int64_t n, tok;  // sequence, first token of the chunk
   int32_t tc;      // tokens of the chunk; 0: no such chunk
 };
-// The chunk of a chunk slot (all threads of the block call it; `sh` is shared).
-__device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot, ChunkPos* sh) {
+// Block index to (slot, head).  32 bits: the launches keep their grids below 2^31, and a 64-bit division takes a
+// thousand cycles of every block's life.
+__device__ __forceinline__ void slot_and_head(const ScanParams& p, uint32_t block, int64_t& slot, int64_t& h) {
+  const uint32_t q = block / static_cast<uint32_t>(p.HV);
+  slot = q;
+  h = block - q * static_cast<uint32_t>(p.HV);
+}
+// The sequence for which `is(n)` holds, or -1; the lanes of each warp search on their own.
+template <typename F>
+__device__ __forceinline__ int64_t find_sequence(const ScanParams& p, F is) {
+  for (int64_t n0 = 0; n0 < p.N; n0 += 32) {
+    const int64_t n = n0 + (threadIdx.x & 31);
+    const uint32_t found = __ballot_sync(0xffffffffu, n < p.N && is(n));
+    if (found) return n0 + __ffs(static_cast<int>(found)) - 1;
+  }
+  return -1;
+}
+// The chunk of a chunk slot (whole warps call it).
+__device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot) {
+  ChunkPos c{0, 0, 0};
+  int64_t start, len, t;
   if (p.cu == nullptr) {
-    ChunkPos c;
     c.n = slot / p.seq_chunks;
-    const int64_t t = (slot - c.n * p.seq_chunks) * kC;
-    c.tok = c.n * p.T + t;
-    c.tc = static_cast<int32_t>(p.T - t < kC ? p.T - t : kC);
-    if (state_block(p, c.n) < 0) c.tc = 0;
-    return c;
+  } else {
+    c.n = find_sequence(p, [&](int64_t n) {
+      int64_t a, l;
+      seq_range(p, n, a, l);
+      const int64_t at = (slot - first_slot(p, n, a)) * kC;
+      return at >= 0 && at < l;
+    });
+    if (c.n < 0) return c;
   }
-  if (threadIdx.x == 0) sh->tc = 0;
-  __syncthreads();
-  for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x) {
-    int64_t start, len;
-    seq_range(p, n, start, len);
-    const int64_t t = (slot - first_slot(p, n, start)) * kC;
-    if (t >= 0 && t < len) {
-      sh->n = n;
-      sh->tok = start + t;
-      sh->tc = state_block(p, n) < 0 ? 0 : static_cast<int32_t>(len - t < kC ? len - t : kC);
-    }
-  }
-  __syncthreads();
-  return *sh;
+  seq_range(p, c.n, start, len);
+  t = (slot - first_slot(p, c.n, start)) * kC;
+  c.tok = start + t;
+  if (state_block(p, c.n) >= 0) c.tc = static_cast<int32_t>(len - t < kC ? len - t : kC);
+  return c;
 }
 
 // A CTA's part of a sequence: `chunks` chunks from `first` on, segment `seg` of `segs`.  The segment slots of sequence n
@@ -157,18 +171,12 @@ __device__ __forceinline__ Segment segment_of(const ScanParams& p, int64_t n, in
   if (s.seg < 0 || s.seg >= s.segs) s.segs = 0;
   return s;
 }
-// The segment of a slot (all threads of the block call it; `sh` is shared).
-__device__ __forceinline__ Segment locate_segment(const ScanParams& p, int64_t slot, int64_t* sh) {
+// The segment of a slot (whole warps call it).
+__device__ __forceinline__ Segment locate_segment(const ScanParams& p, int64_t slot) {
   if (p.seg_chunks == 0) return segment_of(p, slot, slot);
-  if (p.cu == nullptr) return segment_of(p, slot / p.seq_segs, slot);
-  if (threadIdx.x == 0) *sh = -1;
-  __syncthreads();
-  for (int64_t n = threadIdx.x; n < p.N; n += blockDim.x)
-    if (segment_of(p, n, slot).segs) *sh = n;
-  __syncthreads();
-  Segment s{};
-  if (*sh >= 0) s = segment_of(p, *sh, slot);
-  return s;
+  const int64_t n = p.cu == nullptr ? slot / p.seq_segs : find_sequence(p, [&](int64_t m) { return segment_of(p, m, slot).segs > 0; });
+  if (n < 0) return Segment{};
+  return segment_of(p, n, slot);
 }
 
 // ---------------------------------------------------------------- decays

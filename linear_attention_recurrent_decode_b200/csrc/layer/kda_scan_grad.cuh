@@ -38,6 +38,7 @@ struct GradSmem {
   // exp(mu), exp(md), exp(end - mu), exp(end - md) per sub-block and channel
   float emu[kNB][kK], emd[kNB][kK], eru[kNB][kK], erd[kNB][kK];
   float hdr[Record::kHdr / 4];
+  float dn[kNB][kK];                         // from k dn to Ke
   float sc[Record::kScBytes / 4];
   float tail[kNB][kK];                       // the decays' gradients, summed per sub-block
   float dbeta[8][kC];
@@ -45,7 +46,6 @@ struct GradSmem {
   uint32_t mx_do;
   int exact[kNB];
   uint64_t bar[2];
-  ChunkPos pos;
 };
 struct GradPairs {  // over s0 .. dO once those are dead
   float dp[kC][kDP], da[kC][kDP];
@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   GradSmem& sm = *reinterpret_cast<GradSmem*>(smem_raw);
   GradPairs& pr = *reinterpret_cast<GradPairs*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  int64_t slot, h;
+  slot_and_head(p, blockIdx.x, slot, h);
   if (tid == 0) {
     mbar_init(&sm.bar[0], 1);
     mbar_init(&sm.bar[1], 1);
@@ -155,16 +156,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     sm.mx_do = 0;
   }
   if (tid < kNB) sm.exact[tid] = 0;
-  const ChunkPos pos = locate(p, slot, &sm.pos);
+  const ChunkPos pos = locate(p, slot);
   const int tc = pos.tc;
   wait_upstream();
   if (tc == 0) return;
   __syncthreads();
   const unsigned char* const rec = record(p, slot, h);
   if (tid == 0) {
-    mbar_expect(&sm.bar[0], Record::kHdr + Record::kScBytes + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
+    mbar_expect(&sm.bar[0], Record::kHdr + Record::kScBytes + Record::kDnBytes + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
     bulk_load(sm.hdr, rec, Record::kHdr, &sm.bar[0]);
     bulk_load(sm.sc, rec + Record::kSc, Record::kScBytes, &sm.bar[0]);
+    bulk_load(sm.dn, rec + Record::kDn, Record::kDnBytes, &sm.bar[0]);
     bulk_load(sm.ds, rec + Record::kDU, 2 * Record::kPlane, &sm.bar[0]);
     bulk_load(sm.ds + 2 * Record::kPlane, rec + Record::kY, kC * kC * 4, &sm.bar[0]);
     bulk_load(sm.r, rec + Record::kR, 2 * Record::kPlane, &sm.bar[0]);
@@ -433,16 +435,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   const int col = i0 + 2 * (lane & 3);  // this thread's channels: col + 8 n, + 1
   __syncthreads();
   float ke_sum[4][2];
-  // Ke = k dn exp(end - md) exp(later blocks): the column accumulator times it, before the decays go in
+  // Ke is k dn times the sub-block's factor: so is the column accumulator, before the decays go in
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = col + n * 8 + e;
-      float fct = sm.erd[I][i];
-      for (int j = I + 1; j < kNB; ++j) fct *= sm.emu[j][i] * sm.eru[j][i];
-      ke_sum[n][e] = fct * (pr.kd[row][i] * dkc[n][e] + pr.kd[row + 8][i] * dkc[n][2 + e]);
-    }
+  for (int n = 0; n < 4; ++n) {
+    const float2 fct = *reinterpret_cast<const float2*>(&sm.dn[I][col + n * 8]);
+    const float2 k0 = *reinterpret_cast<const float2*>(&pr.kd[row][col + n * 8]), k1 = *reinterpret_cast<const float2*>(&pr.kd[row + 8][col + n * 8]);
+    ke_sum[n][0] = fct.x * fmaf(k0.x, dkc[n][0], k1.x * dkc[n][2]);
+    ke_sum[n][1] = fct.y * fmaf(k0.y, dkc[n][1], k1.y * dkc[n][3]);
+  }
 
   // ---- 7. the pairs
   const bool exact = sm.exact[I] != 0;

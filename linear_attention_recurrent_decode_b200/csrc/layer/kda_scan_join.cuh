@@ -25,8 +25,9 @@ template <bool BACK>
 __global__ void __launch_bounds__(kJoinThreads, 1) kda_scan_join_kernel(const __grid_constant__ ScanParams p) {
   __shared__ float col[kK][kJoinPitch];
   constexpr int kGroups = kV / kJoinCols;
-  const int64_t unit = blockIdx.x / kGroups, n = unit / p.HV, h = unit - n * p.HV;
-  const int v0 = static_cast<int>(blockIdx.x - unit * kGroups) * kJoinCols, tid = threadIdx.x;
+  int64_t n, h;
+  slot_and_head(p, blockIdx.x / kGroups, n, h);
+  const int v0 = static_cast<int>(blockIdx.x % kGroups) * kJoinCols, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   int64_t start, len;
   seq_range(p, n, start, len);

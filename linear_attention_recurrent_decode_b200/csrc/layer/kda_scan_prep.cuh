@@ -69,7 +69,6 @@ struct PrepSmem {
   float beta[kC];
   uint32_t mx[kMxCount];                // block maxima (float bits)
   int exact[kNB];
-  ChunkPos pos;
 };
 static_assert(2 * kC * kC * 2 <= sizeof(float) * kC * kAP, "the M tile fits into pm");
 static_assert(offsetof(PrepSmem, y) - offsetof(PrepSmem, a) >= sizeof(float) * kC * kK && sizeof(float) * kC * kAP >= 2 * kC * kK,
@@ -224,11 +223,12 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t slot = blockIdx.x / p.HV, h = blockIdx.x - slot * p.HV;
+  int64_t slot, h;
+  slot_and_head(p, blockIdx.x, slot, h);
   wait_upstream();
   if (tid < kMxCount) sm.mx[tid] = 0;
   if (tid < kNB) sm.exact[tid] = 0;
-  const ChunkPos pos = locate(p, slot, &sm.pos);
+  const ChunkPos pos = locate(p, slot);
   const int tc = pos.tc;
   if (tc == 0) return;
   __syncthreads();
@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     const float up = exp_of(add(before, sf.mu)), dn = exp_of(add(after, rest));
     sm.up[b][ch] = up;
     sm.dn[b][ch] = dn;
+    if (p.save) reinterpret_cast<float*>(rec + Record::kDn)[b * kK + ch] = dn;
     if (b == 0) hdr[Record::kDecay + ch] = exp_of(add(sf.end, after));
     const float x32 = exp_of(b == 0 ? add(rest, sm.end[1][ch]) : (b == 1 ? rest : (b == 2 ? sf.mu : add(sf.mu, sm.end[2][ch]))));
     const float x16 = exp_of(b & 1 ? sf.mu : rest);
