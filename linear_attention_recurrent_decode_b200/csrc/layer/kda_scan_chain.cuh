@@ -45,7 +45,7 @@ struct ChainSmem {
   unsigned char wr[2][2 * Record::kPlane], ke[2][2 * Record::kPlane];
   unsigned char qt[2 * Record::kPlane], p[kC * kC * 4];
   unsigned char hdr[2][Record::kHdr];
-  float peak[4][kParts][4];      // [exchange][part][quarter of the value columns]
+  alignas(16) float peak[4][kParts][4];      // [exchange][part][quarter of the value columns]
   float sc_s[2][4], sc_u[2][4];  // by chunk parity, for the outputs
   uint64_t full_wr[2], full_ke[2], full_hdr[2], full_qt, full_p, empty_hdr[2];
   uint64_t state, rows, scales[2];  // written by the compute warps: the state, U (or dU), the scales
@@ -171,6 +171,19 @@ __device__ __forceinline__ float quarter_max(ChainSmem& sm, int exchange, float 
   return m;
 }
 
+// The largest over all value columns, once every warp is known to have handed its own in.  S0 and r are kept for the
+// gradients with one scale each, as the products there contract the value columns; a barrier of all warps for it, twice
+// a chunk, made the chains 25 % slower.
+__device__ __forceinline__ float all_max(const ChainSmem& sm, int exchange) {
+  float m = 0.f;
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) {
+    const float4 q = *reinterpret_cast<const float4*>(&sm.peak[exchange][part][0]);
+    m = fmaxf(m, fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));
+  }
+  return m;
+}
+
 // x[n] sc as a pair, this thread's elements `first` .. of K: into tensor memory as the lane's A operand (hi, then lo), or
 // into the record's Core<kV> tile [v][element] with planes `plane` apart (apart from each other: the stores to the record
 // are issued while the products run).  With `f`, the elements times f[0 .. COUNT - 1] (shared memory).
@@ -293,13 +306,12 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
       const int b = static_cast<int>(c & 1);
       const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
       // ---- the state as a pair
-      const float sc_s = pow2_scale(quarter_max(sm, 0, abs_max(s), part, quarter));
+      const float sc_s = pow2_scale(quarter_max(sm, 2 * b, abs_max(s), part, quarter));
       fence_after_sync();
       write_pair<kK, true>(mine + Col::kState, nullptr, 0, v, part * kPartK, s, sc_s);
       tmem_wait_st();
       fence_before_sync();
       warp_arrive(&sm.state, lane);
-      if (save) write_pair<kK, false>(0, rec + Record::kS, kV * kK * 2, v, part * kPartK, s, sc_s);
       float r[kPartT];
       {
         const float4* const rt = reinterpret_cast<const float4*>(rec + Record::kRt) + part * (kPartT / 4) * kV + v;
@@ -337,12 +349,16 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
       }
       warp_arrive(&sm.scales[b], lane);
       if (save) {
-        const float sc_r = pow2_scale(quarter_max(sm, 2, abs_max(r), part, quarter));
+        // Every warp has written its state, and its largest value before that (it is overwritten two chunks on).
+        const float peak_s = all_max(sm, 2 * b);
+        // r's scale from a bound, |Rt| + 128 |Wr| |S0| (loose by some 2^8 of the 2^17 that a pair has to spare)
+        const float sc_saved = pow2_scale(peak_s), sc_r = pow2_scale(fmaf(kK * hdr[Record::kMxWr], peak_s, hdr[Record::kMxRt]));
+        write_pair<kK, false>(0, rec + Record::kS, kV * kK * 2, v, part * kPartK, s, sc_saved);
         write_pair<kC, false>(0, rec + Record::kR, Record::kPlane, v, part * kPartT, r, sc_r);
-        if (part == 0 && lane == 0) {
+        if (threadIdx.x == 0) {
           float* const sc = reinterpret_cast<float*>(rec + Record::kSc);
-          sc[Record::kScS + quarter] = sc_s;
-          sc[Record::kScR + quarter] = sc_r;
+          sc[Record::kScS] = sc_saved;
+          sc[Record::kScR] = sc_r;
         }
       }
       // ---- S1 = Diag(exp(Gamma_C)) S0 + Ke^T U

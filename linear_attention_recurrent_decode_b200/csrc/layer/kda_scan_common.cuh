@@ -48,6 +48,7 @@ struct Record {
   static constexpr int kDecay = 0;     // [128] exp(Gamma_C)
   static constexpr int kBeta = 128;    // [64]
   static constexpr int kScWr = 192, kScKe = 193, kScQt = 194, kScP = 195, kScY = 196;
+  static constexpr int kMxWr = 200, kMxRt = 201;  // the tiles' largest magnitudes
   // byte offsets
   static constexpr int kHdr = 1024;
   static constexpr int kPlane = kC * kK * 2;       // 16 KB: a plane of 64 x 128 elements
@@ -65,9 +66,9 @@ struct Record {
   static constexpr int kR = kS + kV * kK * 4;      // r^T  [v][t]
   static constexpr int kDS = kR + 2 * kPlane;      // dS1^T [v][i]
   static constexpr int kDU = kDS + kV * kK * 4;    // dU^T [v][t]
-  // Scales of the last four, floats [4] each: per 32 value columns.
+  // Scales of the last four; dS1's and dU's one per 32 value columns.
   static constexpr int kSc = kDU + 2 * kPlane;
-  static constexpr int kScS = 0, kScR = 4, kScDS = 8, kScDU = 12, kScBytes = 64;
+  static constexpr int kScS = 0, kScR = 1, kScDS = 4, kScDU = 8, kScBytes = 48;
   static constexpr int64_t kTraining = kSc + kScBytes;
 };
 constexpr int64_t kWsHeader = 256;  // word 0: the error word
@@ -257,8 +258,8 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Starts the copies of the chunk's rows (rows behind its end: its last one's).  Asynchronous copies need no registers:
-// loaded into registers by the threads that use them, 48 values each, they came in batches, 8900 cycles against 3500.
+// Starts the copies of the chunk's rows (rows behind its end: its last one's).  Loaded by the threads that use them, 48
+// values of 2 and 4 bytes each, they took 13000 cycles (an SM has only so many requests in flight), against 2500 here.
 template <int THREADS>
 __device__ __forceinline__ void fetch_rows(const ScanParams& p, int64_t tok, int tc, int64_t h, float (*g)[kK], __nv_bfloat16 (*k)[kK],
                                            __nv_bfloat16 (*q)[kK]) {

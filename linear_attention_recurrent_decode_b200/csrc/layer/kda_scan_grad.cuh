@@ -21,6 +21,7 @@
 #pragma once
 
 #include "kda_scan_common.cuh"
+#include "kda_umma.cuh"
 
 namespace kdal {
 
@@ -34,7 +35,7 @@ struct GradSmem {
   unsigned char ds[kV * kK * 4];             // dS1^T; before: dU^T and beta Y
   unsigned char dr[2 * Record::kPlane];      // dR^T [v][t]
   unsigned char r[2 * Record::kPlane];       // r^T [v][t]
-  unsigned char dO[Record::kPlane];          // dO [t][v]
+  unsigned char dO[Record::kPlane];          // dO [t][v], one plane
   // exp(mu), exp(md), exp(end - mu), exp(end - md) per sub-block and channel
   float emu[kNB][kK], emd[kNB][kK], eru[kNB][kK], erd[kNB][kK];
   float hdr[Record::kHdr / 4];
@@ -42,10 +43,14 @@ struct GradSmem {
   float sc[Record::kScBytes / 4];
   float tail[kNB][kK];                       // the decays' gradients, summed per sub-block
   float dbeta[8][kC];
-  float sc_dr[8][kNB];
-  uint32_t mx_do;
+  uint32_t mx_do, mx_dr;
   int exact[kNB];
-  uint64_t bar[2];
+  uint64_t bar[4];                           // dU, Y, r and S0; dS1; the products, first part and last
+  uint32_t tmem;
+};
+// Columns of tensor memory: products of 64 tokens (M) with 128 channels or 64 tokens.
+struct GradColumns {
+  static constexpr uint32_t kDQ = 0, kDKRow = 128, kDKCol = 256, kDP = 384, kDA = 448, kAll = 512;
 };
 struct GradPairs {  // over s0 .. dO once those are dead
   float dp[kC][kDP], da[kC][kDP];
@@ -146,21 +151,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   GradSmem& sm = *reinterpret_cast<GradSmem*>(smem_raw);
   GradPairs& pr = *reinterpret_cast<GradPairs*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   int64_t slot, h;
   slot_and_head(p, blockIdx.x, slot, h);
   if (tid == 0) {
-    mbar_init(&sm.bar[0], 1);
-    mbar_init(&sm.bar[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.bar[i], 1);
     mbar_fence_init();
-    sm.mx_do = 0;
+    sm.mx_do = sm.mx_dr = 0;
   }
   if (tid < kNB) sm.exact[tid] = 0;
   const ChunkPos pos = locate(p, slot);
   const int tc = pos.tc;
   wait_upstream();
   if (tc == 0) return;
+  if (warp == 0) tmem_alloc(&sm.tmem, GradColumns::kAll);
+  fence_before_sync();
   __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   const unsigned char* const rec = record(p, slot, h);
   if (tid == 0) {
     mbar_expect(&sm.bar[0], Record::kHdr + Record::kScBytes + Record::kDnBytes + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
@@ -173,13 +181,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     bulk_load(sm.s0, rec + Record::kS, kV * kK * 4, &sm.bar[0]);
   }
   // ---- dO as an fp16 tile (exact after scaling)
+  const int ch = tid & (kK - 1), sub = tid >> 7;
   {
     uint4 raw[2];
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = tid + j * kGradThreads, t = c >> 4, pc = c & 15;
-      raw[j] = t < tc ? *reinterpret_cast<const uint4*>(p.d_out + (pos.tok + t) * p.d_out_ts + h * kV + pc * 8) : make_uint4(0, 0, 0, 0);
+      const int t = tid & 63, pc = (tid >> 6) + 8 * j;
+      raw[j] = *reinterpret_cast<const uint4*>(p.d_out + (pos.tok + (t < tc ? t : tc - 1)) * p.d_out_ts + h * kV + pc * 8);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if ((tid & 63) >= tc) raw[j] = make_uint4(0, 0, 0, 0);
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -191,19 +204,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     const float sc = pow2_scale(__uint_as_float(sm.mx_do));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = tid + j * kGradThreads, t = c >> 4, pc = c & 15;
+      const int t = tid & 63, pc = (tid >> 6) + 8 * j;
       uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc, __uint_as_float(w[e] & 0xffff0000u) * sc));
-      *reinterpret_cast<uint4*>(sm.dO + Rows128::off(t, pc * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(sm.dO + Core<kC>::off(t, pc * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   const float sc_do = pow2_scale(__uint_as_float(sm.mx_do));
-  if (!__syncthreads_and(mbar_wait(&sm.bar[0], 0))) {  // the copies never came
-    if (tid == 0) set_error(p);
-    return;
-  }
+  bool ok = __syncthreads_and(mbar_wait(&sm.bar[0], 0));  // if a wait gives up, the block goes on to its end on what it has
   const uint32_t a_s0 = smem_addr(sm.s0), a_ds = smem_addr(sm.ds), a_dr = smem_addr(sm.dr), a_r = smem_addr(sm.r), a_do = smem_addr(sm.dO);
   const float* const beta = sm.hdr + Record::kBeta;
 
@@ -213,10 +223,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     const int grp = warp & 7, v0 = grp * 16, first = warp >> 3;
     const uint32_t a_y = a_ds + 2 * Record::kPlane;
     __nv_bfloat16* const dv = p.dv + pos.tok * p.dv_ts + h * kV + v0;
+    float dr[2][2][4] = {}, m_dr = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int nb = u ? 3 - first : first;  // the sub-block of tokens
-      float acc[2][4] = {};
+      auto& acc = dr[u];
       uint32_t dh[4], dl[4];
       for (int kk = 3; kk >= nb; --kk) {     // s sub-block; Y[s][t] is zero for t >= s
         uint32_t bh[4], bl[4];
@@ -233,11 +244,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         add_scaled(acc[1], x[1], f);
       }
       // dh, dl now hold the sub-block's own dU
-      const float inv = pow2_inv(sm.sc[Record::kScDU + (grp >> 1)]), inv_r = pow2_inv(sm.sc[Record::kScR + (grp >> 1)]);
+      const float inv = pow2_inv(sm.sc[Record::kScDU + (grp >> 1)]), inv_r = pow2_inv(sm.sc[Record::kScR]);
       uint32_t rh[4], rl[4];
       load_a<Core<kV>>(a_r, v0, nb * 16, lane, rh);
       load_a<Core<kV>>(a_r + Record::kPlane, v0, nb * 16, lane, rl);
-      float m = 0.f, db[4] = {0.f, 0.f, 0.f, 0.f};  // tokens nb 16 + 2 (lane & 3) + {0, 1, 8, 9}
+      float db[4] = {0.f, 0.f, 0.f, 0.f};  // tokens nb 16 + 2 (lane & 3) + {0, 1, 8, 9}
 #pragma unroll
       for (int j = 0; j < 4; ++j) {  // fragment register j: rows + (j & 1) 8, columns + (j >> 1) 8
         const float2 du = join2(dh[j], dl[j]), r = join2(rh[j], rl[j]);
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         db[(j >> 1) * 2 + 1] = fmaf(y1, r.y * inv_r, db[(j >> 1) * 2 + 1]);
         c[e] = y0 * beta[t];
         c[e + 1] = y1 * beta[t + 1];
-        m = fmaxf(m, fmaxf(fabsf(c[e]), fabsf(c[e + 1])));
+        m_dr = fmaxf(m_dr, fmaxf(fabsf(c[e]), fabsf(c[e + 1])));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -256,18 +267,36 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         for (int o = 4; o < 32; o <<= 1) db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
         if (lane < 4) sm.dbeta[grp][nb * 16 + (j >> 1) * 8 + 2 * lane + (j & 1)] = db[j];
       }
-      const float sc = pow2_scale(warp_max(m));
-      if (lane == 0) sm.sc_dr[grp][nb] = sc;
-      frag_a(acc[0], acc[1], sc, dh, dl);
-      store_frag<Core<kV>>(sm.dr, Record::kPlane, v0, nb * 16, lane, dh, dl);
       store_out16(dv, p.dv_ts, nb * 16, tc, lane, acc[0], acc[1], 1.f);
     }
+    m_dr = warp_max(m_dr);
+    if (lane == 0) atomicMax(&sm.mx_dr, __float_as_uint(m_dr));
+    __syncthreads();
+    const float sc = pow2_scale(__uint_as_float(sm.mx_dr));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t dh[4], dl[4];
+      frag_a(dr[u][0], dr[u][1], sc, dh, dl);
+      store_frag<Core<kV>>(sm.dr, Record::kPlane, v0, (u ? 3 - first : first) * 16, lane, dh, dl);
+    }
   }
-  fence_async();  // the reads of dU and Y come before dS1 is copied over them
+  fence_async();  // dO and dR come before the products' reads, the reads of dU and Y before dS1 is copied over them
+  fence_before_sync();
   __syncthreads();
-  if (tid == 0) {
-    mbar_expect(&sm.bar[1], kV * kK * 4);
-    bulk_load(sm.ds, rec + Record::kDS, kV * kK * 4, &sm.bar[1]);
+  fence_after_sync();
+  // the chunk's rows, for step 3, over dU and Y; dS1 follows them
+  RawRows& raw = *reinterpret_cast<RawRows*>(sm.ds);
+  static_assert(sizeof(RawRows) <= sizeof(sm.ds), "the raw rows fit");
+  fetch_rows<kGradThreads>(p, pos.tok, tc, h, raw.g, raw.k, raw.q);
+  // ---- 2. The products on the tensor cores, one warp's: dQt = dO S0^T, dKt = -dR S0^T, dP = dO r, dA = -dR r, and, once
+  // dS1 is there, dKe = r dS1^T (scales and signs come later).  The other warps work on the decay factors meanwhile.
+  const float sc_do_inv = pow2_inv(sc_do), sc_dr_inv = pow2_inv(pow2_scale(__uint_as_float(sm.mx_dr)));
+  if (warp == 0) {
+    umma_tiles<kK, kV, kC, false, kV, true, true>(tmem + GradColumns::kDQ, a_do, 0, a_s0, kV * kK * 2);
+    umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKRow, a_dr, Record::kPlane, a_s0, kV * kK * 2);
+    umma_tiles<kC, kV, kC, false, kV, true, true>(tmem + GradColumns::kDP, a_do, 0, a_r, Record::kPlane);
+    umma_tiles<kC, kV, kV, true, kV, true, false>(tmem + GradColumns::kDA, a_dr, Record::kPlane, a_r, Record::kPlane);
+    umma_commit(&sm.bar[2]);
   }
   if (tid < tc) {
     float s = 0.f;
@@ -275,41 +304,47 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     for (int w = 0; w < 8; ++w) s += sm.dbeta[w][tid];
     p.dbeta[(pos.tok + tid) * p.dbeta_ts + h] = s;
   }
-
-  // ---- 2. dQt = scale dO S0^T and dKt = -dR S0^T: warp = 16 tokens x 32 channels, a partial sum per 16 value columns
-  const int I = warp & 3, i0 = (warp >> 2) * 32;
-  float dq[4][4] = {}, dkr[4][4] = {};
-#pragma unroll 2
-  for (int g = 0; g < 8; ++g) {
-    uint32_t a[4], ah[4], al[4];
-    load_a<Rows128>(a_do, I * 16, g * 16, lane, a);
-    load_a_t<Core<kV>>(a_dr, I * 16, g * 16, lane, ah);
-    load_a_t<Core<kV>>(a_dr + Record::kPlane, I * 16, g * 16, lane, al);
-    const float inv_s = pow2_inv(sm.sc[Record::kScS + (g >> 1)]);
-    const float fq = inv_s * (pow2_inv(sc_do) * p.scale), fk = -inv_s * pow2_inv(sm.sc_dr[g][I]);
-#pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      uint32_t bh[4], bl[4];
-      load_b_t<Core<kV>>(a_s0, g * 16, i0 + nb * 16, lane, bh);
-      load_b_t<Core<kV>>(a_s0 + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
-      float x[2][4] = {}, y[2][4] = {};
-      mma_pair(x[0], x[1], a, bl);
-      mma_pair(y[0], y[1], ah, bl);
-      mma_pair(y[0], y[1], al, bh);
-      mma_pair(x[0], x[1], a, bh);
-      mma_pair(y[0], y[1], ah, bh);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        add_scaled(dq[2 * nb + j], x[j], fq);
-        add_scaled(dkr[2 * nb + j], y[j], fk);
-      }
+  // ---- 3. decay factors: thread = channel and sub-block
+  float up[kB], dn[kB], kv[kB], qv[kB];
+  {
+    float g[kB];
+    cp_async_wait_all();
+    __syncthreads();
+    read_sub_block(raw.g, raw.k, raw.q, tc, sub, ch, g, kv, qv);
+    fence_async();
+    __syncthreads();  // the rows are read: dS1 goes over them
+    if (tid == 0) {
+      mbar_expect(&sm.bar[1], kV * kK * 4);
+      bulk_load(sm.ds, rec + Record::kDS, kV * kK * 4, &sm.bar[1]);
     }
+    const SubFactors f = sub_factors(g, up, dn);
+    if (f.exact) sm.exact[sub] = 1;
+    sm.emu[sub][ch] = exp_of(f.mu);
+    sm.emd[sub][ch] = exp_of(f.md);
+    sm.eru[sub][ch] = exp_of(add(f.end, neg(f.mu)));
+    sm.erd[sub][ch] = exp_of(add(f.end, neg(f.md)));
   }
-  if (!__syncthreads_and(mbar_wait(&sm.bar[1], 0))) {
-    if (tid == 0) set_error(p);
-    return;
+  // ---- 4. exp(Gamma_C) sum_v S0 dS1: warp = eight channels, lanes over the value columns; lane e < 8 keeps channel e's
+  // dS1 has a scale per 32 value columns, which dKe contracts: r (done with otherwise) takes up the differences
+  ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[2], 0)) && ok;
+  const float sc_ds = fminf(fminf(sm.sc[Record::kScDS], sm.sc[Record::kScDS + 1]), fminf(sm.sc[Record::kScDS + 2], sm.sc[Record::kScDS + 3]));
+  fence_after_sync();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // a plane's half of the column blocks; lanes over the value columns
+    const int piece = tid + j * kGradThreads;
+    const __half2 f = __float2half2_rn(sc_ds * pow2_inv(sm.sc[Record::kScDS + ((piece & (kV - 1)) >> 5)]));
+    uint4& x = *reinterpret_cast<uint4*>(sm.r + piece * 16);
+    uint32_t y[4] = {x.x, x.y, x.z, x.w};
+    scale_frag(y, f);
+    x = make_uint4(y[0], y[1], y[2], y[3]);
   }
-  // ---- 3. exp(Gamma_C) sum_v S0 dS1: warp = eight channels, lanes over the value columns; lane e < 8 keeps channel e's
+  fence_async();
+  ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[1], 0)) && ok;
+  __syncthreads();
+  if (warp == 0) {
+    umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKCol, a_r, Record::kPlane, a_ds, kV * kK * 2);
+    umma_commit(&sm.bar[3]);
+  }
   float e_sum = 0.f;
   {
     float x[8] = {};
@@ -318,123 +353,73 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       const uint32_t off = Core<kV>::off(q * 32 + lane, warp * 8);
       const uint4 sh = *reinterpret_cast<const uint4*>(sm.s0 + off), sl = *reinterpret_cast<const uint4*>(sm.s0 + kV * kK * 2 + off);
       const uint4 dh = *reinterpret_cast<const uint4*>(sm.ds + off), dl = *reinterpret_cast<const uint4*>(sm.ds + kV * kK * 2 + off);
-      const float inv = pow2_inv(sm.sc[Record::kScS + q]) * pow2_inv(sm.sc[Record::kScDS + q]);
       const uint32_t a[4] = {sh.x, sh.y, sh.z, sh.w}, al[4] = {sl.x, sl.y, sl.z, sl.w};
       const uint32_t d[4] = {dh.x, dh.y, dh.z, dh.w}, ld[4] = {dl.x, dl.y, dl.z, dl.w};
+      const float inv_ds = pow2_inv(sm.sc[Record::kScDS + q]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 s = join2(a[e], al[e]), ds = join2(d[e], ld[e]);
-        x[2 * e] = fmaf(s.x * ds.x, inv, x[2 * e]);
-        x[2 * e + 1] = fmaf(s.y * ds.y, inv, x[2 * e + 1]);
+        x[2 * e] = fmaf(s.x * ds.x, inv_ds, x[2 * e]);
+        x[2 * e + 1] = fmaf(s.y * ds.y, inv_ds, x[2 * e + 1]);
       }
     }
+    const float inv = pow2_inv(sm.sc[Record::kScS]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
-      if (lane == e) e_sum = x[e] * sm.hdr[Record::kDecay + warp * 8 + e];
+      if (lane == e) e_sum = x[e] * inv * sm.hdr[Record::kDecay + warp * 8 + e];
     }
   }
-  // ---- 4. dKe = (beta r) dS1^T
-  float dkc[4][4] = {};
-#pragma unroll 2
-  for (int g = 0; g < 8; ++g) {
-    uint32_t ah[4], al[4];
-    load_a_t<Core<kV>>(a_r, I * 16, g * 16, lane, ah);
-    load_a_t<Core<kV>>(a_r + Record::kPlane, I * 16, g * 16, lane, al);
-    const float f = pow2_inv(sm.sc[Record::kScR + (g >> 1)]) * pow2_inv(sm.sc[Record::kScDS + (g >> 1)]);
+  // ---- 5. the factors, dP and dA over the operand tiles
+  ok = __syncthreads_and(mbar_wait(&sm.bar[3], 0) && ok);  // every product is done, and every warp with S0 and dS1
+  fence_after_sync();
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
-      uint32_t bh[4], bl[4];
-      load_b_t<Core<kV>>(a_ds, g * 16, i0 + nb * 16, lane, bh);
-      load_b_t<Core<kV>>(a_ds + kV * kK * 2, g * 16, i0 + nb * 16, lane, bl);
-      float x[2][4] = {};
-      mma_pair(x[0], x[1], ah, bl);
-      mma_pair(x[0], x[1], al, bh);
-      mma_pair(x[0], x[1], ah, bh);
-      add_scaled(dkc[2 * nb], x[0], f);
-      add_scaled(dkc[2 * nb + 1], x[1], f);
-    }
+  for (int t = 0; t < kB; ++t) {
+    pr.up[sub * kB + t][ch] = up[t];
+    pr.dn[sub * kB + t][ch] = dn[t];
+    pr.ku[sub * kB + t][ch] = kv[t] * up[t];
+    pr.qu[sub * kB + t][ch] = qv[t] * up[t];
+    pr.kd[sub * kB + t][ch] = kv[t] * dn[t];
   }
-  const int row = I * 16 + (lane >> 2);  // this thread's rows: row, row + 8
-  {
-    const float b0 = beta[row], b1 = beta[row + 8];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      dkc[n][0] *= b0;
-      dkc[n][1] *= b0;
-      dkc[n][2] *= b1;
-      dkc[n][3] *= b1;
-    }
-  }
-  __syncthreads();  // every warp is done with S0 and dS1
-  // The raw rows over dS1, for step 6.
-  RawRows& raw = *reinterpret_cast<RawRows*>(sm.ds);
-  static_assert(sizeof(RawRows) <= sizeof(sm.ds), "the raw rows fit");
-  fetch_rows<kGradThreads>(p, pos.tok, tc, h, raw.g, raw.k, raw.q);
-  // ---- 5. dP and dA over S0, 16 x 16 a warp (none above the diagonal)
-  if (const int ti = warp >> 2, si = warp & 3; si <= ti) {
-    const int t = ti * 16 + (lane >> 2), s = si * 16 + 2 * (lane & 3);
-    float cp[2][4] = {}, ca[2][4] = {};
-#pragma unroll 2
-    for (int g = 0; g < 8; ++g) {
-      uint32_t a[4], ah[4], al[4], bh[4], bl[4];
-      load_a<Rows128>(a_do, ti * 16, g * 16, lane, a);
-      load_a_t<Core<kV>>(a_dr, ti * 16, g * 16, lane, ah);
-      load_a_t<Core<kV>>(a_dr + Record::kPlane, ti * 16, g * 16, lane, al);
-      load_b_t<Core<kV>>(a_r, g * 16, si * 16, lane, bh);
-      load_b_t<Core<kV>>(a_r + Record::kPlane, g * 16, si * 16, lane, bl);
-      const float inv_r = pow2_inv(sm.sc[Record::kScR + (g >> 1)]);
-      const float fp = inv_r * (pow2_inv(sc_do) * p.scale), fa = -inv_r * pow2_inv(sm.sc_dr[g][ti]);
-      float x[2][4] = {}, y[2][4] = {};
-      mma_pair(x[0], x[1], a, bl);
-      mma_pair(y[0], y[1], ah, bl);
-      mma_pair(y[0], y[1], al, bh);
-      mma_pair(x[0], x[1], a, bh);
-      mma_pair(y[0], y[1], ah, bh);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        add_scaled(cp[j], x[j], fp);
-        add_scaled(ca[j], y[j], fa);
-      }
-    }
+  const int I = warp & 3, i0 = (warp >> 2) * 32;  // the warp's tokens (its lanes of tensor memory) and channels
+  const uint32_t mine = tmem + (static_cast<uint32_t>(I * 32) << 16);
+  if (const int si = warp >> 2; si <= I) {        // none above the diagonal
+    float cp[2][4], ca[2][4];
+    tmem_ld_tiles(mine + GradColumns::kDP + si * 16, cp);
+    tmem_ld_tiles(mine + GradColumns::kDA + si * 16, ca);
+    const float inv_r = pow2_inv(sm.sc[Record::kScR]), fp = inv_r * sc_do_inv * p.scale, fa = -inv_r * sc_dr_inv;
+    const int t = I * 16 + (lane >> 2), s = si * 16 + 2 * (lane & 3);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int tt = t + (e >> 1) * 8, ss = s + n * 8 + (e & 1);
         const float b = beta[ss];
-        pr.dp[tt][ss] = ss <= tt ? cp[n][e] * b : 0.f;
-        pr.da[tt][ss] = ss < tt ? ca[n][e] * b : 0.f;
+        pr.dp[tt][ss] = ss <= tt ? cp[n][e] * fp * b : 0.f;
+        pr.da[tt][ss] = ss < tt ? ca[n][e] * fa * b : 0.f;
       }
   }
-  cp_async_wait_all();
-  __syncthreads();  // every warp is done with the operand tiles, the raw rows are there
-  // ---- 6. decay factors
-  const int ch = tid & (kK - 1), sub = tid >> 7;
+  // ---- 6. the products with the states into registers: tokens I 16 .., channels i0 ..
+  const int row = I * 16 + (lane >> 2), col = i0 + 2 * (lane & 3);  // this thread's rows: row, row + 8; channels col + 8 n, + 1
+  float dq[4][4], dkr[4][4], dkc[4][4], ke_sum[4][2];
+  tmem_ld_tiles(mine + GradColumns::kDQ + i0, dq);
+  tmem_ld_tiles(mine + GradColumns::kDKRow + i0, dkr);
+  tmem_ld_tiles(mine + GradColumns::kDKCol + i0, dkc);
   {
-    float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
-    read_sub_block(raw.g, raw.k, raw.q, tc, sub, ch, g, kv, qv);
-    __syncthreads();  // the factors go over them
-    const SubFactors f = sub_factors(g, up, dn);
+    const float inv_s = pow2_inv(sm.sc[Record::kScS]), inv_r = pow2_inv(sm.sc[Record::kScR]) * pow2_inv(sc_ds);
+    const float fq = inv_s * sc_do_inv * p.scale, fk = -inv_s * sc_dr_inv, b0 = beta[row] * inv_r, b1 = beta[row + 8] * inv_r;
 #pragma unroll
-    for (int t = 0; t < kB; ++t) {
-      pr.up[sub * kB + t][ch] = up[t];
-      pr.dn[sub * kB + t][ch] = dn[t];
-      pr.ku[sub * kB + t][ch] = kv[t] * up[t];
-      pr.qu[sub * kB + t][ch] = qv[t] * up[t];
-      pr.kd[sub * kB + t][ch] = kv[t] * dn[t];
-    }
-    if (f.exact) sm.exact[sub] = 1;
-    sm.emu[sub][ch] = exp_of(f.mu);
-    sm.emd[sub][ch] = exp_of(f.md);
-    sm.eru[sub][ch] = exp_of(add(f.end, neg(f.mu)));
-    sm.erd[sub][ch] = exp_of(add(f.end, neg(f.md)));
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dq[n][e] *= fq;
+        dkr[n][e] *= fk;
+        dkc[n][e] *= e < 2 ? b0 : b1;
+      }
   }
-  // ... of the sum over v: Ke dKe joins in step 8
-  const int col = i0 + 2 * (lane & 3);  // this thread's channels: col + 8 n, + 1
+  fence_before_sync();
   __syncthreads();
-  float ke_sum[4][2];
   // Ke is k dn times the sub-block's factor: so is the column accumulator, before the decays go in
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
@@ -555,6 +540,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       if (tt < tc) p.dg[(pos.tok + tt) * p.dg_ts + h * kK + ch] = acc;
     }
   }
+  if (!ok && tid == 0) set_error(p);
+  if (warp == 0) tmem_dealloc(tmem, GradColumns::kAll);
 }
 
 }  // namespace kdal

@@ -49,7 +49,7 @@ struct PrepTiles {    // over the factors once those are in registers; pairs (hi
   unsigned char r16[2][2 * kHalfPlane];       // k, q of sub-blocks 1 and 3 with the decay from their starts
   unsigned char c16[2 * kHalfPlane];          // k of sub-blocks 0 and 2 with the decay to their ends
 };
-enum PrepMax { kMxV, kMxKt, kMxQt, kMxKe, kMxR32K, kMxR32Q, kMxC32, kMxR16K, kMxR16Q, kMxC16, kMxP, kMxY, kMxWr, kMxBeta, kMxCount };
+enum PrepMax { kMxV, kMxKt, kMxQt, kMxKe, kMxR32K, kMxR32Q, kMxC32, kMxR16K, kMxR16Q, kMxC16, kMxP, kMxY, kMxWr, kMxRt, kMxBeta, kMxCount };
 
 struct PrepSmem {
   union {
@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   const uint32_t mt_a = smem_addr(mt), kt_a = smem_addr(sm.t.kt), vt_a = smem_addr(sm.vt);
   const int g16 = (warp & 7) * 16, first = warp >> 3;  // sub-blocks `first` and 3 - first
   float* const rt = reinterpret_cast<float*>(rec + Record::kRt);
+  float m_rt = 0.f;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int nb = u ? 3 - first : first;
@@ -534,10 +535,13 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-        *reinterpret_cast<float2*>(rt + ((t0 + n * 8) >> 2) * (kV * 4) + (v0 + hf * 8) * 4 + (t0 & 3)) =
-            make_float2((hi[n][2 * hf] + lo[n][2 * hf]) * inv, (hi[n][2 * hf + 1] + lo[n][2 * hf + 1]) * inv);
+      for (int hf = 0; hf < 2; ++hf) {
+        const float2 x = make_float2((hi[n][2 * hf] + lo[n][2 * hf]) * inv, (hi[n][2 * hf + 1] + lo[n][2 * hf + 1]) * inv);
+        *reinterpret_cast<float2*>(rt + ((t0 + n * 8) >> 2) * (kV * 4) + (v0 + hf * 8) * 4 + (t0 & 3)) = x;
+        m_rt = fmaxf(m_rt, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
   }
+  block_max(&sm.mx[kMxRt], m_rt, lane);
   // ---- 9. Wr = M Kt: warp = 16 key channels, the same token sub-blocks
   float acc[2][2][4];
   float m_wr = 0.f;
@@ -584,6 +588,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     hdr[Record::kScKe] = scale_of(kMxKe);
     hdr[Record::kScQt] = scale_of(kMxQt);
     hdr[Record::kScY] = sc_y;
+    hdr[Record::kMxWr] = __uint_as_float(sm.mx[kMxWr]);
+    hdr[Record::kMxRt] = __uint_as_float(sm.mx[kMxRt]);
   }
   __syncthreads();
   for (int c = tid; c < 2 * Record::kPlane / 16; c += kPrepThreads)
