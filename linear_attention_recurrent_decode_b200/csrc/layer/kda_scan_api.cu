@@ -172,22 +172,22 @@ bool launch_forward(ks::ScanParams p, int64_t slots, int64_t seg_slots, kda_stre
   if (!launch(ks::kda_scan_prep_kernel, slots * p.HV, ks::kPrepThreads, sizeof(ks::PrepSmem), stream, p)) return false;
   if (p.seg_chunks > 0) {
     p.transitions = 1;
-    if (!launch(ks::kda_scan_forward_kernel, seg_slots * p.HV * 2, ks::kForwardThreads, kChainSmem, stream, p) ||
+    if (!launch(ks::kda_scan_forward_kernel, seg_slots * p.HV * 2, ks::kChainThreads, kChainSmem, stream, p) ||
         !launch(ks::kda_scan_join_kernel<false>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, 0, stream, p))
       return false;
     p.transitions = 0;
   }
-  return launch(ks::kda_scan_forward_kernel, seg_slots * p.HV, ks::kForwardThreads, kChainSmem, stream, p);
+  return launch(ks::kda_scan_forward_kernel, seg_slots * p.HV, ks::kChainThreads, kChainSmem, stream, p);
 }
 bool launch_backward(ks::ScanParams p, int64_t slots, int64_t seg_slots, kda_stream_t stream) {
   if (p.seg_chunks > 0) {
     p.transitions = 1;
-    if (!launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kBackwardThreads, kChainSmem, stream, p) ||
+    if (!launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kChainThreads, kChainSmem, stream, p) ||
         !launch(ks::kda_scan_join_kernel<true>, p.N * p.HV * kJoinGroups, ks::kJoinThreads, 0, stream, p))
       return false;
     p.transitions = 0;
   }
-  return launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kBackwardThreads, kChainSmem, stream, p) &&
+  return launch(ks::kda_scan_backward_kernel, seg_slots * p.HV, ks::kChainThreads, kChainSmem, stream, p) &&
          launch(ks::kda_scan_grad_kernel, slots * p.HV, ks::kGradThreads, sizeof(ks::GradSmem), stream, p);
 }
 

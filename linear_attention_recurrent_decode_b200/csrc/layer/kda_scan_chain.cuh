@@ -25,9 +25,11 @@
 // their right starts.  That is three times the work in (1 / segments) of the
 // time.  Backwards the transition is M's transpose.
 //
-// Warps: 0-15 compute, 16 copies, 17 issues the products, 18-21 (forward) read
-// the outputs back.  A chunk's critical path is two products with a conversion
-// behind each; the outputs' products and read-back run beside it.
+// Warps: 0-15 compute, 16 copies, 17 issues the products.  A chunk's critical
+// path is two products with a conversion behind each.  The outputs' products run
+// behind the state's, under the next chunk's first conversion, and the compute
+// warps read them back and store them while that chunk's first product runs
+// (four warps of their own for it left 80 registers a thread, too few).
 #pragma once
 
 #include "kda_scan_common.cuh"
@@ -46,13 +48,11 @@ struct ChainSmem {
   unsigned char qt[2 * Record::kPlane], p[kC * kC * 4];
   unsigned char hdr[2][Record::kHdr];
   alignas(16) float peak[4][kParts][4];      // [exchange][part][quarter of the value columns]
-  float sc_s[2][4], sc_u[2][4];  // by chunk parity, for the outputs
   uint64_t full_wr[2], full_ke[2], full_hdr[2], full_qt, full_p, empty_hdr[2];
-  uint64_t state, rows, scales[2];  // written by the compute warps: the state, U (or dU), the scales
+  uint64_t state, rows;             // written by the compute warps: the state, U (or dU)
   // Products done, by chunk parity: S0^T Wr^T (or dS1^T Ke^T), the state's with U; with Qt; forward: the outputs' with P.
   // A tile's place is free again once the products that read it are.
   uint64_t first[2], last[2], with_qt, out_done;
-  uint64_t out_free;                // forward: the outputs are read
   uint64_t d_out;                   // backward: dO is written
   uint64_t end;
   uint32_t tmem;
@@ -76,7 +76,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ void chain_init(ChainSmem& sm, int header_readers) {
+__device__ __forceinline__ void chain_init(ChainSmem& sm) {
   if (threadIdx.x < 32) tmem_alloc(&sm.tmem, kTmemColumns);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -85,8 +85,7 @@ __device__ __forceinline__ void chain_init(ChainSmem& sm, int header_readers) {
       mbar_init(&sm.full_hdr[i], 1);
       mbar_init(&sm.first[i], 1);
       mbar_init(&sm.last[i], 1);
-      mbar_init(&sm.empty_hdr[i], header_readers);
-      mbar_init(&sm.scales[i], kComputeWarps);
+      mbar_init(&sm.empty_hdr[i], kComputeWarps);
     }
     mbar_init(&sm.full_qt, 1);
     mbar_init(&sm.full_p, 1);
@@ -95,7 +94,6 @@ __device__ __forceinline__ void chain_init(ChainSmem& sm, int header_readers) {
     mbar_init(&sm.rows, kComputeWarps);
     mbar_init(&sm.d_out, kComputeWarps);
     mbar_init(&sm.out_done, 1);
-    mbar_init(&sm.out_free, 4);
     mbar_init(&sm.end, 1);
     mbar_fence_init();
   }
@@ -255,9 +253,9 @@ __device__ __forceinline__ float abs_max(const float (&x)[N], const float* f) { 
 struct ForwardColumns {
   static constexpr uint32_t kState = 0, kU = 128, kX = 192, kO1 = 256, kO2 = 320, kDelta = 384;
 };
-constexpr int kForwardThreads = (kComputeWarps + 6) * 32;
+constexpr int kChainThreads = (kComputeWarps + 2) * 32;
 
-__global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(kChainThreads, 1) kda_scan_forward_kernel(const __grid_constant__ ScanParams p) {
   using Col = ForwardColumns;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
@@ -279,13 +277,13 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
     wait_upstream();
     if (!p.transitions) {
       const int64_t rows = len < chunks * kC ? len : chunks * kC;
-      for (int64_t t = threadIdx.x; t < rows * 16; t += kForwardThreads)
+      for (int64_t t = threadIdx.x; t < rows * 16; t += kChainThreads)
         *reinterpret_cast<uint4*>(p.out + (start + (t >> 4)) * p.out_ts + h * kV + (t & 15) * 8) = make_uint4(0, 0, 0, 0);
     }
     return;
   }
   const bool outputs = p.out != nullptr && !p.transitions, save = p.save && !p.transitions;
-  chain_init(sm, outputs ? kComputeWarps + 4 : kComputeWarps);
+  chain_init(sm);
   const int64_t sblk = (blk * p.HV + h) * kK * kV, gblk = (slot * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
   unsigned char* rec = record(p, first_slot(p, n, seg.start) + seg.first, h);
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -302,11 +300,33 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
 #pragma unroll
       for (int j = 0; j < kPartK; ++j) s[j] = part * kPartK + j == v ? 1.f : 0.f;
     }
+    // O = scale (Qt S0 + P U) of a chunk, its factors kept from there: this thread's value column and tokens; neighbours
+    // trade a token each, so that a thread stores two values.
+    float out_f1 = 0.f, out_f2 = 0.f;
+    auto put_outputs = [&](int64_t c) {
+      w.warp(&sm.out_done, c);
+      fence_after_sync();
+      const int rows = static_cast<int>(len - c * kC < kC ? len - c * kC : kC) - part * kPartT - (lane & 1);
+      __nv_bfloat16* out = p.out + (start + c * kC + part * kPartT + (lane & 1)) * p.out_ts + h * kV + (v & ~1);
+      uint32_t a[kPartT], x[kPartT];
+      tmem_ld(mine + Col::kO1 + part * kPartT, a);
+      tmem_ld(mine + Col::kO2 + part * kPartT, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < kPartT; j += 2, out += 2 * p.out_ts) {
+        const float o0 = fmaf(__uint_as_float(a[j]), out_f1, __uint_as_float(x[j]) * out_f2);
+        const float o1 = fmaf(__uint_as_float(a[j + 1]), out_f1, __uint_as_float(x[j + 1]) * out_f2);
+        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? o0 : o1, 1);
+        const __nv_bfloat162 y = lane & 1 ? __floats2bfloat162_rn(got, o1) : __floats2bfloat162_rn(o0, got);
+        if (j < rows) *reinterpret_cast<__nv_bfloat162*>(out) = y;
+      }
+    };
     for (int64_t c = 0; c < chunks; ++c, rec += step) {
       const int b = static_cast<int>(c & 1);
       const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
       // ---- the state as a pair
       const float sc_s = pow2_scale(quarter_max(sm, 2 * b, abs_max(s), part, quarter));
+      if (outputs && c > 0) w.warp(&sm.with_qt, c - 1);  // the outputs' product read the last one
       fence_after_sync();
       write_pair<kK, true>(mine + Col::kState, nullptr, 0, v, part * kPartK, s, sc_s);
       tmem_wait_st();
@@ -324,6 +344,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
           r[4 * j + 3] = x.w;
         }
       }
+      if (outputs && c > 0) put_outputs(c - 1);
       w.warp(&sm.full_hdr[b], c >> 1);
       // ---- r = Rt - S0 Wr, U = beta r
       w.warp(&sm.first[b], c >> 1);
@@ -343,11 +364,6 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
       tmem_wait_st();
       fence_before_sync();
       warp_arrive(&sm.rows, lane);
-      if (part == 0 && lane == 0) {
-        sm.sc_s[b][quarter] = sc_s;
-        sm.sc_u[b][quarter] = sc_u;
-      }
-      warp_arrive(&sm.scales[b], lane);
       if (save) {
         // Every warp has written its state, and its largest value before that (it is overwritten two chunks on).
         const float peak_s = all_max(sm, 2 * b);
@@ -362,12 +378,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
         }
       }
       // ---- S1 = Diag(exp(Gamma_C)) S0 + Ke^T U
+      out_f1 = pow2_inv(sc_s) * pow2_inv(hdr[Record::kScQt]) * p.scale;
+      out_f2 = pow2_inv(sc_u) * pow2_inv(hdr[Record::kScP]) * p.scale;
       w.warp(&sm.last[b], c >> 1);
       fence_after_sync();
       add_product<true>(mine + Col::kDelta + part * kPartK, hdr + Record::kDecay + part * kPartK, pow2_inv(sc_u) * pow2_inv(hdr[Record::kScKe]), s);
       fence_before_sync();
       warp_arrive(&sm.empty_hdr[b], lane);
     }
+    if (outputs && chunks > 0) put_outputs(chunks - 1);
     if (!w.ok) {
       if (lane == 0) set_error(p);
     } else if (p.transitions) {
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
   } else if (warp == kComputeWarps) {
     if (lane == 0) chain_copies<true>(sm, w, rec, step, chunks, outputs);
     __syncwarp();
-  } else if (warp == kComputeWarps + 1) {
+  } else {
     for (int64_t c = 0; c < chunks; ++c) {
       const int b = static_cast<int>(c & 1);
       w.warp(&sm.full_wr[b], c >> 1);
@@ -386,19 +405,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
       fence_after_sync();
       umma_pairs<kC, kK, kC, false>(tmem + Col::kX, tmem + Col::kState, smem_addr(sm.wr[b]), Record::kPlane);
       umma_commit(&sm.first[b]);
-      if (outputs) {
-        w.warp(&sm.full_qt, c);
-        if (c > 0) w.warp(&sm.out_free, c - 1);
-        fence_after_sync();
-        umma_pairs<kC, kK, kC, false>(tmem + Col::kO1, tmem + Col::kState, smem_addr(sm.qt), Record::kPlane);
-        umma_commit(&sm.with_qt);
-      }
       w.warp(&sm.full_ke[b], c >> 1);
       w.warp(&sm.rows, c);
       fence_after_sync();
       umma_pairs<kK, kC, kC, true>(tmem + Col::kDelta, tmem + Col::kU, smem_addr(sm.ke[b]), Record::kPlane);
       umma_commit(&sm.last[b]);
-      if (outputs) {
+      if (outputs) {  // over outputs that every warp has read: it wrote its rows after that
+        w.warp(&sm.full_qt, c);
+        umma_pairs<kC, kK, kC, false>(tmem + Col::kO1, tmem + Col::kState, smem_addr(sm.qt), Record::kPlane);
+        umma_commit(&sm.with_qt);
         w.warp(&sm.full_p, c);
         umma_pairs<kC, kC, kC, false>(tmem + Col::kO2, tmem + Col::kU, smem_addr(sm.p), kC * kC * 2);
         umma_commit(&sm.out_done);
@@ -410,45 +425,6 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
     }
     __syncwarp();
     if (!w.ok && lane == 0) set_error(p);
-  } else if (outputs) {
-    // ---- O = scale (Qt S0 + P U): lanes are value columns; neighbours trade a token each, so that a thread stores two values
-    for (int64_t c = 0; c < chunks; ++c) {
-      const int b = static_cast<int>(c & 1);
-      const int tc = static_cast<int>(len - c * kC < kC ? len - c * kC : kC);
-      const float* const hdr = reinterpret_cast<const float*>(sm.hdr[b]);
-      w.warp(&sm.full_hdr[b], c >> 1);
-      w.warp(&sm.scales[b], c >> 1);
-      const float f1 = pow2_inv(sm.sc_s[b][quarter]) * pow2_inv(hdr[Record::kScQt]) * p.scale;
-      const float f2 = pow2_inv(sm.sc_u[b][quarter]) * pow2_inv(hdr[Record::kScP]) * p.scale;
-      warp_arrive(&sm.empty_hdr[b], lane);
-      w.warp(&sm.out_done, c);
-      fence_after_sync();
-      uint32_t y[kC / 2];  // two values of one token each
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t a[16], x[16];
-        tmem_ld(mine + Col::kO1 + g * 16, a);
-        tmem_ld(mine + Col::kO2 + g * 16, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float o0 = fmaf(__uint_as_float(a[j]), f1, __uint_as_float(x[j]) * f2);
-          const float o1 = fmaf(__uint_as_float(a[j + 1]), f1, __uint_as_float(x[j + 1]) * f2);
-          const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? o0 : o1, 1);
-          const __nv_bfloat162 z = lane & 1 ? __floats2bfloat162_rn(got, o1) : __floats2bfloat162_rn(o0, got);
-          y[g * 8 + (j >> 1)] = *reinterpret_cast<const uint32_t*>(&z);
-        }
-      }
-      fence_before_sync();
-      warp_arrive(&sm.out_free, lane);  // ahead of the stores: the next chunk's products wait for it
-      __nv_bfloat16* const out = p.out + (start + c * kC) * p.out_ts + h * kV + (v & ~1);
-#pragma unroll
-      for (int j = 0; j < kC / 2; ++j) {
-        const int t = 2 * j + (lane & 1);
-        if (t < tc) *reinterpret_cast<uint32_t*>(out + t * p.out_ts) = y[j];
-      }
-    }
-    if (!w.ok && lane == 0) set_error(p);
   }
   chain_exit(sm);
 }
@@ -458,9 +434,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) kda_scan_forward_kernel(co
 struct BackwardColumns {
   static constexpr uint32_t kState = 0, kDelta = 0, kDO = 128, kU = 160, kX1 = 224, kX2 = 288, kExtra = 352;
 };
-constexpr int kBackwardThreads = (kComputeWarps + 2) * 32;
 
-__global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(const __grid_constant__ ScanParams p) {
+__global__ void __launch_bounds__(kChainThreads, 1) kda_scan_backward_kernel(const __grid_constant__ ScanParams p) {
   using Col = BackwardColumns;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   ChainSmem& sm = *reinterpret_cast<ChainSmem*>(smem_raw);
@@ -472,7 +447,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) kda_scan_backward_kernel(
   // The first segment's start gradient is the result itself, and nobody's end.
   if (seg.segs == 0 || (p.transitions && seg.seg == 0)) return;
   const int64_t n = seg.n, start = seg.start + seg.first * kC, len = seg.len - seg.first * kC, chunks = seg.chunks;
-  chain_init(sm, kComputeWarps);
+  chain_init(sm);
   const int64_t sblk = (n * p.HV + h) * kK * kV, gblk = (slot * p.HV + h) * kK * kV, step = p.HV * p.rec_bytes;
   unsigned char* rec = record(p, first_slot(p, n, seg.start) + seg.first + (chunks > 0 ? chunks - 1 : 0), h);
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0), mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
