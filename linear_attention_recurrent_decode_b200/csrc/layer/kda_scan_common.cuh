@@ -294,11 +294,12 @@ __device__ __forceinline__ void read_sub_block(const float (*gs)[kK], const __nv
   }
 }
 
-// Round-to-nearest split of an fp32 value into a tf32 pair (the MMA reads the
-// upper 19 bits of each).
+// Split of an fp32 value into a tf32 pair, both rounded to nearest (the MMA
+// reads the upper 19 bits of each and would truncate the low part: a bias of
+// 2^-23, which the sums of differences behind the decays' gradients show).
 __device__ __forceinline__ void tf32_pair(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 
 }  // namespace kdal

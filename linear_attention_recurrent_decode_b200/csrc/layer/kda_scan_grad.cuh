@@ -9,8 +9,14 @@
 //   dq_t  = dQt_t exp(Gamma_t) + sum_s dP_ts k_s E_ts
 //   dk_t  = [dKt_t exp(Gamma_t) + sum_s dA_ts k_s E_ts]                      "row"
 //         + [dKe_t exp(Gamma_C - Gamma_t) + sum_s (dP_st q_s + dA_st k_s) E_st] "column"
-//   dg_t  = sum_{t' >= t} (q dq + k dk_row - k dk_column)_t' + sum_v S1 dS1,
-// the last term being exp(Gamma_C) sum_v S0 dS1 + sum_t Ke dKe per channel.
+// dg_t is what crosses token t: the products q dq + k dk of every pair (t', s) with s < t <= t', with S0 as the earliest s
+// and dS1 as the latest t'.  For t in sub-block b that is
+//   sum_{t' >= t in b} (in-block pairs' row minus column, and rows' from before b)
+//   + sum_{s < t in b} (columns' from behind b, and Ke dKe) + sum_{s before b} Ke dKe + exp(Gamma_C) sum_v S0 dS1
+//   + sum_{blocks behind b} rows' from before them - sum_{b and blocks behind} columns' from behind them.
+// A sum of rows minus columns over the whole rest of the chunk is the same, but every pair behind t comes in twice there
+// and cancels, a token with itself (P_tt) and dKe with sum_v S1 dS1 too: under strong decays that left dg ten times less
+// exact.
 //
 // The decays are applied sub-block by sub-block (16 tokens) on the
 // accumulators: a row block I starts from its dQt and, for J = 0 .. I - 1,
@@ -41,8 +47,9 @@ struct GradSmem {
   float hdr[Record::kHdr / 4];
   float dn[kNB][kK];                         // from k dn to Ke
   float sc[Record::kScBytes / 4];
-  float tail[kNB][kK];                       // the decays' gradients, summed per sub-block
+  float ended[kNB][kK];                      // Ke dKe summed per sub-block
   float dbeta[8][kC];
+  float dp_own[kC];                          // dP_tt
   uint32_t mx_do, mx_dr;
   int exact[kNB];
   uint64_t bar[4];                           // dU, Y, r and S0; dS1; the products, first part and last
@@ -56,6 +63,7 @@ struct GradPairs {  // over s0 .. dO once those are dead
   float dp[kC][kDP], da[kC][kDP];
   float up[kC][kGP], dn[kC][kGP];            // exp(L - mu), exp(md - L)
   float ku[kC][kGP], qu[kC][kGP], kd[kC][kGP];  // k up, q up, k dn
+  float rows[kNB][kK], columns[kNB][kK];     // parts of the decays' gradients, summed per sub-block
 };
 static_assert(sizeof(GradPairs) <= offsetof(GradSmem, emu), "the factors fit over the operand tiles");
 static_assert(2 * sizeof(float) * kC * kDP <= kV * kK * 4, "dP and dA fit over S0");
@@ -125,7 +133,8 @@ __device__ __forceinline__ void pair_b(const float (*b)[kGP], int k0, int i0, in
   tf32_pair(b[k0 + c][i0 + r], bh[0], bl[0]);
   tf32_pair(b[k0 + c + 4][i0 + r], bh[1], bl[1]);
 }
-// c += (ah + al) (bh + bl) without al.bl, the cross terms first.
+// c += (ah + al) (bh + bl) without al.bl, the cross terms first.  The MMA adds to its accumulator with truncation: c is a
+// few products' alone, and joins a longer sum by an ordinary addition.
 __device__ __forceinline__ void mma3_tf32(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh)[2],
                                           const uint32_t (&bl)[2]) {
   mma_tf32(c, ah, bl);
@@ -396,45 +405,41 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       for (int e = 0; e < 4; ++e) {
         const int tt = t + (e >> 1) * 8, ss = s + n * 8 + (e & 1);
         const float b = beta[ss];
-        pr.dp[tt][ss] = ss <= tt ? cp[n][e] * fp * b : 0.f;
+        const float x = cp[n][e] * fp * b;
+        if (ss == tt) sm.dp_own[tt] = x;
+        pr.dp[tt][ss] = ss < tt ? x : 0.f;
         pr.da[tt][ss] = ss < tt ? ca[n][e] * fa * b : 0.f;
       }
   }
   // ---- 6. the products with the states into registers: tokens I 16 .., channels i0 ..
   const int row = I * 16 + (lane >> 2), col = i0 + 2 * (lane & 3);  // this thread's rows: row, row + 8; channels col + 8 n, + 1
-  float dq[4][4], dkr[4][4], dkc[4][4], ke_sum[4][2];
+  float dq[4][4], dkr[4][4], dkc[4][4] = {};
   tmem_ld_tiles(mine + GradColumns::kDQ + i0, dq);
   tmem_ld_tiles(mine + GradColumns::kDKRow + i0, dkr);
-  tmem_ld_tiles(mine + GradColumns::kDKCol + i0, dkc);
   {
-    const float inv_s = pow2_inv(sm.sc[Record::kScS]), inv_r = pow2_inv(sm.sc[Record::kScR]) * pow2_inv(sc_ds);
-    const float fq = inv_s * sc_do_inv * p.scale, fk = -inv_s * sc_dr_inv, b0 = beta[row] * inv_r, b1 = beta[row + 8] * inv_r;
+    const float inv_s = pow2_inv(sm.sc[Record::kScS]), fq = inv_s * sc_do_inv * p.scale, fk = -inv_s * sc_dr_inv;
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         dq[n][e] *= fq;
         dkr[n][e] *= fk;
-        dkc[n][e] *= e < 2 ? b0 : b1;
       }
   }
-  fence_before_sync();
   __syncthreads();
-  // Ke is k dn times the sub-block's factor: so is the column accumulator, before the decays go in
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const float2 fct = *reinterpret_cast<const float2*>(&sm.dn[I][col + n * 8]);
-    const float2 k0 = *reinterpret_cast<const float2*>(&pr.kd[row][col + n * 8]), k1 = *reinterpret_cast<const float2*>(&pr.kd[row + 8][col + n * 8]);
-    ke_sum[n][0] = fct.x * fmaf(k0.x, dkc[n][0], k1.x * dkc[n][2]);
-    ke_sum[n][1] = fct.y * fmaf(k0.y, dkc[n][1], k1.y * dkc[n][3]);
-  }
 
   // ---- 7. the pairs
-  const bool exact = sm.exact[I] != 0;
-  for (int J = 0; J <= I; ++J) {  // row blocks: earlier tokens
-    scale_cols(dq, &(J < I ? sm.emd : sm.emu)[J][col]);
-    scale_cols(dkr, &(J < I ? sm.emd : sm.emu)[J][col]);
-    if (J == I && exact) break;
+  // q or k again, at this thread's elements (rows behind the chunk: the last one's); read where they are used, not kept
+  auto fetch = [&](const __nv_bfloat16* x, int64_t ts, __nv_bfloat162 (&to)[4][2]) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const __nv_bfloat16* const at = x + (pos.tok + (row + hf * 8 < tc ? row + hf * 8 : tc - 1)) * ts + h * kK + col;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) to[n][hf] = *reinterpret_cast<const __nv_bfloat162*>(at + n * 8);
+    }
+  };
+  // the products with block J's keys; with its queries and keys
+  auto row_block = [&](int J, float (&xq)[4][4], float (&xk)[4][4]) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       uint32_t ph[4], pl[4], ah[4], al[4];
@@ -444,27 +449,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       for (int n = 0; n < 4; ++n) {
         uint32_t bh[2], bl[2];
         pair_b(pr.kd, J * 16 + kk * 8, i0 + n * 8, lane, bh, bl);
-        mma3_tf32(dq[n], ph, pl, bh, bl);
-        mma3_tf32(dkr[n], ah, al, bh, bl);
+        mma3_tf32(xq[n], ph, pl, bh, bl);
+        mma3_tf32(xk[n], ah, al, bh, bl);
       }
     }
-    if (J < I) {
-      scale_cols(dq, &sm.erd[J][col]);
-      scale_cols(dkr, &sm.erd[J][col]);
-    }
-  }
-  __nv_bfloat162 qk[4][2][2];  // q and k again, at this thread's elements (rows behind the chunk: the last one's)
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int64_t tk = pos.tok + (row + hf * 8 < tc ? row + hf * 8 : tc - 1);
-      qk[n][hf][0] = *reinterpret_cast<const __nv_bfloat162*>(p.q + tk * p.q_ts + h * kK + col + n * 8);
-      qk[n][hf][1] = *reinterpret_cast<const __nv_bfloat162*>(p.k + tk * p.k_ts + h * kK + col + n * 8);
-    }
-  for (int J = kNB - 1; J >= I; --J) {  // column blocks: later tokens
-    scale_cols(dkc, &(J > I ? sm.eru : sm.erd)[J][col]);
-    if (J == I && exact) break;
+  };
+  auto column_block = [&](int J, float (&x)[4][4]) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       uint32_t ph[4], pl[4], ah[4], al[4];
@@ -474,70 +464,168 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       for (int n = 0; n < 4; ++n) {
         uint32_t bh[2], bl[2];
         pair_b(pr.qu, J * 16 + kk * 8, i0 + n * 8, lane, bh, bl);
-        mma3_tf32(dkc[n], ph, pl, bh, bl);
+        mma3_tf32(x[n], ph, pl, bh, bl);
         pair_b(pr.ku, J * 16 + kk * 8, i0 + n * 8, lane, bh, bl);
-        mma3_tf32(dkc[n], ah, al, bh, bl);
+        mma3_tf32(x[n], ah, al, bh, bl);
       }
     }
-    if (J > I) scale_cols(dkc, &sm.emu[J][col]);
+  };
+  // sums of a block's rows per channel, to the block's lanes 0 .. 3
+  auto block_sum = [&](float (&x)[4][2], float (*to)[kK]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x[n][e] += __shfl_xor_sync(0xffffffffu, x[n][e], o);
+        if (lane < 4) to[I][col + n * 8 + e] = x[n][e];
+      }
+  };
+  const bool exact = sm.exact[I] != 0;
+  {  // rows: earlier tokens
+    for (int J = 0; J < I; ++J) {
+      scale_cols(dq, &sm.emd[J][col]);
+      scale_cols(dkr, &sm.emd[J][col]);
+      float xq[4][4] = {}, xk[4][4] = {};  // this block's alone: see mma3_tf32
+      row_block(J, xq, xk);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        add_scaled(dq[n], xq[n], 1.f);
+        add_scaled(dkr[n], xk[n], 1.f);
+      }
+      scale_cols(dq, &sm.erd[J][col]);
+      scale_cols(dkr, &sm.erd[J][col]);
+    }
+    scale_cols(dq, &sm.emu[I][col]);
+    scale_cols(dkr, &sm.emu[I][col]);
+    float xq[4][4] = {}, xk[4][4] = {}, sum[4][2] = {};
+    __nv_bfloat162 qe[4][2], ke[4][2];
+    fetch(p.q, p.q_ts, qe);
+    fetch(p.k, p.k_ts, ke);
+    if (exact) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float3 d = grad_exact_element(p, pr, I, pos.tok, tc, h, row + (e >> 1) * 8, col + n * 8 + (e & 1));
+          xq[n][e] = d.x;
+          xk[n][e] = d.y;
+        }
+    } else {
+      row_block(I, xq, xk);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float2& at = *reinterpret_cast<float2*>(&pr.up[row + hf * 8][col + n * 8]);  // this thread's own elements
+        const float2 u2 = at, q2 = __bfloat1622float2(qe[n][hf]), k2 = __bfloat1622float2(ke[n][hf]);
+        float2 y;
+        auto element = [&](int e, float u, float q, float k) {
+          const float ui = exact ? 1.f : u, bq = dq[n][e] * u, bk = dkr[n][e] * u, iq = xq[n][e] * ui, ik = xk[n][e] * ui;
+          const float before = fmaf(q, bq, k * bk);
+          sum[n][e & 1] += before;
+          dq[n][e] = bq + iq;
+          dkr[n][e] = bk + ik;
+          return before + fmaf(q, iq, k * ik);
+        };
+        y.x = element(2 * hf, u2.x, q2.x, k2.x);
+        y.y = element(2 * hf + 1, u2.y, q2.y, k2.y);
+        at = y;
+      }
+    block_sum(sum, pr.rows);
   }
+  {  // columns: later tokens
+    for (int J = kNB - 1; J > I; --J) {
+      scale_cols(dkc, &sm.eru[J][col]);
+      float x[4][4] = {};
+      column_block(J, x);
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < 4; ++n) add_scaled(dkc[n], x[n], 1.f);
+      scale_cols(dkc, &sm.emu[J][col]);
+    }
+    scale_cols(dkc, &sm.erd[I][col]);
+    float x[4][4] = {}, ended[4][4], sum[4][2] = {};
+    __nv_bfloat162 ke[4][2];
+    fetch(p.k, p.k_ts, ke);
+    if (exact) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = row + (e >> 1) * 8, i = col + n * 8 + (e & 1);
-      const float u = pr.up[t][i];
-      dq[n][e] *= u;
-      dkr[n][e] *= u;
-      dkc[n][e] *= pr.dn[t][i];
-      if (exact) {
-        const float3 d = grad_exact_element(p, pr, I, pos.tok, tc, h, t, i);
-        dq[n][e] += d.x;
-        dkr[n][e] += d.y;
-        dkc[n][e] += d.z;
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = grad_exact_element(p, pr, I, pos.tok, tc, h, row + (e >> 1) * 8, col + n * 8 + (e & 1)).z;
+    } else {
+      column_block(I, x);
+    }
+    tmem_ld_tiles(mine + GradColumns::kDKCol + i0, ended);  // dKe
+    const float inv_r = pow2_inv(sm.sc[Record::kScR]) * pow2_inv(sc_ds), b0 = beta[row] * inv_r, b1 = beta[row + 8] * inv_r;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float2 fct = *reinterpret_cast<const float2*>(&sm.dn[I][col + n * 8]);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float2& at = *reinterpret_cast<float2*>(&pr.up[row + hf * 8][col + n * 8]);
+        float2& end = *reinterpret_cast<float2*>(&pr.dn[row + hf * 8][col + n * 8]);
+        const float2 d2 = end, k2 = __bfloat1622float2(ke[n][hf]);
+        float2 y = at, z;
+        auto element = [&](int e, float d, float k, float f, float& inside) {
+          const float di = exact ? 1.f : d, last = ended[n][e] * (hf ? b1 : b0) * (f * d), bc = dkc[n][e] * d, ic = x[n][e] * di;
+          const float behind = k * bc;
+          sum[n][e & 1] += behind;
+          inside = fmaf(-k, ic, inside);
+          dkr[n][e] += (bc + ic) + last;
+          return fmaf(k, last, behind);
+        };
+        z.x = element(2 * hf, d2.x, k2.x, fct.x, y.x);
+        z.y = element(2 * hf + 1, d2.y, k2.y, fct.y, y.y);
+        at = y;
+        end = z;
       }
     }
+    block_sum(sum, pr.columns);
+  }
+  fence_before_sync();
   __syncthreads();  // the factors are dead: the decays' gradients go over them
-  // ---- 8. dq, dk; dg by a sum from the chunk's end
-  float (*const dgam)[kGP] = pr.up;
-  float (*const keb)[kK] = reinterpret_cast<float (*)[kK]>(&pr.ku[0][0]);  // [4 row blocks x 8 rows][128]
+  // ---- 8. dq, dk; dg: thread = channel and sub-block
+  __nv_bfloat162 qe[4][2], ke[4][2];
+  fetch(p.q, p.q_ts, qe);
+  fetch(p.k, p.k_ts, ke);
   float* const ev = &pr.qu[0][0];  // [128]
   if (lane < 8) ev[warp * 8 + lane] = e_sum;
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) keb[I * 8 + (lane >> 2)][col + n * 8 + e] = ke_sum[n][e];
-#pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int t = row + hf * 8, i = col + n * 8;
+      const int t = row + hf * 8, i = col + n * 8, e = 2 * hf;
       const int64_t tk = pos.tok + t;
-      const float2 q = __bfloat1622float2(qk[n][hf][0]), k = __bfloat1622float2(qk[n][hf][1]);
-      const float q0 = dq[n][2 * hf], q1 = dq[n][2 * hf + 1], r0 = dkr[n][2 * hf], r1 = dkr[n][2 * hf + 1];
-      const float c0 = dkc[n][2 * hf], c1 = dkc[n][2 * hf + 1];
+      const float own = sm.dp_own[t];
+      const float2 q = __bfloat1622float2(qe[n][hf]), k = __bfloat1622float2(ke[n][hf]);
       if (t < tc) {
-        *reinterpret_cast<__nv_bfloat162*>(p.dq + tk * p.dq_ts + h * kK + i) = __floats2bfloat162_rn(q0, q1);
-        *reinterpret_cast<__nv_bfloat162*>(p.dk + tk * p.dk_ts + h * kK + i) = __floats2bfloat162_rn(r0 + c0, r1 + c1);
+        *reinterpret_cast<__nv_bfloat162*>(p.dq + tk * p.dq_ts + h * kK + i) =
+            __floats2bfloat162_rn(fmaf(own, k.x, dq[n][e]), fmaf(own, k.y, dq[n][e + 1]));
+        *reinterpret_cast<__nv_bfloat162*>(p.dk + tk * p.dk_ts + h * kK + i) =
+            __floats2bfloat162_rn(fmaf(own, q.x, dkr[n][e]), fmaf(own, q.y, dkr[n][e + 1]));
       }
-      // rows behind the chunk: their gradients are zero
-      *reinterpret_cast<float2*>(&dgam[t][i]) = make_float2(fmaf(q.x, q0, k.x * (r0 - c0)), fmaf(q.y, q1, k.y * (r1 - c1)));
     }
   }
+  float lead[kB], ahead = 0.f;  // of the sub-block: the columns' from behind it and Ke dKe, ahead of each token
+#pragma unroll
+  for (int t = 0; t < kB; ++t) {
+    lead[t] = ahead;
+    ahead += pr.dn[sub * kB + t][ch];
+  }
+  sm.ended[sub][ch] = ahead - pr.columns[sub][ch];
   __syncthreads();
   {
-    float sum = 0.f;  // a sub-block's tokens, from the end
-#pragma unroll
-    for (int t = kB - 1; t >= 0; --t) sum += dgam[sub * kB + t][ch];
-    sm.tail[sub][ch] = sum;
     float acc = ev[ch];
-#pragma unroll 8
-    for (int w = 0; w < 32; ++w) acc += keb[w][ch];
-    __syncthreads();
-    for (int j = kNB - 1; j > sub; --j) acc += sm.tail[j][ch];
+    for (int j = 0; j < sub; ++j) acc += sm.ended[j][ch];
+    float cross = -pr.columns[sub][ch];
+    for (int j = sub + 1; j < kNB; ++j) cross += pr.rows[j][ch] - pr.columns[j][ch];
+    acc += cross;
 #pragma unroll
     for (int t = kB - 1; t >= 0; --t) {
       const int tt = sub * kB + t;
-      acc += dgam[tt][ch];
-      if (tt < tc) p.dg[(pos.tok + tt) * p.dg_ts + h * kK + ch] = acc;
+      acc += pr.up[tt][ch];
+      if (tt < tc) p.dg[(pos.tok + tt) * p.dg_ts + h * kK + ch] = acc + lead[t];
     }
   }
   if (!ok && tid == 0) set_error(p);

@@ -43,7 +43,7 @@ struct PrepFactors {
   float kd[kC][kFP];  // k dn
 };
 struct PrepTiles {    // over the factors once those are in registers; pairs (hi, lo)
-  unsigned char kt[2 * Record::kPlane];       // Kt; then Wr
+  unsigned char kt[2 * Record::kPlane];       // Kt
   unsigned char r32[2][2 * kHalfPlane];       // k, q of tokens 32.. with the decay from token 32's start
   unsigned char c32[2 * kHalfPlane];          // k of tokens ..31 with the decay to there
   unsigned char r16[2][2 * kHalfPlane];       // k, q of sub-blocks 1 and 3 with the decay from their starts
@@ -349,11 +349,24 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       dst[t][s] = s < t + kind ? x : 0.f;
     }
   }
-  // ---- 4. tiles of the decayed rows, over the factors: Qt and Ke to the record, the others to shared memory;
-  // warp = eight channels, lane = token (and the one 32 further on)
+  // ---- 4. tiles of the decayed rows, over the factors; warp = eight channels, lane = token (and the one 32 further on).
+  // Qt and Ke stay in registers until the solve leaves most warps idle.
+  const int i0 = warp * 8;
+  float qu[2][8], kd[2][8];
+  // x[8] f[8] sc as a pair of 16-byte pieces
+  auto put = [&](unsigned char* hi, unsigned char* lo, uint32_t off, const float (&x)[8], const float (&f)[8], float sc) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(x[2 * e] * f[2 * e] * sc, x[2 * e + 1] * f[2 * e + 1] * sc, h[e], l[e]);
+    *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
+  };
+  auto get = [&](const float* src, float (&f)[8]) {
+    *reinterpret_cast<float4*>(&f[0]) = *reinterpret_cast<const float4*>(src);
+    *reinterpret_cast<float4*>(&f[4]) = *reinterpret_cast<const float4*>(src + 4);
+  };
   {
-    const int i0 = warp * 8;
-    float ku[2][8], qu[2][8], kd[2][8];
+    float ku[2][8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = j * 32 + lane;
@@ -365,18 +378,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       }
     }
     __syncthreads();
-    // x[8] f[8] sc as a pair of 16-byte pieces
-    auto put = [&](unsigned char* hi, unsigned char* lo, uint32_t off, const float (&x)[8], const float (&f)[8], float sc) {
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) split2(x[2 * e] * f[2 * e] * sc, x[2 * e + 1] * f[2 * e + 1] * sc, h[e], l[e]);
-      *reinterpret_cast<uint4*>(hi + off) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(lo + off) = make_uint4(l[0], l[1], l[2], l[3]);
-    };
-    auto get = [&](const float* src, float (&f)[8]) {
-      *reinterpret_cast<float4*>(&f[0]) = *reinterpret_cast<const float4*>(src);
-      *reinterpret_cast<float4*>(&f[4]) = *reinterpret_cast<const float4*>(src + 4);
-    };
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = j * 32 + lane, tb = t / kB;  // tb: 0, 1 and then 2, 3
@@ -384,9 +385,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       float f[8];
       get(&sm.up[tb][i0], f);
       put(sm.t.kt, sm.t.kt + Record::kPlane, off, ku[j], f, scale_of(kMxKt));
-      put(rec + Record::kQt, rec + Record::kQt + Record::kPlane, off, qu[j], f, scale_of(kMxQt));
-      get(&sm.dn[tb][i0], f);
-      put(rec + Record::kKe, rec + Record::kKe + Record::kPlane, off, kd[j], f, scale_of(kMxKe));
       get(&sm.x32[tb][i0], f);
       const uint32_t off32 = Core<32>::off(lane, i0), off16 = Core<32>::off(j * kB + (lane & 15), i0);
       if (j == 1) {
@@ -440,6 +438,18 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   }
   __syncthreads();
 
+  auto put_qt_ke = [&]() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int t = j * 32 + lane;
+      const uint32_t off = Core<kC>::off(t, i0);
+      float f[8];
+      get(&sm.up[t / kB][i0], f);
+      put(rec + Record::kQt, rec + Record::kQt + Record::kPlane, off, qu[j], f, scale_of(kMxQt));
+      get(&sm.dn[t / kB][i0], f);
+      put(rec + Record::kKe, rec + Record::kKe + Record::kPlane, off, kd[j], f, scale_of(kMxKe));
+    }
+  };
   // ---- 6. Y = A (I + diag(beta) A)^-1: four warps, the diagonal blocks by substitution, then pairs of blocks
   if (warp < 4) {
     float m = 0.f;
@@ -465,7 +475,9 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     asm volatile("bar.sync 1, 128;" ::: "memory");
     m = fmaxf(m, solve_below<32>(sm, 32, warp * 8, lane));
     block_max(&sm.mx[kMxY], m, lane);
-  } else {  // the other warps: P to the record
+    put_qt_ke();
+  } else {  // the other warps: Qt, Ke and P to the record
+    put_qt_ke();
     const int w = tid - 128;
     float m = 0.f;
     for (int e = w; e < kC * kC; e += kPrepThreads - 128)
@@ -569,7 +581,7 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
       }
   }
   block_max(&sm.mx[kMxWr], m_wr, lane);
-  __syncthreads();  // every warp is done with Kt
+  __syncthreads();
   const float sc_wr = scale_of(kMxWr);
 #pragma unroll
   for (int u = 0; u < 2; ++u)
@@ -580,8 +592,8 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
         uint32_t hi, lo;
         split2(acc[u][n][2 * hf] * sc_wr, acc[u][n][2 * hf + 1] * sc_wr, hi, lo);
         const uint32_t off = Core<kC>::off((u ? 3 - first : first) * 16 + hf * 8 + (lane >> 2), g16 + n * 8 + 2 * (lane & 3));
-        *reinterpret_cast<uint32_t*>(sm.t.kt + off) = hi;
-        *reinterpret_cast<uint32_t*>(sm.t.kt + Record::kPlane + off) = lo;
+        *reinterpret_cast<uint32_t*>(rec + Record::kWr + off) = hi;  // a warp's are a whole line of the Core tile
+        *reinterpret_cast<uint32_t*>(rec + Record::kWr + Record::kPlane + off) = lo;
       }
   if (tid == 0) {
     hdr[Record::kScWr] = sc_wr;
@@ -591,9 +603,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     hdr[Record::kMxWr] = __uint_as_float(sm.mx[kMxWr]);
     hdr[Record::kMxRt] = __uint_as_float(sm.mx[kMxRt]);
   }
-  __syncthreads();
-  for (int c = tid; c < 2 * Record::kPlane / 16; c += kPrepThreads)
-    *reinterpret_cast<uint4*>(rec + Record::kWr + 16 * c) = *reinterpret_cast<const uint4*>(sm.t.kt + 16 * c);
 }
 
 }  // namespace kdal

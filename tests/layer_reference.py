@@ -16,9 +16,11 @@ Tolerances, from the arithmetic and the number formats:
   within 2^-22 of itself.  Decays make such elements: where everything at the start has been forgotten, results fall to
   any size while their operands' tiles do not, and are off by up to 2^-39 of the products that forgot them.  With at most
   8 such products in a chunk: FLOOR = 2^-36 of the largest input (values, states, gradients), absolute.
-* dg is a difference of sums over the rest of the chunk (64 tokens, random signs: a factor of 8) of q dq + k (dk_row -
-  dk_column): DG_REL = 8 SCAN_REL of the largest value, and of the terms |q dq| + |k dk|, whose difference may vanish
-  (for a single token from a zero state it does, exactly).
+* dg is a difference of sums, of rows and columns of its 16-token sub-block (random signs: a factor of 4) and of whole
+  sub-blocks: DG_REL = 4 SCAN_REL of the largest value, and of the terms |q dq| + |k dk|, whose difference may vanish
+  (for a single token from a zero state it does, exactly).  Over a whole tensor the errors are random: a product's is
+  1.6 2^-24 in the mean (two operand pairs rounded, a dropped product, four additions), and dg adds up some 40 of them,
+  sqrt(40) 1.6 2^-24 = 6e-7 of terms of its own size: DG_NORM, normwise, is twice that.
 * The norm and rotation: sums of D <= 256 squares in fp32, a reciprocal square root (2 ulp), cos and sin (2 ulp) and a
   handful of products: below 32 ulp = 2^-19 of the head's largest value.  QK_REL = 2^-19; the weights' gradients, sums
   of fp32 products in fp32 and fp64, within 2^-19 of the sum of the terms' magnitudes.
@@ -29,7 +31,8 @@ import torch
 
 BF16_HALF_STEP = 2.0 ** -8
 SCAN_REL = 2.5e-5
-DG_REL = 8 * SCAN_REL
+DG_REL = 4 * SCAN_REL
+DG_NORM = 1.2e-6
 FLOOR = 2.0 ** -36
 QK_REL = 2.0 ** -19
 

@@ -119,7 +119,7 @@ A, M, U, I = kda.KDA_ERR_ALIAS, kda.KDA_ERR_MISALIGNED, kda.KDA_ERR_UNSUPPORTED,
     (dict(workspace=None), I), (dict(workspace_bytes=1000), I), (dict(slot_idx=BASE + (11 << 28), num_slots=0), I),
     (dict(out=BASE), A), (dict(out=BASE + (1 << 28) + 4096), A), (dict(final_state=BASE), A), (dict(workspace=BASE), A),
     (dict(out=BASE + (7 << 28)), A), (dict(final_state=BASE + (6 << 28) + 16), A), (dict(out=BASE + (10 << 28)), A),
-    (dict(T=1 << 62), U), (dict(N=1 << 62, cu_seqlens=None), U), (dict(T=1 << 32, N=1), U),
+    (dict(T=1 << 62), U), (dict(slot_idx=BASE + (11 << 28), num_slots=1 << 62), U), (dict(N=1 << 62, cu_seqlens=None), U), (dict(T=1 << 32, N=1), U),
 ])
 def test_scan_refusals(lib, kw, status):
     assert lib.kda_scan(ctypes.byref(scan_args(**kw)), None) == status

@@ -291,6 +291,19 @@ def test_scan_gradients_decays_and_edges(decay, edge, cuda_device):
     check_gradients(got, want[2:], c, q, k, d_out, d_final)
 
 
+@pytest.mark.parametrize("decay", ["softplus", "mild"])
+def test_scan_decay_gradients_normwise(decay, cuda_device):
+    """dg is what crosses each token: as a sum of rows minus columns over the rest of the chunk, strong decays would leave
+    it as a small difference of large sums."""
+    q, k, v, g, beta, cu = inputs([300, 64, 20], 2, decay, seed=75)
+    d_out = torch.randn(384, 2, V, device=cuda_device, generator=torch.Generator(device=cuda_device).manual_seed(3)).bfloat16()
+    state, d_final, c = states(3, 2, 6, 0.02), states(3, 2, 7, 0.02), cu.tolist()
+    want = ref.scan_gradients(q, k, v, g, beta, state, c, K ** -0.5, d_out, d_final)[5]
+    got = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)[3]
+    for a, b in zip(c, c[1:]):
+        assert float((got[a:b].double() - want[a:b]).norm() / want[a:b].norm()) <= ref.DG_NORM
+
+
 def test_scan_gradients_against_differences(cuda_device):
     """The directional derivative of the 64-bit loss, by central differences, against the kernel's gradients."""
     q, k, v, g, beta, cu = inputs([90, 40], 2, seed=81)
