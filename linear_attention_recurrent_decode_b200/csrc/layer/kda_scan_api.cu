@@ -162,7 +162,7 @@ bool launch(F kernel, int64_t grid, int threads, int smem, kda_stream_t stream, 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.tokens > 0;  // without tokens the forward chains, which look up their sequence before they wait, are first
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
 }
 

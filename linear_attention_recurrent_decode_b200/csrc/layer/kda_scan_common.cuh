@@ -114,33 +114,41 @@ __device__ __forceinline__ void slot_and_head(const ScanParams& p, uint32_t bloc
   slot = q;
   h = block - q * static_cast<uint32_t>(p.HV);
 }
-// The sequence for which `is(n)` holds, or -1; the lanes of each warp search on their own.
+// The last packed sequence with first(n, its first token) <= slot, and its range, or -1; `first` grows with n (decreasing
+// offsets end the search somewhere in range).  The lanes of each warp probe 32 sequences at a time: one step to 32
+// sequences, two to 1024 (4096 sequences of 64 tokens, one head, us a call: 810, and 2350 looking at all of them).
 template <typename F>
-__device__ __forceinline__ int64_t find_sequence(const ScanParams& p, F is) {
-  for (int64_t n0 = 0; n0 < p.N; n0 += 32) {
-    const int64_t n = n0 + (threadIdx.x & 31);
-    const uint32_t found = __ballot_sync(0xffffffffu, n < p.N && is(n));
-    if (found) return n0 + __ffs(static_cast<int>(found)) - 1;
+__device__ __forceinline__ int64_t find_sequence(const ScanParams& p, int64_t slot, int64_t& start, int64_t& len, F first) {
+  uint32_t lo = 0, hi = static_cast<uint32_t>(p.N);
+  for (;;) {
+    const uint32_t step = (hi - lo + 31) >> 5, n = lo + (threadIdx.x & 31) * step;
+    int64_t a = 0, l = 0;
+    if (n < hi) seq_range(p, n, a, l);
+    const uint32_t found = __ballot_sync(0xffffffffu, n < hi && first(n, a) <= slot);
+    if (!found) return -1;
+    const int at = 31 - __clz(static_cast<int>(found));
+    lo += at * step;
+    if (step == 1) {  // a packed call's offsets have 32 bits
+      start = __shfl_sync(0xffffffffu, static_cast<int32_t>(a), at);
+      len = __shfl_sync(0xffffffffu, static_cast<int32_t>(l), at);
+      return lo;
+    }
+    hi = hi < lo + step ? hi : lo + step;
   }
-  return -1;
 }
 // The chunk of a chunk slot (whole warps call it).
 __device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot) {
   ChunkPos c{0, 0, 0};
-  int64_t start, len, t;
+  int64_t start, len;
   if (p.cu == nullptr) {
     c.n = slot / p.seq_chunks;
+    seq_range(p, c.n, start, len);
   } else {
-    c.n = find_sequence(p, [&](int64_t n) {
-      int64_t a, l;
-      seq_range(p, n, a, l);
-      const int64_t at = (slot - first_slot(p, n, a)) * kC;
-      return at >= 0 && at < l;
-    });
+    c.n = find_sequence(p, slot, start, len, [&](int64_t n, int64_t a) { return first_slot(p, n, a); });
     if (c.n < 0) return c;
   }
-  seq_range(p, c.n, start, len);
-  t = (slot - first_slot(p, c.n, start)) * kC;
+  const int64_t t = (slot - first_slot(p, c.n, start)) * kC;
+  if (t >= len) return c;
   c.tok = start + t;
   if (state_block(p, c.n) >= 0) c.tc = static_cast<int32_t>(len - t < kC ? len - t : kC);
   return c;
@@ -156,28 +164,30 @@ struct Segment {
 __device__ __forceinline__ int64_t first_segment(const ScanParams& p, int64_t n, int64_t start) {
   return p.cu == nullptr ? n * p.seq_segs : start / (static_cast<int64_t>(kC) * p.seg_chunks) + n;
 }
-__device__ __forceinline__ Segment segment_of(const ScanParams& p, int64_t n, int64_t slot) {
-  Segment s;
-  s.n = n;
-  seq_range(p, n, s.start, s.len);
-  const int64_t chunks = (s.len + kC - 1) / kC;
-  if (p.seg_chunks == 0) {
-    s.seg = 0, s.segs = 1, s.first = 0, s.chunks = chunks;
-    return s;
-  }
-  s.segs = chunks == 0 ? 1 : (chunks + p.seg_chunks - 1) / p.seg_chunks;
-  s.seg = slot - first_segment(p, n, s.start);
-  s.first = s.seg * p.seg_chunks;
-  s.chunks = chunks - s.first < p.seg_chunks ? chunks - s.first : p.seg_chunks;
-  if (s.seg < 0 || s.seg >= s.segs) s.segs = 0;
-  return s;
-}
 // The segment of a slot (whole warps call it).
 __device__ __forceinline__ Segment locate_segment(const ScanParams& p, int64_t slot) {
-  if (p.seg_chunks == 0) return segment_of(p, slot, slot);
-  const int64_t n = p.cu == nullptr ? slot / p.seq_segs : find_sequence(p, [&](int64_t m) { return segment_of(p, m, slot).segs > 0; });
-  if (n < 0) return Segment{};
-  return segment_of(p, n, slot);
+  Segment s;
+  s.seg = 0, s.segs = 1, s.first = 0;
+  if (p.seg_chunks == 0) {
+    s.n = slot;
+    seq_range(p, s.n, s.start, s.len);
+    s.chunks = (s.len + kC - 1) / kC;
+    return s;
+  }
+  if (p.cu == nullptr) {
+    s.n = slot / p.seq_segs;
+    seq_range(p, s.n, s.start, s.len);
+  } else {
+    s.n = find_sequence(p, slot, s.start, s.len, [&](int64_t n, int64_t a) { return first_segment(p, n, a); });
+    if (s.n < 0) return Segment{};
+  }
+  const int64_t chunks = (s.len + kC - 1) / kC;
+  s.segs = chunks == 0 ? 1 : (chunks + p.seg_chunks - 1) / p.seg_chunks;
+  s.seg = slot - first_segment(p, s.n, s.start);
+  s.first = s.seg * p.seg_chunks;
+  s.chunks = chunks - s.first < p.seg_chunks ? chunks - s.first : p.seg_chunks;
+  if (s.seg >= s.segs) s.segs = 0;
+  return s;
 }
 
 // ---------------------------------------------------------------- decays

@@ -199,6 +199,43 @@ def test_scan_slots_of_long_sequences(cuda_device):
     check_scan(out.view(2 * T, 1, V), final, q, k, v, g, beta, state, cu.tolist(), K ** -0.5)
 
 
+def test_scan_many_sequences(cuda_device):
+    """More sequences than one, and than two, steps of the search for a chunk's sequence, of 0 to 3 tokens but for a long
+    one, some without any at both ends."""
+    lens = [0, 0] + [(n * 7) % 4 for n in range(1500)] + [70] + [(n * 5) % 4 for n in range(700)] + [0]
+    q, k, v, g, beta, cu = inputs(lens, 1, seed=50, tail=3)
+    state = states(len(lens), 1, 8)
+    out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu)
+    d_out, d_final = torch.ones_like(v), states(len(lens), 1, 9)
+    got = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)
+    c = cu.tolist()
+    for n in (0, 1, 2, 3, 4, 31, 32, 33, 1023, 1024, 1025, 1501, 1502, 1503, 2000, len(lens) - 2, len(lens) - 1):
+        rows = slice(c[n], c[n + 1])
+        x = [t[rows].contiguous() for t in (q, k, v, g, beta)]
+        one = torch.tensor([0, lens[n]], dtype=torch.int32, device="cuda")
+        o, f = kda.kda_scan(*x, state[n:n + 1], cu_seqlens=one)
+        d = kda.kda_scan_backward(d_out[rows].contiguous(), *x, state[n:n + 1], d_final_state=d_final[n:n + 1], cu_seqlens=one)
+        assert torch.equal(out[rows], o) and torch.equal(final[n], f[0]), n
+        assert all(torch.equal(a[rows], b) for a, b in zip(got[:5], d)) and torch.equal(got[5][n], d[5][0]), n
+    for a, b in zip(c, c[1:]):
+        assert bool(torch.isfinite(out[a:b]).all()) and bool(torch.isfinite(got[3][a:b]).all())
+
+
+def test_scan_no_tokens_is_ordered_behind_the_stream(cuda_device):
+    """Dense sequences of no token: the states of the named slots pass through, named by work still in flight."""
+    pool, final = states(6, 2, 12), torch.zeros(6, 2, K, V, device="cuda")
+    slots = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    big = torch.randn(4096, 4096, device="cuda")
+    empty = [torch.empty(3, 0, 2, w, dtype=t, device="cuda") for w, t in ((K, torch.bfloat16),) * 3 + ((K, torch.float32),)]
+    beta = torch.empty(3, 0, 2, device="cuda")
+    big @ big
+    slots.copy_(torch.tensor([4, 0, 2], device="cuda"))
+    kda.kda_scan(*empty, beta, pool, slot_idx=slots, final_state=final)
+    want = torch.zeros_like(final)
+    want[[4, 0, 2]] = pool[[4, 0, 2]]
+    assert torch.equal(final, want)
+
+
 def test_scan_bad_offsets_stay_in_bounds(cuda_device):
     """Offsets that decrease or leave the rows are clamped: an error in them cannot reach other memory."""
     q, k, v, g, beta, _ = inputs([100], 2, seed=41)
