@@ -51,28 +51,33 @@ struct PrepTiles {    // over the factors once those are in registers; pairs (hi
 };
 enum PrepMax { kMxV, kMxKt, kMxQt, kMxKe, kMxR32K, kMxR32Q, kMxC32, kMxR16K, kMxR16Q, kMxC16, kMxP, kMxY, kMxWr, kMxRt, kMxBeta, kMxCount };
 
+struct PrepNext {     // the next chunk's rows, over all tiles but Kt once those are read
+  unsigned char kt[2 * Record::kPlane];
+  RawRows raw;
+  uint4 v[kC * kV / 8];
+};
+
 struct PrepSmem {
   union {
-    struct {
-      PrepFactors f;
-      __nv_bfloat16 q[kC][kK];          // the raw queries
-    };
+    PrepFactors f;
     PrepTiles t;
+    PrepNext next;
   };
   unsigned char vt[Record::kPlane];     // V tile [t][v]
   float a[kC][kAP];                     // A
   float pm[kC][kAP];                    // P; then the tile M
-  float y[kC][kAP];                     // Y; a, pm and y first hold the raw log-decays and keys
+  float y[kC][kAP];                     // Y
   Sum end[kNB][kK];                     // log-decay of a sub-block
   float up[kNB][kK], dn[kNB][kK];       // to Kt and Qt, to Ke
   float x32[kNB][kK], x16[kNB][kK];     // to the tiles r32 or c32, r16 or c16
   float beta[kC];
   uint32_t mx[kMxCount];                // block maxima (float bits)
   int exact[kNB];
+  uint4 taken;                          // the block taken over next
+  uint64_t taken_full;
 };
 static_assert(2 * kC * kC * 2 <= sizeof(float) * kC * kAP, "the M tile fits into pm");
-static_assert(offsetof(PrepSmem, y) - offsetof(PrepSmem, a) >= sizeof(float) * kC * kK && sizeof(float) * kC * kAP >= 2 * kC * kK,
-              "the raw rows fit");
+static_assert(sizeof(PrepNext) <= sizeof(PrepTiles), "the raw rows fit over the tiles");
 static_assert(sizeof(PrepSmem) <= 232448, "shared memory of an SM");
 
 __device__ __forceinline__ void block_max(uint32_t* slot, float m, int lane) {
@@ -225,36 +230,45 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int64_t slot, h;
   slot_and_head(p, blockIdx.x, slot, h);
+  if (tid == 0) {
+    mbar_init(&sm.taken_full, 1);
+    mbar_fence_init();
+  }
   wait_upstream();
-  if (tid < kMxCount) sm.mx[tid] = 0;
-  if (tid < kNB) sm.exact[tid] = 0;
-  const ChunkPos pos = locate(p, slot);
+  ChunkPos pos = locate(p, slot);
+  if (pos.tc == 0) return;
+  auto fetch = [&]() {
+    fetch_rows<kPrepThreads>(p, pos.tok, pos.tc, h, sm.next.raw.g, sm.next.raw.k, sm.next.raw.q);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = tid + j * kPrepThreads, t = c >> 4;
+      cp_async16(&sm.next.v[c], p.v + (pos.tok + (t < pos.tc ? t : pos.tc - 1)) * p.v_ts + h * kV + (c & 15) * 8);
+    }
+  };
+  auto scale_of = [&](PrepMax i) { return pow2_scale(__uint_as_float(sm.mx[i])); };
+  fetch();
+  for (uint32_t phase = 0;; phase ^= 1) {
   const int tc = pos.tc;
-  if (tc == 0) return;
-  __syncthreads();
   unsigned char* const rec = record(p, slot, h);
   float* const hdr = reinterpret_cast<float*>(rec);
-  auto scale_of = [&](PrepMax i) { return pow2_scale(__uint_as_float(sm.mx[i])); };
-
-  float (*const graw)[kK] = reinterpret_cast<float (*)[kK]>(&sm.a[0][0]);
-  __nv_bfloat16 (*const kraw)[kK] = reinterpret_cast<__nv_bfloat16 (*)[kK]>(&sm.y[0][0]);
-  fetch_rows<kPrepThreads>(p, pos.tok, tc, h, graw, kraw, sm.q);
-  // v: 16-byte pieces, kept in registers until the scale is known
-  uint4 vraw[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int t = (tid + j * kPrepThreads) >> 4;
-    vraw[j] = *reinterpret_cast<const uint4*>(p.v + (pos.tok + (t < tc ? t : tc - 1)) * p.v_ts + h * kV + (tid & 15) * 8);
-  }
+  float be = 0.f;
+  if (warp < 2 && tid < tc) be = __ldg(p.beta + (pos.tok + tid) * p.beta_ts + h);
+  cp_async_wait_all();
+  __syncthreads();
+  if (tid == 0) request_block(&sm.taken, &sm.taken_full);
+  if (tid < kMxCount) sm.mx[tid] = 0;
+  if (tid < kNB) sm.exact[tid] = 0;
   // ---- 1. decay factors: thread = channel and sub-block
   const int ch = tid & (kK - 1), b = tid >> 7;
   SubFactors sf;
+  uint4 vraw[2];  // v: kept in registers until the scale is known
   float m_ku = 0.f, m_qu = 0.f, m_kd = 0.f;
   {
     float g[kB], kv[kB], qv[kB], up[kB], dn[kB];
-    cp_async_wait_all();
-    __syncthreads();
-    read_sub_block(graw, kraw, sm.q, tc, b, ch, g, kv, qv);
+    read_sub_block(sm.next.raw.g, sm.next.raw.k, sm.next.raw.q, tc, b, ch, g, kv, qv);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) vraw[j] = sm.next.v[tid + j * kPrepThreads];
+    __syncthreads();  // the factors go over the rows
     sf = sub_factors(g, up, dn);
 #pragma unroll
     for (int t = 0; t < kB; ++t) {
@@ -282,7 +296,6 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
   }
   block_max(&sm.mx[kMxV], m_v, lane);
   if (warp < 2) {
-    const float be = tid < tc ? __ldg(p.beta + (pos.tok + tid) * p.beta_ts + h) : 0.f;
     sm.beta[tid] = be;
     hdr[Record::kBeta + tid] = be;
     block_max(&sm.mx[kMxBeta], fabsf(be), lane);
@@ -436,7 +449,21 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     for (int j = 0; j < kNB; ++j)
       if (sm.exact[j]) prep_exact_block(p, sm, j, pos.tok, tc, h);
   }
-  __syncthreads();
+  // the next chunk: its rows arrive over the tiles just read while the rest is computed
+  bool more = false, ok = true;
+  for (;;) {
+    ok = __syncthreads_and(mbar_wait(&sm.taken_full, phase));
+    const int64_t block = ok ? taken_block(&sm.taken) : -1;
+    if (block < 0) break;
+    slot_and_head(p, static_cast<uint32_t>(block), slot, h);
+    pos = locate(p, slot);
+    more = pos.tc > 0;
+    if (more) break;
+    __syncthreads();
+    if (tid == 0) request_block(&sm.taken, &sm.taken_full);
+    phase ^= 1;
+  }
+  if (more) fetch();
 
   auto put_qt_ke = [&]() {
 #pragma unroll
@@ -602,6 +629,11 @@ __global__ void __launch_bounds__(kPrepThreads, 1) kda_scan_prep_kernel(const __
     hdr[Record::kScY] = sc_y;
     hdr[Record::kMxWr] = __uint_as_float(sm.mx[kMxWr]);
     hdr[Record::kMxRt] = __uint_as_float(sm.mx[kMxRt]);
+  }
+  if (!more) {
+    if (!ok && tid == 0) set_error(p);
+    return;
+  }
   }
 }
 

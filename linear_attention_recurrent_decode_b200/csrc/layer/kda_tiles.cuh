@@ -205,4 +205,27 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* mbar, uint32_t parity) {
 // Orders this thread's ordinary shared-memory accesses before later bulk copies into the same bytes.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// ---------------------------------------------------------------- blocks that go on
+// A running block takes over a block of the same grid that has not started (cluster launch control): request (one thread;
+// the last answer has been read by all) and, once the barrier's phase is done, its index, or -1 if there is none left.
+// After a -1 no further request is made.
+__device__ __forceinline__ void request_block(uint4* answer, uint64_t* mbar) {
+  fence_async();
+  mbar_expect(mbar, sizeof(uint4));
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(smem_addr(answer)), "r"(smem_addr(mbar)) : "memory");
+}
+__device__ __forceinline__ int64_t taken_block(const uint4* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, a;\n\t}\n"
+      : "=r"(got), "=r"(x) : "r"(smem_addr(answer)) : "memory");
+  fence_async();
+  return got ? static_cast<int64_t>(x) : -1;
+}
+
 }  // namespace kdal
