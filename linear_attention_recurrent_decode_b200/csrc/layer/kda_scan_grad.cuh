@@ -37,7 +37,7 @@ constexpr int kDP = kC + 4;
 
 struct GradSmem {
   // The operand tiles; later dP and dA over the first, and the factors after them.
-  unsigned char s0[kV * kK * 4];             // S0^T [v][i] hi, lo
+  unsigned char s0[kV * kK * 4];             // S0^T [v][i] hi, lo; before: the chunk's raw rows
   unsigned char ds[kV * kK * 4];             // dS1^T; before: dU^T and beta Y
   unsigned char dr[2 * Record::kPlane];      // dR^T [v][t]
   unsigned char r[2 * Record::kPlane];       // r^T [v][t]
@@ -52,7 +52,7 @@ struct GradSmem {
   float dp_own[kC];                          // dP_tt
   uint32_t mx_do, mx_dr;
   int exact[kNB];
-  uint64_t bar[4];                           // dU, Y, r and S0; dS1; the products, first part and last
+  uint64_t bar[5];                           // dU, Y and r; S0; dS1; dP and dA; the other products
   uint32_t tmem;
 };
 // Columns of tensor memory: products of 64 tokens (M) with 128 channels or 64 tokens.
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   int64_t slot, h;
   slot_and_head(p, blockIdx.x, slot, h);
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&sm.bar[i], 1);
+    for (int i = 0; i < 5; ++i) mbar_init(&sm.bar[i], 1);
     mbar_fence_init();
     sm.mx_do = sm.mx_dr = 0;
   }
@@ -179,30 +179,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   const unsigned char* const rec = record(p, slot, h);
-  if (tid == 0) {
-    mbar_expect(&sm.bar[0], Record::kHdr + Record::kScBytes + Record::kDnBytes + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane + kV * kK * 4);
-    bulk_load(sm.hdr, rec, Record::kHdr, &sm.bar[0]);
-    bulk_load(sm.sc, rec + Record::kSc, Record::kScBytes, &sm.bar[0]);
-    bulk_load(sm.dn, rec + Record::kDn, Record::kDnBytes, &sm.bar[0]);
-    bulk_load(sm.ds, rec + Record::kDU, 2 * Record::kPlane, &sm.bar[0]);
-    bulk_load(sm.ds + 2 * Record::kPlane, rec + Record::kY, kC * kC * 4, &sm.bar[0]);
-    bulk_load(sm.r, rec + Record::kR, 2 * Record::kPlane, &sm.bar[0]);
-    bulk_load(sm.s0, rec + Record::kS, kV * kK * 4, &sm.bar[0]);
-  }
-  // ---- dO as an fp16 tile (exact after scaling)
+  RawRows& raw = *reinterpret_cast<RawRows*>(sm.s0);
+  static_assert(sizeof(RawRows) <= sizeof(sm.s0), "the raw rows fit");
+  // ---- dO as an fp16 tile (exact after scaling); its loads go ahead of the copies, which keep the SM's port busy
   const int ch = tid & (kK - 1), sub = tid >> 7;
   {
-    uint4 raw[2];
+    uint4 raw_do[2];
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = tid & 63, pc = (tid >> 6) + 8 * j;
-      raw[j] = *reinterpret_cast<const uint4*>(p.d_out + (pos.tok + (t < tc ? t : tc - 1)) * p.d_out_ts + h * kV + pc * 8);
+      raw_do[j] = *reinterpret_cast<const uint4*>(p.d_out + (pos.tok + (t < tc ? t : tc - 1)) * p.d_out_ts + h * kV + pc * 8);
     }
+    if (tid == 0) {
+      mbar_expect(&sm.bar[0], Record::kHdr + Record::kScBytes + Record::kDnBytes + 2 * Record::kPlane + kC * kC * 4 + 2 * Record::kPlane);
+      bulk_load(sm.hdr, rec, Record::kHdr, &sm.bar[0]);
+      bulk_load(sm.sc, rec + Record::kSc, Record::kScBytes, &sm.bar[0]);
+      bulk_load(sm.dn, rec + Record::kDn, Record::kDnBytes, &sm.bar[0]);
+      bulk_load(sm.ds, rec + Record::kDU, 2 * Record::kPlane, &sm.bar[0]);
+      bulk_load(sm.ds + 2 * Record::kPlane, rec + Record::kY, kC * kC * 4, &sm.bar[0]);
+      bulk_load(sm.r, rec + Record::kR, 2 * Record::kPlane, &sm.bar[0]);
+    }
+    fetch_rows<kGradThreads>(p, pos.tok, tc, h, raw.g, raw.k, raw.q);  // for step 3
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if ((tid & 63) >= tc) raw[j] = make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+      if ((tid & 63) >= tc) raw_do[j] = make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {raw_do[j].x, raw_do[j].y, raw_do[j].z, raw_do[j].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int t = tid & 63, pc = (tid >> 6) + 8 * j;
-      uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+      uint32_t w[4] = {raw_do[j].x, raw_do[j].y, raw_do[j].z, raw_do[j].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         w[e] = as_u32(__floats2half2_rn(__uint_as_float(w[e] << 16) * sc, __uint_as_float(w[e] & 0xffff0000u) * sc));
@@ -289,23 +291,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       store_frag<Core<kV>>(sm.dr, Record::kPlane, v0, (u ? 3 - first : first) * 16, lane, dh, dl);
     }
   }
+  cp_async_wait_all();
   fence_async();  // dO and dR come before the products' reads, the reads of dU and Y before dS1 is copied over them
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  // the chunk's rows, for step 3, over dU and Y; dS1 follows them
-  RawRows& raw = *reinterpret_cast<RawRows*>(sm.ds);
-  static_assert(sizeof(RawRows) <= sizeof(sm.ds), "the raw rows fit");
-  fetch_rows<kGradThreads>(p, pos.tok, tc, h, raw.g, raw.k, raw.q);
-  // ---- 2. The products on the tensor cores, one warp's: dQt = dO S0^T, dKt = -dR S0^T, dP = dO r, dA = -dR r, and, once
-  // dS1 is there, dKe = r dS1^T (scales and signs come later).  The other warps work on the decay factors meanwhile.
+  // ---- 2. The products on the tensor cores, one warp's: dP = dO r, dA = -dR r and, once S0 and dS1 are there,
+  // dQt = dO S0^T, dKt = -dR S0^T, dKe = r dS1^T (scales and signs come later).  The other warps work on the decay factors
+  // meanwhile.
   const float sc_do_inv = pow2_inv(sc_do), sc_dr_inv = pow2_inv(pow2_scale(__uint_as_float(sm.mx_dr)));
   if (warp == 0) {
-    umma_tiles<kK, kV, kC, false, kV, true, true>(tmem + GradColumns::kDQ, a_do, 0, a_s0, kV * kK * 2);
-    umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKRow, a_dr, Record::kPlane, a_s0, kV * kK * 2);
     umma_tiles<kC, kV, kC, false, kV, true, true>(tmem + GradColumns::kDP, a_do, 0, a_r, Record::kPlane);
     umma_tiles<kC, kV, kV, true, kV, true, false>(tmem + GradColumns::kDA, a_dr, Record::kPlane, a_r, Record::kPlane);
-    umma_commit(&sm.bar[2]);
+    umma_commit(&sm.bar[3]);
   }
   if (tid < tc) {
     float s = 0.f;
@@ -317,14 +315,14 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   float up[kB], dn[kB], kv[kB], qv[kB];
   {
     float g[kB];
-    cp_async_wait_all();
-    __syncthreads();
     read_sub_block(raw.g, raw.k, raw.q, tc, sub, ch, g, kv, qv);
     fence_async();
-    __syncthreads();  // the rows are read: dS1 goes over them
+    __syncthreads();  // the rows are read: S0 goes over them
     if (tid == 0) {
       mbar_expect(&sm.bar[1], kV * kK * 4);
-      bulk_load(sm.ds, rec + Record::kDS, kV * kK * 4, &sm.bar[1]);
+      bulk_load(sm.s0, rec + Record::kS, kV * kK * 4, &sm.bar[1]);
+      mbar_expect(&sm.bar[2], kV * kK * 4);
+      bulk_load(sm.ds, rec + Record::kDS, kV * kK * 4, &sm.bar[2]);
     }
     const SubFactors f = sub_factors(g, up, dn);
     if (f.exact) sm.exact[sub] = 1;
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   }
   // ---- 4. exp(Gamma_C) sum_v S0 dS1: warp = eight channels, lanes over the value columns; lane e < 8 keeps channel e's
   // dS1 has a scale per 32 value columns, which dKe contracts: r (done with otherwise) takes up the differences
-  ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[2], 0)) && ok;
+  ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[3], 0)) && ok;
   const float sc_ds = fminf(fminf(sm.sc[Record::kScDS], sm.sc[Record::kScDS + 1]), fminf(sm.sc[Record::kScDS + 2], sm.sc[Record::kScDS + 3]));
   fence_after_sync();
 #pragma unroll
@@ -349,10 +347,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   }
   fence_async();
   ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[1], 0)) && ok;
+  if (warp == 0) {
+    umma_tiles<kK, kV, kC, false, kV, true, true>(tmem + GradColumns::kDQ, a_do, 0, a_s0, kV * kK * 2);
+    umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKRow, a_dr, Record::kPlane, a_s0, kV * kK * 2);
+  }
+  ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[2], 0)) && ok;
   __syncthreads();
   if (warp == 0) {
     umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKCol, a_r, Record::kPlane, a_ds, kV * kK * 2);
-    umma_commit(&sm.bar[3]);
+    umma_commit(&sm.bar[4]);
   }
   float e_sum = 0.f;
   {
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     }
   }
   // ---- 5. the factors, dP and dA over the operand tiles
-  ok = __syncthreads_and(mbar_wait(&sm.bar[3], 0) && ok);  // every product is done, and every warp with S0 and dS1
+  ok = __syncthreads_and(mbar_wait(&sm.bar[4], 0) && ok);  // every product is done, and every warp with S0 and dS1
   fence_after_sync();
 #pragma unroll
   for (int t = 0; t < kB; ++t) {
