@@ -441,6 +441,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       for (int n = 0; n < 4; ++n) to[n][hf] = *reinterpret_cast<const __nv_bfloat162*>(at + n * 8);
     }
   };
+  auto put_out = [&](__nv_bfloat16* to, int64_t ts, int n, int hf, float x, float y) {
+    const int t = row + hf * 8;
+    if (t < tc) *reinterpret_cast<__nv_bfloat162*>(to + (pos.tok + t) * ts + h * kK + col + n * 8) = __floats2bfloat162_rn(x, y);
+  };
   // the products with block J's keys; with its queries and keys
   auto row_block = [&](int J, float (&xq)[4][4], float (&xk)[4][4]) {
 #pragma unroll
@@ -522,19 +526,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         float2& at = *reinterpret_cast<float2*>(&pr.up[row + hf * 8][col + n * 8]);  // this thread's own elements
+        const float own = sm.dp_own[row + hf * 8];
         const float2 u2 = at, q2 = __bfloat1622float2(qe[n][hf]), k2 = __bfloat1622float2(ke[n][hf]);
         float2 y;
         auto element = [&](int e, float u, float q, float k) {
           const float ui = exact ? 1.f : u, bq = dq[n][e] * u, bk = dkr[n][e] * u, iq = xq[n][e] * ui, ik = xk[n][e] * ui;
           const float before = fmaf(q, bq, k * bk);
           sum[n][e & 1] += before;
-          dq[n][e] = bq + iq;
-          dkr[n][e] = bk + ik;
+          dq[n][e] = fmaf(own, k, bq + iq);
+          dkr[n][e] = fmaf(own, q, bk + ik);
           return before + fmaf(q, iq, k * ik);
         };
         y.x = element(2 * hf, u2.x, q2.x, k2.x);
         y.y = element(2 * hf + 1, u2.y, q2.y, k2.y);
         at = y;
+        put_out(p.dq, p.dq_ts, n, hf, dq[n][2 * hf], dq[n][2 * hf + 1]);
       }
     block_sum(sum, pr.rows);
   }
@@ -575,41 +581,23 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
           const float behind = k * bc;
           sum[n][e & 1] += behind;
           inside = fmaf(-k, ic, inside);
-          dkr[n][e] += (bc + ic) + last;
+          dkr[n][e] += (bc + ic) + last;  // dk
           return fmaf(k, last, behind);
         };
         z.x = element(2 * hf, d2.x, k2.x, fct.x, y.x);
         z.y = element(2 * hf + 1, d2.y, k2.y, fct.y, y.y);
         at = y;
         end = z;
+        put_out(p.dk, p.dk_ts, n, hf, dkr[n][2 * hf], dkr[n][2 * hf + 1]);
       }
     }
     block_sum(sum, pr.columns);
   }
   fence_before_sync();
   __syncthreads();  // the factors are dead: the decays' gradients go over them
-  // ---- 8. dq, dk; dg: thread = channel and sub-block
-  __nv_bfloat162 qe[4][2], ke[4][2];
-  fetch(p.q, p.q_ts, qe);
-  fetch(p.k, p.k_ts, ke);
+  // ---- 8. dg: thread = channel and sub-block
   float* const ev = &pr.qu[0][0];  // [128]
   if (lane < 8) ev[warp * 8 + lane] = e_sum;
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int t = row + hf * 8, i = col + n * 8, e = 2 * hf;
-      const int64_t tk = pos.tok + t;
-      const float own = sm.dp_own[t];
-      const float2 q = __bfloat1622float2(qe[n][hf]), k = __bfloat1622float2(ke[n][hf]);
-      if (t < tc) {
-        *reinterpret_cast<__nv_bfloat162*>(p.dq + tk * p.dq_ts + h * kK + i) =
-            __floats2bfloat162_rn(fmaf(own, k.x, dq[n][e]), fmaf(own, k.y, dq[n][e + 1]));
-        *reinterpret_cast<__nv_bfloat162*>(p.dk + tk * p.dk_ts + h * kK + i) =
-            __floats2bfloat162_rn(fmaf(own, q.x, dkr[n][e]), fmaf(own, q.y, dkr[n][e + 1]));
-      }
-    }
-  }
   float lead[kB], ahead = 0.f;  // of the sub-block: the columns' from behind it and Ke dKe, ahead of each token
 #pragma unroll
   for (int t = 0; t < kB; ++t) {
