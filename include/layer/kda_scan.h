@@ -45,7 +45,8 @@
  * (operands as fp16 or tf32 pairs of 22 bits, fp32 accumulation, decays
  * accumulated in pairs of fp32); bf16 results are rounded once.  An infinity or NaN in a
  * sequence's inputs makes that sequence's and head's results undefined from
- * its chunk (64 tokens) on, nothing else.
+ * its chunk (64 tokens) on, nothing else; but a log-decay of -inf, like any
+ * below -1e4, is a decay of zero.
  *
  * Workspace.  Caller-owned device memory of kda_scan_workspace_bytes bytes; the
  * library allocates nothing.  With save = 1 (and a workspace sized for
@@ -59,7 +60,8 @@
  *
  * Execution: kda_scan enqueues 2 kernels (4 where long sequences of few heads
  * are walked in segments), kda_scan_backward 2 (4), and those of the forward pass
- * before them with saved = 0, on `stream`; no host synchronisation; can be captured in a CUDA graph.
+ * before them with saved = 0, on `stream`; no host synchronisation; can be
+ * captured in a CUDA graph.
  * Results do not depend on the launch's timing (no atomics on data).
  *
  * Errors: as in kda_decode.h, nothing is enqueued unless KDA_OK is returned.

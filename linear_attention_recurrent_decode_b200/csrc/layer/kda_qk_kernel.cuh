@@ -13,10 +13,10 @@
 // of one tensor; its rows' cos and sin are computed once, in shared memory, and
 // shared by all heads, while the loads are in flight.
 //
-// Measured (B200, 16384 rows, D = 128): forward, 32 + 32 heads, 101 us, 5.3 TB/s
+// Measured (B200, 16384 rows, D = 128): forward, 32 + 32 heads, 100 us, 5.3 TB/s
 // (0.81 of the measured copy rate), the instructions being the next bound (0.7
 // of the issue slots); four heads a thread and five blocks an SM against 115 us
-// for two heads.  Backward with weights, 32 + 8 heads, 144 us, 3.5 TB/s: two
+// for two heads.  Backward with weights, 32 + 8 heads, 140 us, 3.6 TB/s: two
 // heads a thread and three blocks an SM against 147 to 165 us for one, three or
 // four; loading the next tile ahead of computing one was slower (170 us, the
 // registers).

@@ -45,7 +45,8 @@ bool chunk_slots(int64_t N, int64_t T, bool packed, int64_t* slots) {
 // Chunks of a segment, 0 for none, and the segment slots of the call.  Segments are for calls whose sequences and heads
 // leave half the SMs idle or more, with room for a sequence of 24 chunks (below, walking it twice and joining cost what
 // the segments save); as long as the first of the two walks, two blocks a segment, then fills the SMs once, and at least
-// 8 chunks.  Measured, us a call: 8192 tokens of 8 heads 590 without and 317 with segments, with gradients 1618 and 799.
+// 8 chunks.  Measured when they were added, us a call: 8192 tokens of 8 heads 590 without and 317 with segments, with
+// gradients 1618 and 799.
 constexpr int64_t kSms = 148;
 bool segments(int64_t N, int64_t T, bool packed, int64_t HV, int32_t* seg_chunks, int64_t* slots) {
   const int64_t total = packed ? T / ks::kC : (T + ks::kC - 1) / ks::kC;  // the longest sequence's chunks at most

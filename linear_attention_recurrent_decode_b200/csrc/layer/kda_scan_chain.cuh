@@ -30,6 +30,10 @@
 // behind the state's, under the next chunk's first conversion, and the compute
 // warps read them back and store them while that chunk's first product runs
 // (four warps of their own for it left 80 registers a thread, too few).
+//
+// Measured (B200): 4.7 us a chunk forwards and 5.2 backwards, whatever the
+// number of CTAs up to one an SM: the latency of that path (conversion, product,
+// read-back, twice), not the tensor cores (22 % of their cycles) or memory (22 %).
 #pragma once
 
 #include "kda_scan_common.cuh"

@@ -23,9 +23,14 @@
 // middle of its cumulative log-decays (see SubFactors), and the products run in
 // tf32 pairs, whose range takes the e^+-60 of those factors.
 //
-// What bounds it: the instructions of the factors and of the fp16 splits, not
-// the products.  512 threads, one sub-block and channel each (256 left the
-// schedulers short of warps); one CTA an SM, its shared memory.
+// What bounds it: the latency of its phases, each of which leaves half of the
+// issue slots empty (the factors 4000 cycles of a chunk's 31000, the products
+// inside and across sub-blocks 6000, the tiles' splits 4500, the solve 5700, Rt
+// and Wr 5000); 512 threads, one sub-block and channel each (256 left the
+// schedulers short of warps), one CTA an SM by its shared memory and registers.
+// A block goes on with another chunk, whose rows arrive under the solve (see
+// request_block).  Measured (B200): 2112 chunks and heads 273 us, one block a
+// chunk 291; a plain copy would move its bytes in 70.
 #pragma once
 
 #include "kda_scan_common.cuh"

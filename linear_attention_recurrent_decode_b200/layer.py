@@ -225,7 +225,8 @@ def kda_scan(q, k, v, g, beta, initial_state=None, *, cu_seqlens=None, slot_idx=
 
     Packed: q, k ``[rows, HV, K]``, v ``[rows, HV, V]`` (bf16), g ``[rows, HV, K]``, beta ``[rows, HV]`` (fp32) with
     ``cu_seqlens`` (device int32 ``[N + 1]``).  Dense: the same with ``[N, T, ...]`` and no ``cu_seqlens``.  Rows may be
-    strided views (slices of one packed buffer).  Rows outside every sequence are neither read nor written.
+    strided views (slices of one packed buffer).  Rows outside every sequence are neither read nor written: in an ``out``
+    allocated here they hold anything.
 
     States are fp32 ``[N, HV, K, V]``; ``initial_state=None`` starts from zeros, ``final_state`` is allocated if not
     given.  For serving, ``slot_idx`` (device int32 ``[N]``) names blocks of a pool: ``initial_state`` is the pool,
@@ -271,7 +272,8 @@ def kda_scan_backward(d_out, q, k, v, g, beta, initial_state=None, *, d_final_st
     The forward call's inputs, ``cu_seqlens`` and ``scale`` are given again.  With ``saved=True``, ``workspace`` is the
     one a ``kda_scan(..., save=True)`` of the same inputs left; otherwise the forward pass is computed again first.
     Gradients are allocated if not given; given ones may be strided views.  Gradient rows outside every sequence are left
-    as they were."""
+    as they were, and hold anything if allocated here: where a batch is padded and all rows are summed over later, give
+    zeroed gradients."""
     if saved and workspace is None:
         raise ValueError("saved=True needs the forward call's workspace")
     a, lead, (N, HV, K, V), workspace, dev = _scan_args(q, k, v, g, beta, cu_seqlens, scale, workspace, True)
