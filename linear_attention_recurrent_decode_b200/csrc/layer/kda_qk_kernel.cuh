@@ -89,7 +89,6 @@ __device__ __forceinline__ float head_sum(float x) {
 // [thread][2], so that neighbouring lanes read neighbouring 16 bytes (in pair order they met in two of the banks).  The angle is
 // position * inv_freq in fp64, taken in half turns and reduced to one turn
 // there; cos and sin then see an argument exact to fp32.
-template <QkRotate ROT>
 __device__ __forceinline__ void qk_table(const QkParams& p, int64_t row0, int span, float2* tab) {
   const int half = p.rot >> 1;
   for (int e = threadIdx.x; e < span * half; e += kQkThreads) {
@@ -102,42 +101,52 @@ __device__ __forceinline__ void qk_table(const QkParams& p, int64_t row0, int sp
     u -= 2.0 * rint(0.5 * u);
     float s, c;
     sincospif(static_cast<float>(u), &s, &c);
-    constexpr int kLog = ROT == kQkHalves ? 3 : 2;  // pairs of a thread
-    const int at = ((((i & ((1 << kLog) - 1)) >> 1) * (half >> kLog) + (i >> kLog)) << 1) + (i & 1);
+    const int at = ((((i & 3) >> 1) * (half >> 2) + (i >> 2)) << 1) + (i & 1);  // four pairs of a thread
     tab[r * half + at] = make_float2(c * p.scale, s * p.scale);
   }
 }
 
+// Where a thread's 8 components lie in a head, four and four.  Neighbours but for the halves' layout, where both
+// partners of a pair are the same thread's: with 8 neighbours each, trading them by shuffles was 10 % of the time.
+template <QkRotate ROT>
+struct QkPlace {
+  int32_t o0, o1;
+  __device__ __forceinline__ QkPlace(const QkParams& p, int l) {
+    const bool apart = ROT == kQkHalves && l * 8 < p.rot;
+    o0 = apart ? l * 4 : l * 8;
+    o1 = apart ? (p.rot >> 1) + l * 4 : l * 8 + 4;
+  }
+  __device__ __forceinline__ uint4 load(const __nv_bfloat16* head) const {
+    if constexpr (ROT != kQkHalves) return *reinterpret_cast<const uint4*>(head + o0);
+    const uint2 a = *reinterpret_cast<const uint2*>(head + o0), b = *reinterpret_cast<const uint2*>(head + o1);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* head, uint4 x) const {
+    if constexpr (ROT != kQkHalves) {
+      *reinterpret_cast<uint4*>(head + o0) = x;
+    } else {
+      *reinterpret_cast<uint2*>(head + o0) = make_uint2(x.x, x.y);
+      *reinterpret_cast<uint2*>(head + o1) = make_uint2(x.z, x.w);
+    }
+  }
+};
+
 // This thread's 8 components turned by the row's angles (cs: its row of the table), backwards if BACK.
 template <QkRotate ROT, bool BACK>
 __device__ __forceinline__ void qk_rotate(const QkParams& p, const float2* cs, int l, float (&f)[8]) {
-  if constexpr (ROT == kQkInterleaved) {
-    if (l * 8 >= p.rot) return;
-    const float4* const t4 = reinterpret_cast<const float4*>(cs) + l;
+  if (ROT == kQkNone || l * 8 >= p.rot) return;
+  const float4* const t4 = reinterpret_cast<const float4*>(cs) + l;
+  constexpr int kA = ROT == kQkHalves ? 1 : 2, kB = ROT == kQkHalves ? 4 : 1;  // pair i: components kA i and kA i + kB
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 t = t4[e * (p.rot >> 3)];
-      const float a = f[4 * e], b = f[4 * e + 1], c = f[4 * e + 2], d = f[4 * e + 3];
-      const float s0 = BACK ? -t.y : t.y, s1 = BACK ? -t.w : t.w;
-      f[4 * e] = a * t.x - b * s0;
-      f[4 * e + 1] = a * s0 + b * t.x;
-      f[4 * e + 2] = c * t.z - d * s1;
-      f[4 * e + 3] = c * s1 + d * t.z;
-    }
-  } else if constexpr (ROT == kQkHalves) {
-    const int hv = p.rot >> 4;  // threads of a half
-    const bool first = l < hv, in = l < 2 * hv;
-    const int lane = threadIdx.x & 31, from = in ? (first ? lane + hv : lane - hv) : lane;
-    const float sg = first == BACK ? 1.f : -1.f;
-    const float4* const t4 = reinterpret_cast<const float4*>(cs) + (first ? l : l - hv);
+  for (int e = 0; e < 2; ++e) {
+    const float4 t = t4[e * (p.rot >> 3)];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float o0 = __shfl_sync(0xffffffffu, f[2 * e], from), o1 = __shfl_sync(0xffffffffu, f[2 * e + 1], from);
-      if (in) {
-        const float4 t = t4[e * hv];
-        f[2 * e] = fmaf(sg * t.y, o0, f[2 * e] * t.x);
-        f[2 * e + 1] = fmaf(sg * t.w, o1, f[2 * e + 1] * t.z);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const float c = i ? t.z : t.x, s = BACK ? -(i ? t.w : t.y) : (i ? t.w : t.y);
+      float &x = f[kA * (2 * e + i)], &y = f[kA * (2 * e + i) + kB];
+      const float a = x, b = y;
+      x = a * c - b * s;
+      y = a * s + b * c;
     }
   }
 }
@@ -176,17 +185,18 @@ __global__ void __launch_bounds__(kQkThreads, 5) kda_qk_forward_kernel(const __g
   const int grp = threadIdx.x >> LANES, l = threadIdx.x & ((1 << LANES) - 1);
   const bool used = l * 8 < p.D;
   const QkTile<LANES, VPT> it(t, static_cast<int64_t>(blockIdx.x) - (which ? p.t[0].tiles : 0), grp, used);
-  const __nv_bfloat16* const xb = t.x + it.row0 * t.x_ts + l * 8;
-  __nv_bfloat16* const yb = t.y + it.row0 * t.y_ts + l * 8;
+  const QkPlace<ROT> at(p, l);
+  const __nv_bfloat16* const xb = t.x + it.row0 * t.x_ts;
+  __nv_bfloat16* const yb = t.y + it.row0 * t.y_ts;
   uint4 x[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
-    x[j] = it.in[j] ? *reinterpret_cast<const uint4*>(xb + it.r[j] * t.x_ts + it.head[j] * p.D) : make_uint4(0, 0, 0, 0);
+    x[j] = it.in[j] ? at.load(xb + it.r[j] * t.x_ts + it.head[j] * p.D) : make_uint4(0, 0, 0, 0);
   float w[8];
   const bool weighted = t.w != nullptr;
-  if (weighted && used) unpack8(__ldg(reinterpret_cast<const uint4*>(t.w) + l), w);
+  if (weighted && used) unpack8(at.load(t.w), w);
   if constexpr (ROT != kQkNone) {
-    qk_table<ROT>(p, it.row0, it.span(t), tab);
+    qk_table(p, it.row0, it.span(t), tab);
     __syncthreads();
   }
 #pragma unroll
@@ -206,7 +216,7 @@ __global__ void __launch_bounds__(kQkThreads, 5) kda_qk_forward_kernel(const __g
       }
     }
     qk_rotate<ROT, false>(p, tab + it.r[j] * (p.rot >> 1), l, f);
-    if (it.in[j]) *reinterpret_cast<uint4*>(yb + it.r[j] * t.y_ts + it.head[j] * p.D) = pack8(f);
+    if (it.in[j]) at.store(yb + it.r[j] * t.y_ts + it.head[j] * p.D, pack8(f));
   }
 }
 
@@ -220,24 +230,25 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackwardCtas) kda_qk_backward_k
   const QkTensor& t = p.t[which];
   const int grp = threadIdx.x >> LANES, l = threadIdx.x & ((1 << LANES) - 1);
   const bool used = l * 8 < p.D, weighted = t.w != nullptr;
+  const QkPlace<ROT> at(p, l);
   float w[8], dw[8] = {};
-  if (weighted && used) unpack8(__ldg(reinterpret_cast<const uint4*>(t.w) + l), w);
+  if (weighted && used) unpack8(at.load(t.w), w);
   for (int64_t tile = static_cast<int64_t>(blockIdx.x) - (which ? p.t[0].ctas : 0); tile < t.tiles; tile += t.ctas) {
     const QkTile<LANES, VPT> it(t, tile, grp, used);
-    const __nv_bfloat16* const xb = t.x + it.row0 * t.x_ts + l * 8;
-    const __nv_bfloat16* const db = t.dy + it.row0 * t.dy_ts + l * 8;
-    __nv_bfloat16* const yb = t.y + it.row0 * t.y_ts + l * 8;
+    const __nv_bfloat16* const xb = t.x + it.row0 * t.x_ts;
+    const __nv_bfloat16* const db = t.dy + it.row0 * t.dy_ts;
+    __nv_bfloat16* const yb = t.y + it.row0 * t.y_ts;
     uint4 x[VPT], dy[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       x[j] = dy[j] = make_uint4(0, 0, 0, 0);
       if (it.in[j]) {
-        if (p.norm) x[j] = *reinterpret_cast<const uint4*>(xb + it.r[j] * t.x_ts + it.head[j] * p.D);
-        dy[j] = *reinterpret_cast<const uint4*>(db + it.r[j] * t.dy_ts + it.head[j] * p.D);
+        if (p.norm) x[j] = at.load(xb + it.r[j] * t.x_ts + it.head[j] * p.D);
+        dy[j] = at.load(db + it.r[j] * t.dy_ts + it.head[j] * p.D);
       }
     }
     if constexpr (ROT != kQkNone) {
-      qk_table<ROT>(p, it.row0, it.span(t), tab);
+      qk_table(p, it.row0, it.span(t), tab);
       __syncthreads();
     }
 #pragma unroll
@@ -266,7 +277,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackwardCtas) kda_qk_backward_k
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = inv * fmaf(-f[e], sg, g[e]);
       }
-      if (it.in[j]) *reinterpret_cast<uint4*>(yb + it.r[j] * t.y_ts + it.head[j] * p.D) = pack8(g);
+      if (it.in[j]) at.store(yb + it.r[j] * t.y_ts + it.head[j] * p.D, pack8(g));
     }
     if constexpr (ROT != kQkNone) __syncthreads();  // the table is rewritten
   }
@@ -274,7 +285,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkBackwardCtas) kda_qk_backward_k
   float* const red = reinterpret_cast<float*>(tab);  // [groups][D]
   if (used) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[grp * p.D + l * 8 + e] = dw[e];
+    for (int e = 0; e < 8; ++e) red[grp * p.D + (e < 4 ? at.o0 + e : at.o1 + e - 4)] = dw[e];
   }
   __syncthreads();
   for (int d = threadIdx.x; d < p.D; d += kQkThreads) {
