@@ -31,7 +31,7 @@ namespace kdal {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkMaxCtas = 1024;  // of the backward pass: rows of its partial sums
-constexpr int kQkBackwardCtas = 3;  // an SM
+constexpr int kQkBackwardCtas = 4;  // an SM
 
 struct QkTensor {
   const __nv_bfloat16* x; int64_t x_ts;
