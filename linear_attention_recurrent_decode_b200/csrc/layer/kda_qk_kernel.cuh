@@ -6,20 +6,22 @@
 // Backward from dy: the rotation's transpose turns back, g; then with x^ = x i
 //   dw = sum over rows and heads of g x^,   dx = i (g w - x^ sum(g w x^) (/ D)).
 //
-// What bounds it: device memory, one read and one write of every element.  A
-// thread holds 8 components (16 bytes) of a head, the head's threads are a
-// power of two of neighbouring lanes (unused ones idle for D = 96), sums and
-// the halves' partners go by shuffles.  A tile is 256 threads' heads, VPT each,
-// of one tensor; its rows' cos and sin are computed once, in shared memory, and
-// shared by all heads, while the loads are in flight.
+// What bounds it: device memory, one read and one write of every element; next
+// the instructions, and of those the angles'.  A thread holds 8 components (16
+// bytes) of a head, the head's threads are a power of two of neighbouring lanes
+// (unused ones idle for D = 96), sums go by shuffles.  A tile is 256 threads'
+// heads, VPT each, of one tensor; its rows' cos and sin are computed once, in
+// shared memory, and shared by all heads, while the loads are in flight.
 //
-// Measured (B200, 16384 rows, D = 128): forward, 32 + 32 heads, 100 us, 5.3 TB/s
-// (0.81 of the measured copy rate), the instructions being the next bound (0.7
-// of the issue slots); four heads a thread and five blocks an SM against 115 us
-// for two heads.  Backward with weights, 32 + 8 heads, 140 us, 3.6 TB/s: two
-// heads a thread and three blocks an SM against 147 to 165 us for one, three or
-// four; loading the next tile ahead of computing one was slower (170 us, the
-// registers).
+// Measured (B200, 16384 rows, D = 128): forward, 32 + 32 heads rotated in
+// interleaved pairs, 98 us, 5.5 TB/s (0.83 of the measured copy rate); 32 + 8
+// heads with weights in halves 75 us (0.68; 0.86 of the issue slots), without
+// rotation 52 us (0.97).  Four heads a thread and five blocks an SM against 81,
+// 80 and 74 us (32 + 8 heads) for three, five and six heads.  Backward with
+// weights, 32 + 8 heads, 131 us, 3.8 TB/s, 0.72 of the issue slots; without
+// rotation 96.  Two heads a thread and four blocks an SM against 138 and 157 us
+// for three and five blocks; three heads are alike; loading the next tile ahead
+// of computing one, or its angles, was slower.
 #pragma once
 
 #include <cuda_bf16.h>
