@@ -101,8 +101,8 @@ _BF16, _F32 = torch.bfloat16, torch.float32
 
 
 def _device() -> int:
-    """The current device's index (-1 without CUDA: every tensor is then refused)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+    """The current device's index (-2 without CUDA, which no tensor's is: every one is then refused)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
 
 
 def _on_stream(call):
@@ -131,14 +131,17 @@ def _on_device(t, name, dev):
 def _row_stride(t, name, dtype, shape, lead, dev):
     """Row stride of a tensor of this shape whose rows (over the first ``lead`` dimensions) are evenly strided and
     dense inside."""
-    _on_device(t, name, dev)
+    if type(t) is not torch.Tensor or t.get_device() != dev:
+        _on_device(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
-        return math.prod(shape[lead:])
+        return shape[-1] if lead == len(shape) - 1 else shape[-1] * shape[-2]  # rows of one or two dimensions
     want, strides = 1, t.stride()
+    if lead == 1 and len(strides) == 3 and shape[0] > 1 and strides[2] == 1 and strides[1] == shape[2]:
+        return strides[0]  # columns of one packed buffer
     for d in range(len(shape) - 1, lead - 1, -1):
         if shape[d] > 1 and strides[d] != want:
             raise ValueError(f"{name}: each row must be contiguous")
@@ -163,7 +166,8 @@ def _empty(x, shape=None, dtype=None):
 
 
 def _state(t, name, blocks, HV, K, V, dev):
-    _on_device(t, name, dev)
+    if not (type(t) is torch.Tensor and t.get_device() == dev):
+        _on_device(t, name, dev)
     if t.dtype != _F32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 tensor")
     if t.dim() != 4 or t.shape[1:] != (HV, K, V) or (blocks is not None and t.shape[0] != blocks):
@@ -246,10 +250,10 @@ def kda_scan(q, k, v, g, beta, initial_state=None, *, cu_seqlens=None, slot_idx=
         a.slot_idx, a.num_slots = slot_idx.data_ptr(), blocks
         if final_state is None:
             final_state = initial_state
-    if final_state is None:
-        final_state = _empty(q, (N, HV, K, V), _F32)
     if initial_state is not None:
         a.initial_state = _state(initial_state, "initial_state", blocks, HV, K, V, dev)
+    if final_state is None:
+        final_state = _empty(q, (N, HV, K, V), _F32) if initial_state is None else _empty(initial_state)
     a.final_state = _state(final_state, "final_state", blocks, HV, K, V, dev)
     if out is None:
         out = _empty(v)
