@@ -41,6 +41,7 @@
 namespace kdal {
 
 constexpr int kGradThreads = 512;  // 256 left the schedulers short of warps: each phase waits on its own loads
+static_assert(kGradThreads == 512, "the count of the barrier ahead of dKe");
 constexpr int kGP = kK + 8;  // padded rows of the fp32 factors, read as [k][n] fragments
 constexpr int kDP = kC + 4;
 
@@ -305,15 +306,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  // ---- 2. The products on the tensor cores, one warp's: dP = dO r, dA = -dR r and, once S0 and dS1 are there,
-  // dQt = dO S0^T, dKt = -dR S0^T, dKe = r dS1^T (scales and signs come later).  The other warps work on the decay factors
-  // meanwhile.
+  // ---- 2. The products on the tensor cores, issued by two warps among the others' work on the decay factors: dP = dO r,
+  // dA = -dR r and, once S0 and dS1 are there, dQt = dO S0^T, dKt = -dR S0^T, dKe = r dS1^T (scales and signs come later).
   const float sc_do_inv = pow2_inv(sc_do), sc_dr_inv = pow2_inv(pow2_scale(__uint_as_float(sm.mx_dr)));
-  if (warp == 0) {
-    umma_tiles<kC, kV, kC, false, kV, true, true>(tmem + GradColumns::kDP, a_do, 0, a_r, Record::kPlane);
-    umma_tiles<kC, kV, kV, true, kV, true, false>(tmem + GradColumns::kDA, a_dr, Record::kPlane, a_r, Record::kPlane);
-    umma_commit(&sm.bar[3]);
-  }
   if (tid < tc) {
     float s = 0.f;
 #pragma unroll
@@ -332,6 +327,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       bulk_load(sm.s0, rec + Record::kS, kV * kK * 4, &sm.bar[1]);
       mbar_expect(&sm.bar[2], kV * kK * 4);
       bulk_load(sm.ds, rec + Record::kDS, kV * kK * 4, &sm.bar[2]);
+    }
+    if (warp == 0) {
+      umma_tiles<kC, kV, kC, false, kV, true, true>(tmem + GradColumns::kDP, a_do, 0, a_r, Record::kPlane);
+      umma_tiles<kC, kV, kV, true, kV, true, false>(tmem + GradColumns::kDA, a_dr, Record::kPlane, a_r, Record::kPlane);
+      umma_commit(&sm.bar[3]);
     }
     const SubFactors f = sub_factors(g, up, dn);
     if (f.exact) sm.exact[sub] = 1;
@@ -356,15 +356,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
   }
   fence_async();
   ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[1], 0)) && ok;
-  if (warp == 0) {
+  if (warp == 1) {
     umma_tiles<kK, kV, kC, false, kV, true, true>(tmem + GradColumns::kDQ, a_do, 0, a_s0, kV * kK * 2);
     umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKRow, a_dr, Record::kPlane, a_s0, kV * kK * 2);
   }
   ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar[2], 0)) && ok;
-  __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {  // r is complete when every warp is here; the others need not wait
+    asm volatile("bar.sync 1, 512;" ::: "memory");
     umma_tiles<kK, kV, kV, true, kV, true, false>(tmem + GradColumns::kDKCol, a_r, Record::kPlane, a_ds, kV * kK * 2);
     umma_commit(&sm.bar[4]);
+  } else {
+    asm volatile("bar.arrive 1, 512;" ::: "memory");
   }
   float e_sum = 0.f;
   {

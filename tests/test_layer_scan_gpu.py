@@ -418,6 +418,33 @@ def test_scan_streams_graphs_and_repeats(cuda_device):
     assert kda.scan_error(ws) == 0
 
 
+def test_scan_two_calls_at_once(cuda_device):
+    """A captured training step replayed on one stream beside an eager one on another, each with its workspace."""
+    def make(lens, H, seed):
+        x = inputs(lens, H, seed=seed)
+        ws = torch.zeros(kda.scan_workspace_bytes(sum(lens), len(lens), H, training=True), dtype=torch.uint8, device="cuda")
+        return x[:5], x[5], ws
+
+    def step(x, cu, ws):
+        out, final = kda.kda_scan(*x, cu_seqlens=cu, workspace=ws, save=True)
+        return [out, final, *kda.kda_scan_backward(out, *x, cu_seqlens=cu, workspace=ws, saved=True)]
+
+    a, b = make([700, 64, 1, 2000], 8, 21), make([333] * 30, 8, 22)
+    want_a, want_b = step(*a), step(*b)
+    torch.cuda.synchronize()
+    one, two, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got_a = step(*a)
+    for _ in range(5):
+        with torch.cuda.stream(one):
+            graph.replay()
+        with torch.cuda.stream(two):
+            got_b = step(*b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got_a + got_b, want_a + want_b))
+    assert kda.scan_error(a[2]) == kda.scan_error(b[2]) == 0
+
+
 def test_scan_workspace_contents_do_not_matter(cuda_device):
     q, k, v, g, beta, cu = inputs([100, 3], 2, seed=111)
     want = kda.kda_scan(q, k, v, g, beta, cu_seqlens=cu)
