@@ -27,12 +27,12 @@
 //
 // What bounds it, like the chunk preparation: the latency of its phases on one
 // block of 512 threads an SM (its operands fill the shared memory).  Of a chunk's
-// 47000 cycles the first loads take 7000, y and the factors 9000, the products
-// with the states and exp(Gamma_C) sum_v S0 dS1 8000, the pairs 18000 (tf32
+// 47000 cycles the first loads take 8000, y and the factors 10000, the products
+// with the states and exp(Gamma_C) sum_v S0 dS1 7000, the pairs 19000 (tf32
 // splits and MMAs, half of either's rate).  Measured (B200): 2112 chunks and
-// heads 409 us; a plain copy would move its bytes in 120.  Blocks that go on with
+// heads 403 us; a plain copy would move its bytes in 120.  Blocks that go on with
 // the next chunk and fetch its first operands under the decays' gradients, as the
-// preparation's do, were slower (430 us).
+// preparation's do, were 20 us slower.
 #pragma once
 
 #include "kda_scan_common.cuh"
