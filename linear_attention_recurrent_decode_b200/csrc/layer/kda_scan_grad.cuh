@@ -61,7 +61,7 @@ struct GradSmem {
   float dbeta[8][kC];
   float dp_own[kC];                          // dP_tt
   uint32_t mx_do, mx_dr;
-  int exact[kNB];
+  uint32_t exact[kNB][kK / 32];              // channels out of the factors' range, a bit each
   uint64_t bar[5];                           // dU, Y and r; S0; dS1; dP and dA; the other products
   uint32_t tmem;
 };
@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     mbar_fence_init();
     sm.mx_do = sm.mx_dr = 0;
   }
-  if (tid < kNB) sm.exact[tid] = 0;
   const ChunkPos pos = locate(p, slot);
   const int tc = pos.tc;
   wait_upstream();
@@ -334,7 +333,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
       umma_commit(&sm.bar[3]);
     }
     const SubFactors f = sub_factors(g, up, dn);
-    if (f.exact) sm.exact[sub] = 1;
+    const uint32_t out_of_range = __ballot_sync(0xffffffffu, f.exact);
+    if (lane == 0) sm.exact[sub][warp & 3] = out_of_range;
     sm.emu[sub][ch] = exp_of(f.mu);
     sm.emd[sub][ch] = exp_of(f.md);
     sm.eru[sub][ch] = exp_of(add(f.end, neg(f.mu)));
@@ -499,7 +499,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
         if (lane < 4) to[I][col + n * 8 + e] = x[n][e];
       }
   };
-  const bool exact = sm.exact[I] != 0;
+  // This thread's channels whose pairs inside the block have to be summed directly: bit 8 n + e; nearly always none.
+  const uint32_t exact_word = sm.exact[I][warp >> 2], exact = exact_word >> (2 * (lane & 3));
   {  // rows: earlier tokens
     for (int J = 0; J < I; ++J) {
       scale_cols(dq, &sm.emd[J][col]);
@@ -520,37 +521,46 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     __nv_bfloat162 qe[4][2], ke[4][2];
     fetch(p.q, p.q_ts, qe);
     fetch(p.k, p.k_ts, ke);
-    if (exact) {
+    row_block(I, xq, xk);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = pr.up[row + (e >> 1) * 8][col + n * 8 + (e & 1)];
+        dq[n][e] *= u;
+        dkr[n][e] *= u;
+        xq[n][e] *= u;
+        xk[n][e] *= u;
+      }
+    if (exact_word) {
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float3 d = grad_exact_element(p, pr, I, pos.tok, tc, h, row + (e >> 1) * 8, col + n * 8 + (e & 1));
-          xq[n][e] = d.x;
-          xk[n][e] = d.y;
-        }
-    } else {
-      row_block(I, xq, xk);
+        for (int e = 0; e < 4; ++e)
+          if ((exact >> (8 * n + (e & 1))) & 1) {
+            const float3 d = grad_exact_element(p, pr, I, pos.tok, tc, h, row + (e >> 1) * 8, col + n * 8 + (e & 1));
+            xq[n][e] = d.x;
+            xk[n][e] = d.y;
+          }
+      __syncwarp();
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float2& at = *reinterpret_cast<float2*>(&pr.up[row + hf * 8][col + n * 8]);  // this thread's own elements
         const float own = sm.dp_own[row + hf * 8];
-        const float2 u2 = at, q2 = __bfloat1622float2(qe[n][hf]), k2 = __bfloat1622float2(ke[n][hf]);
+        const float2 q2 = __bfloat1622float2(qe[n][hf]), k2 = __bfloat1622float2(ke[n][hf]);
         float2 y;
-        auto element = [&](int e, float u, float q, float k) {
-          const float ui = exact ? 1.f : u, bq = dq[n][e] * u, bk = dkr[n][e] * u, iq = xq[n][e] * ui, ik = xk[n][e] * ui;
-          const float before = fmaf(q, bq, k * bk);
+        auto element = [&](int e, float q, float k) {
+          const float before = fmaf(q, dq[n][e], k * dkr[n][e]), inside = fmaf(q, xq[n][e], k * xk[n][e]);
           sum[n][e & 1] += before;
-          dq[n][e] = fmaf(own, k, bq + iq);
-          dkr[n][e] = fmaf(own, q, bk + ik);
-          return before + fmaf(q, iq, k * ik);
+          dq[n][e] = fmaf(own, k, dq[n][e] + xq[n][e]);
+          dkr[n][e] = fmaf(own, q, dkr[n][e] + xk[n][e]);
+          return before + inside;
         };
-        y.x = element(2 * hf, u2.x, q2.x, k2.x);
-        y.y = element(2 * hf + 1, u2.y, q2.y, k2.y);
-        at = y;
+        y.x = element(2 * hf, q2.x, k2.x);
+        y.y = element(2 * hf + 1, q2.y, k2.y);
+        *reinterpret_cast<float2*>(&pr.up[row + hf * 8][col + n * 8]) = y;  // this thread's own elements
         put_out(p.dq, p.dq_ts, n, hf, dq[n][2 * hf], dq[n][2 * hf + 1]);
       }
     block_sum(sum, pr.rows);
@@ -568,37 +578,45 @@ __global__ void __launch_bounds__(kGradThreads, 1) kda_scan_grad_kernel(const __
     float x[4][4] = {}, ended[4][4], sum[4][2] = {};
     __nv_bfloat162 ke[4][2];
     fetch(p.k, p.k_ts, ke);
-    if (exact) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[n][e] = grad_exact_element(p, pr, I, pos.tok, tc, h, row + (e >> 1) * 8, col + n * 8 + (e & 1)).z;
-    } else {
-      column_block(I, x);
-    }
+    column_block(I, x);
     tmem_ld_tiles(mine + GradColumns::kDKCol + i0, ended);  // dKe
     const float inv_r = pow2_inv(sm.sc[Record::kScR]) * pow2_inv(sc_ds), b0 = beta[row] * inv_r, b1 = beta[row + 8] * inv_r;
 #pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float d = pr.dn[row + (e >> 1) * 8][col + n * 8 + (e & 1)], f = sm.dn[I][col + n * 8 + (e & 1)];
+        dkc[n][e] *= d;
+        x[n][e] *= d;
+        ended[n][e] *= (e >> 1 ? b1 : b0) * (f * d);
+      }
+    if (exact_word) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((exact >> (8 * n + (e & 1))) & 1)
+            x[n][e] = grad_exact_element(p, pr, I, pos.tok, tc, h, row + (e >> 1) * 8, col + n * 8 + (e & 1)).z;
+      __syncwarp();
+    }
+#pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const float2 fct = *reinterpret_cast<const float2*>(&sm.dn[I][col + n * 8]);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         float2& at = *reinterpret_cast<float2*>(&pr.up[row + hf * 8][col + n * 8]);
-        float2& end = *reinterpret_cast<float2*>(&pr.dn[row + hf * 8][col + n * 8]);
-        const float2 d2 = end, k2 = __bfloat1622float2(ke[n][hf]);
+        const float2 k2 = __bfloat1622float2(ke[n][hf]);
         float2 y = at, z;
-        auto element = [&](int e, float d, float k, float f, float& inside) {
-          const float di = exact ? 1.f : d, last = ended[n][e] * (hf ? b1 : b0) * (f * d), bc = dkc[n][e] * d, ic = x[n][e] * di;
-          const float behind = k * bc;
+        auto element = [&](int e, float k, float& inside) {
+          const float behind = k * dkc[n][e];
           sum[n][e & 1] += behind;
-          inside = fmaf(-k, ic, inside);
-          dkr[n][e] += (bc + ic) + last;  // dk
-          return fmaf(k, last, behind);
+          inside = fmaf(-k, x[n][e], inside);
+          dkr[n][e] += (dkc[n][e] + x[n][e]) + ended[n][e];  // dk
+          return fmaf(k, ended[n][e], behind);
         };
-        z.x = element(2 * hf, d2.x, k2.x, fct.x, y.x);
-        z.y = element(2 * hf + 1, d2.y, k2.y, fct.y, y.y);
+        z.x = element(2 * hf, k2.x, y.x);
+        z.y = element(2 * hf + 1, k2.y, y.y);
         at = y;
-        end = z;
+        *reinterpret_cast<float2*>(&pr.dn[row + hf * 8][col + n * 8]) = z;
         put_out(p.dk, p.dk_ts, n, hf, dkr[n][2 * hf], dkr[n][2 * hf + 1]);
       }
     }
