@@ -106,8 +106,10 @@ __device__ __forceinline__ void store_out16(__nv_bfloat16* out, int64_t ts, int 
   }
 }
 
-// Direct sums inside sub-block b (its decays are out of the factors' range):
-// one accumulator element (t, i), pairs from the log-decays between them.
+// Direct sums inside sub-block b for a channel i whose decays are out of the
+// factors' range: one accumulator element (t, i), pairs from the log-decays
+// between them.  Only such channels' elements: for all of a sub-block with one,
+// the gradients took three times as long.
 __device__ __noinline__ float3 grad_exact_element(const ScanParams& p, const GradPairs& f, int b, int64_t tok, int tc, int64_t h,
                                                   int t, int i) {
   if (t >= tc) return make_float3(0.f, 0.f, 0.f);
