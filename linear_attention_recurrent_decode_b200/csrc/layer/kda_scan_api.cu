@@ -47,7 +47,7 @@ bool chunk_slots(int64_t N, int64_t T, bool packed, int64_t* slots) {
 // the segments save); as long as the first of the two walks, two blocks a segment, then fills the SMs once, and at least
 // 8 chunks.  Measured when they were added, us a call: 8192 tokens of 8 heads 590 without and 317 with segments, with
 // gradients 1618 and 799.
-constexpr int64_t kSms = 148;
+constexpr int64_t kSms = ks::kSms;
 bool segments(int64_t N, int64_t T, bool packed, int64_t HV, int32_t* seg_chunks, int64_t* slots) {
   const int64_t total = packed ? T / ks::kC : (T + ks::kC - 1) / ks::kC;  // the longest sequence's chunks at most
   *seg_chunks = 0;

@@ -39,10 +39,12 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
 // before its first access of global memory; the others touch what earlier
 // kernels wrote, or write anything, only behind their wait.  Every block waits
 // before it ends: a kernel that is complete has everything before it complete.
-// No kernel lets the next one start earlier (griddepcontrol.launch_dependents):
-// that measured up to 6 % slower for long calls, as the next kernel's blocks then
-// take the SMs that the running one's last blocks are given.
+// Kernels whose grids leave SMs idle may let the next one start earlier; for long
+// calls that measured up to 6 % slower, as the next kernel's blocks then take the
+// SMs that the running one's last blocks are given.
+constexpr uint32_t kSms = 148;
 __device__ __forceinline__ void wait_upstream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- scales
 // The power of two that puts a tile whose largest magnitude is `m` in
