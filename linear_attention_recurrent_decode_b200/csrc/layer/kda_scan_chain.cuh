@@ -296,10 +296,14 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_scan_forward_kernel(cons
   if (warp < kComputeWarps) {
     const int part = warp >> 2;
     float s[kPartK];
-    // a segment's start: the first's is the call's, the others' the end of the one before (zero for their E)
-    const float* const from = seg.seg == 0 ? (p.s_in == nullptr ? nullptr : p.s_in + sblk)
-                                           : (p.transitions ? nullptr : p.seg_state + gblk - p.HV * kK * kV);
+    // A segment's start: the first's is the call's, the others' the end of the one before (zero for their E).  The walk for
+    // E copies the call's to the first segment's block of seg_map, which has no M, and the walk for the results starts
+    // from that copy: s_out may be s_in, and the block of the last segment stores there whenever it is done.
+    const float* const call = p.s_in == nullptr ? nullptr : p.s_in + sblk;
+    const float* const from = seg.seg > 0 ? (p.transitions ? nullptr : p.seg_state + gblk - p.HV * kK * kV)
+                                          : (call == nullptr || p.transitions || seg.segs == 1 ? call : p.seg_map + gblk);
     load_state(from, v, part, s);
+    if (p.transitions && from != nullptr) store_state(p.seg_map + gblk, v, part, s);
     if (map) {
 #pragma unroll
       for (int j = 0; j < kPartK; ++j) s[j] = part * kPartK + j == v ? 1.f : 0.f;

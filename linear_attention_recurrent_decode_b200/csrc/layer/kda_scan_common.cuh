@@ -28,7 +28,7 @@ struct ScanParams {
   int32_t seg_chunks, seq_segs;  // chunks of a segment; segments of a sequence of the dense form
   int32_t transitions;      // the chain call computes the segments' transitions instead of the results
   float* seg_state;         // [segment slots, HV, K, V] states at the segments' ends (or starts, backwards)
-  float* seg_map;           // [segment slots, HV, K, K] transition matrices
+  float* seg_map;           // [segment slots, HV, K, K] transition matrices; a first segment's: the state it starts from
   // backward
   const __nv_bfloat16* d_out; int64_t d_out_ts;
   const float* d_final;     // [N, HV, K, V] or null

@@ -199,6 +199,27 @@ def test_scan_slots_of_long_sequences(cuda_device):
     check_scan(out.view(2 * T, 1, V), final, q, k, v, g, beta, state, cu.tolist(), K ** -0.5)
 
 
+def test_scan_long_sequences_in_place(cuda_device):
+    """The last segment of a sequence, here of one token, stores the final state while the first may not have started: the
+    walk of the results takes the initial state from a copy in the workspace, made by the kernel before."""
+    H, T = 3, 64 * 24 + 1
+    q, k, v, g, beta, cu = inputs([T], H, "mild", seed=34)
+    start, pool = states(1, H, 8), states(3, H, 9)
+    want, wfinal = kda.kda_scan(q, k, v, g, beta, start, cu_seqlens=cu)
+    check_scan(want, wfinal, q, k, v, g, beta, start, cu.tolist(), K ** -0.5)
+    pool[2] = start[0]
+    ws = torch.zeros(kda.scan_workspace_bytes(T, 1, H), dtype=torch.uint8, device=cuda_device)
+    slots = torch.tensor([2], dtype=torch.int32, device=cuda_device)
+    out, _ = kda.kda_scan(q, k, v, g, beta, pool, cu_seqlens=cu, slot_idx=slots, workspace=ws)
+    assert torch.equal(out, want) and torch.equal(pool[2], wfinal[0])
+    blocks = ws[ws.numel() % (K * V * 4):].view(torch.float32).view(-1, K, V)  # the segments' states lie at the end
+    for h in range(H):
+        assert bool((blocks == start[0, h]).all(-1).all(-1).any()), f"no copy of head {h}'s start"
+    state = start.clone()
+    out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu, final_state=state)
+    assert final is state and torch.equal(out, want) and torch.equal(state, wfinal)
+
+
 def test_scan_many_sequences(cuda_device):
     """More sequences than one, and than two, steps of the search for a chunk's sequence, of 0 to 3 tokens but for a long
     one, some without any at both ends."""
