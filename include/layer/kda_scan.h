@@ -26,10 +26,10 @@
  * sequences concerned are then undefined.
  *
  * Layouts.  q, k bf16 [rows, HV, K]; v, out bf16 [rows, HV, V]; g fp32
- * [rows, HV, K] (log-decay, normally <= 0; growing decays are computed as long
- * as a chunk's growth stays in fp32's range); beta fp32 [rows, HV].  Every one
- * has a row stride in elements (>= the row's width), heads dense inside a row:
- * q, k and v may be slices of one packed row buffer, and so may the gradients.
+ * [rows, HV, K] (log-decay, normally <= 0; growing ones: see Accuracy); beta
+ * fp32 [rows, HV].  Every one has a row stride in elements (>= the row's width),
+ * heads dense inside a row: q, k and v may be slices of one packed row buffer,
+ * and so may the gradients.
  * States fp32 [N, HV, K, V], dense.  With slot_idx (device int32 [N],
  * kda_scan only) sequence n's state is block slot_idx[n] of [num_slots, HV, K,
  * V] pools instead; a slot < 0 or >= num_slots makes the sequence inactive
@@ -41,12 +41,27 @@
  * d_out, dq, dk, dv 16 bytes with strides that are multiples of 8 elements;
  * workspace and states 16 bytes; g, beta, dg, dbeta, cu_seqlens, slot_idx 4.
  *
- * Accuracy.  States, sums and every fp32 result are computed to fp32 accuracy
- * (operands as fp16 or tf32 pairs of 22 bits, fp32 accumulation, decays
- * accumulated in pairs of fp32); bf16 results are rounded once.  An infinity or NaN in a
- * sequence's inputs makes that sequence's and head's results undefined from
- * its chunk (64 tokens) on, nothing else; but a log-decay of -inf, like any
- * below -1e4, is a decay of zero.
+ * Accuracy.  Operands are pairs of fp16 or tf32 numbers (22 bits) with one
+ * power-of-two scale for a chunk (64 tokens) and head, accumulated in fp32, with
+ * decays accumulated in pairs of fp32; bf16 results are rounded once.  A value
+ * keeps 2^-22 of itself or 2^-39 of the largest one under its scale, whichever
+ * is more, so fp32 results are as exact as fp32 relative to the largest of their
+ * chunk and head.  Apart from it:
+ *   - tokens, or value columns of the same 32, more than 2^17 below that
+ *     largest lose bits;
+ *   - in dq, dk, dg and dbeta, which sum over the value columns, so does what
+ *     columns of initial states or values more than 2^9 below the largest add;
+ *   - growth (g > 0) is a spread of magnitudes within its chunk: up to 2^16 over
+ *     64 tokens keeps every token's own accuracy, more takes it from those that
+ *     are left behind.
+ * Range: values, states, gradients and what decays make of them, chunk by chunk,
+ * with largest magnitudes of 0 or 2^-80 to 2^100, and products of two (a state
+ * and its gradient) inside fp32's.  Below, bits and then values are lost; above
+ * lie infinities and NaN.
+ * An infinity or NaN in a sequence's inputs makes that sequence's and head's
+ * outputs and final state undefined from its chunk on, and all gradients of that
+ * sequence and head, nothing else; but a log-decay of -inf, like any below -1e4,
+ * is a decay of zero.
  *
  * Workspace.  Caller-owned device memory of kda_scan_workspace_bytes bytes; the
  * library allocates nothing.  With save = 1 (and a workspace sized for

@@ -48,14 +48,17 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 
 // ---------------------------------------------------------------- scales
 // The power of two that puts a tile whose largest magnitude is `m` in
-// [2^13, 2^14), kept within 2^+-50 so that products of two scales times any
-// state stay inside fp32; 1 for a zero, infinite or NaN maximum (the values
-// then carry themselves).
+// [2^13, 2^14), kept within 2^+-100: magnitudes from 2^-86 (below, pairs lose
+// bits) to 2^115 (above, they overflow), and a scale times a factor that goes
+// before it, or the inverse of one times a product's accumulator (up to 2^35),
+// stays inside fp32.  Two inverses may be multiplied first: that leaves fp32's
+// range only where the product itself does.  1 for a zero, infinite or NaN
+// maximum (the values then carry themselves).
 __device__ __forceinline__ float pow2_scale(float m) {
   const int e = static_cast<int>(__float_as_uint(m) >> 23) & 0xff;  // m >= 0
   if (e == 0 || e == 255) return 1.f;
   int s = 13 - (e - 127);
-  s = s > 50 ? 50 : (s < -50 ? -50 : s);
+  s = s > 100 ? 100 : (s < -100 ? -100 : s);
   return __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
 }
 // The inverse of a power of two.

@@ -362,6 +362,67 @@ def test_scan_decay_gradients_normwise(decay, cuda_device):
         assert float((got[a:b].double() - want[a:b]).norm() / want[a:b].norm()) <= ref.DG_NORM
 
 
+@pytest.mark.parametrize("magnitude", [2.0 ** -80, 2.0 ** -60, 2.0 ** -45, 2.0 ** 45, 2.0 ** 70, 2.0 ** 95])
+def test_scan_far_magnitudes(magnitude, cuda_device):
+    """Near both ends of the documented range, 2^-80 to 2^100; the largest of these values and states is near 2^3."""
+    q, k, v, g, beta, cu = inputs([150], 2, "mild", seed=13)
+    v, state = v * magnitude, states(1, 2, 6) * magnitude
+    out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu)
+    check_scan(out, final, q, k, v, g, beta, state, cu.tolist(), K ** -0.5)
+
+
+@pytest.mark.parametrize("mv,md", [(1.0, 2.0 ** -80), (1.0, 2.0 ** 90), (2.0 ** -70, 2.0 ** 90), (2.0 ** 90, 2.0 ** -70), (2.0 ** -45, 2.0 ** -30)])
+def test_scan_gradients_far_magnitudes(mv, md, cuda_device):
+    """A power of two on the values or on the gradients changes nothing but the results' exponents, other than where fp32
+    ends at 2^-149, which is less than 2^-36 of these results' largest."""
+    q, k, v, g, beta, cu = inputs([150, 30], 2, "mild", seed=14)
+    state, d_final = states(2, 2, 6), states(2, 2, 7)
+    d_out = torch.randn(180, 2, V, device=cuda_device, generator=torch.Generator(device=cuda_device).manual_seed(4)).bfloat16()
+    want = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)
+    check_gradients(want, ref.scan_gradients(q, k, v, g, beta, state, cu.tolist(), K ** -0.5, d_out, d_final)[2:], cu.tolist(), q, k,
+                    d_out, d_final)
+    got = kda.kda_scan_backward(d_out * md, q, k, v * mv, g, beta, state * mv, d_final_state=d_final * md, cu_seqlens=cu)
+    for name, a, b in zip(GRADS, got, want):
+        m = md if name in ("dv", "dstate") else mv * md
+        ref.check(a, b.double() * m, ref.FLOOR, name, ref.BF16_HALF_STEP if name in ("dq", "dk", "dv") else 0.0)
+
+
+def test_scan_columns_of_different_magnitude(cuda_device):
+    """Value columns from 1 down to 2^-16 under one scale (32 columns share one): a pair's 2^-39 of the largest is still
+    within 2^-23 of the smallest column's own, so each column is held to its own magnitude; and its gradients likewise."""
+    q, k, v, g, beta, cu = inputs([150, 30], 2, "mild", seed=15)
+    size = torch.exp2(-16.0 * (torch.arange(V, device=cuda_device) % 32) / 31).bfloat16()
+    v, state, d_final = v * size, states(2, 2, 6) * size, states(2, 2, 7) * size
+    d_out = torch.randn(180, 2, V, device=cuda_device, generator=torch.Generator(device=cuda_device).manual_seed(5)).bfloat16() * size
+    c = cu.tolist()
+    out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu)
+    grads = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)
+    want = ref.scan_gradients(q, k, v, g, beta, state, c, K ** -0.5, d_out, d_final)
+    for i in range(V):
+        ref.check(out[..., i], want[0][..., i], ref.SCAN_REL, f"out, column {i}", ref.BF16_HALF_STEP)
+        ref.check(final[..., i], want[1][..., i], ref.SCAN_REL, f"state, column {i}")
+        ref.check(grads[2][..., i], want[4][..., i], ref.SCAN_REL, f"dv, column {i}", ref.BF16_HALF_STEP)
+        ref.check(grads[5][..., i], want[7][..., i], ref.SCAN_REL, f"dstate, column {i}")
+    check_gradients(grads, want[2:], c, q, k, d_out, d_final)
+
+
+def test_scan_growth_over_a_chunk(cuda_device):
+    """Decays that grow, by the documented 2^16 over a chunk of 64 tokens, then fall: a token's operands are up to 2^16 below
+    the chunk's largest, whose 2^-39 is 2^-23 of theirs, so each token's outputs are held to their own magnitude."""
+    q, k, v, g, beta, cu = inputs([128], 2, seed=16)
+    g[:64], g[64:] = 0.173, -0.173  # 64 of them: 2^15.97
+    state = states(1, 2, 6)
+    out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu)
+    d_out, d_final = torch.ones_like(v), states(1, 2, 7)
+    want = ref.scan_gradients(q, k, v, g, beta, state, cu.tolist(), K ** -0.5, d_out, d_final)
+    for t in range(128):
+        for h in range(2):
+            ref.check(out[t, h], want[0][t, h], ref.SCAN_REL, f"out of token {t}, head {h}", ref.BF16_HALF_STEP)
+    ref.check(final, want[1], ref.SCAN_REL, "state")
+    got = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)
+    check_gradients(got, want[2:], cu.tolist(), q, k, d_out, d_final)
+
+
 def test_scan_gradients_against_differences(cuda_device):
     """The directional derivative of the 64-bit loss, by central differences, against the kernel's gradients."""
     q, k, v, g, beta, cu = inputs([90, 40], 2, seed=81)
