@@ -45,8 +45,9 @@ bool chunk_slots(int64_t N, int64_t T, bool packed, int64_t* slots) {
 // Chunks of a segment, 0 for none, and the segment slots of the call.  Segments are for calls whose sequences and heads
 // leave half the SMs idle or more, with room for a sequence of 24 chunks (below, walking it twice and joining cost what
 // the segments save); as long as the first of the two walks, two blocks a segment, then fills the SMs once, and at least
-// 8 chunks.  Measured when they were added, us a call: 8192 tokens of 8 heads 590 without and 317 with segments, with
-// gradients 1618 and 799.
+// 8 chunks.  Where the longest sequence is not much longer than one, all are walked whole (worth_segments): a packed
+// call's lengths are on the device, so it may launch the walk for the segments' ends and the join for none, 8 us.
+// Measured, us a call: 8192 tokens of 8 heads 635 without and 269 with segments, with gradients 1753 and 674.
 constexpr int64_t kSms = ks::kSms;
 bool segments(int64_t N, int64_t T, bool packed, int64_t HV, int32_t* seg_chunks, int64_t* slots) {
   const int64_t total = packed ? T / ks::kC : (T + ks::kC - 1) / ks::kC;  // the longest sequence's chunks at most
@@ -54,11 +55,12 @@ bool segments(int64_t N, int64_t T, bool packed, int64_t HV, int32_t* seg_chunks
   *slots = N;
   int64_t units;
   if (!mul_ok(N, HV, &units)) return false;
-  if (units * 2 >= kSms || total < 24) return true;
+  if (units > ks::kMostCut || total < 24) return true;
   const int64_t all = (packed ? total : total * N) * HV;
   int64_t len = (2 * all + kSms - 1) / kSms;
   len = len < 8 ? 8 : len;
   if (len > 0x7fffffff) return false;
+  if (!ks::worth_segments(total, len)) return true;
   *seg_chunks = static_cast<int32_t>(len);
   *slots = packed ? total / len + N : N * ((total + len - 1) / len);
   return true;

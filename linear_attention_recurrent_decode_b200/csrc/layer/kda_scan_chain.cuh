@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_scan_forward_kernel(cons
     const float* const call = p.s_in == nullptr ? nullptr : p.s_in + sblk;
     const float* const from = seg.seg > 0 ? (p.transitions ? nullptr : p.seg_state + gblk - p.HV * kK * kV)
                                           : (call == nullptr || p.transitions || seg.segs == 1 ? call : p.seg_map + gblk);
+    float* const to = p.transitions ? (map ? p.seg_map : p.seg_state) + gblk : (last && p.s_out != nullptr ? p.s_out + sblk : nullptr);
     load_state(from, v, part, s);
     if (p.transitions && from != nullptr) store_state(p.seg_map + gblk, v, part, s);
     if (map) {
@@ -311,11 +312,15 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_scan_forward_kernel(cons
     // O = scale (Qt S0 + P U) of a chunk, its factors kept from there: this thread's value column and tokens; neighbours
     // trade a token each, so that a thread stores two values.
     float out_f1 = 0.f, out_f2 = 0.f;
-    auto put_outputs = [&](int64_t c) {
+    int64_t left = len - part * kPartT - (lane & 1);
+    __nv_bfloat16* out_at = p.out + (start + part * kPartT + (lane & 1)) * p.out_ts + h * kV + (v & ~1);
+    auto put_outputs = [&](int64_t c) {  // of each chunk in turn
       w.warp(&sm.out_done, c);
       fence_after_sync();
-      const int rows = static_cast<int>(len - c * kC < kC ? len - c * kC : kC) - part * kPartT - (lane & 1);
-      __nv_bfloat16* out = p.out + (start + c * kC + part * kPartT + (lane & 1)) * p.out_ts + h * kV + (v & ~1);
+      const int rows = static_cast<int>(left < kC ? left : kC);
+      left -= kC;
+      __nv_bfloat16* out = out_at;
+      out_at += kC * p.out_ts;
       uint32_t a[kPartT], x[kPartT];
       tmem_ld(mine + Col::kO1 + part * kPartT, a);
       tmem_ld(mine + Col::kO2 + part * kPartT, x);
@@ -397,10 +402,8 @@ __global__ void __launch_bounds__(kChainThreads, 1) kda_scan_forward_kernel(cons
     if (outputs && chunks > 0) put_outputs(chunks - 1);
     if (!w.ok) {
       if (lane == 0) set_error(p);
-    } else if (p.transitions) {
-      store_state((map ? p.seg_map : p.seg_state) + gblk, v, part, s);
-    } else if (last && p.s_out != nullptr) {
-      store_state(p.s_out + sblk, v, part, s);
+    } else if (to != nullptr) {
+      store_state(to, v, part, s);
     }
   } else if (warp == kComputeWarps) {
     if (lane == 0) chain_copies<true>(sm, w, rec, step, chunks, outputs);

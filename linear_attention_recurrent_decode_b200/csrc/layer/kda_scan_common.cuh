@@ -154,6 +154,13 @@ __device__ __forceinline__ ChunkPos locate(const ScanParams& p, int64_t slot) {
   return c;
 }
 
+// Whether a call whose longest sequence has that many chunks walks its sequences in segments of `len`: two walks of a
+// segment (the one for the segments' ends has no outputs, 3.7 us a chunk for 4.7) and joining have to be less than one
+// walk of the longest.  Measured, one sequence, us a call whole and in segments, where it is x times a segment: 8192
+// tokens x = 2.3 991, 898; 1.8 1108, 1097; 1.5 1219, 1314; 2048 tokens x = 2.3 264, 259; 1.8 299, 308 (782, 764 with
+// gradients); 1.5 331, 364.
+__host__ __device__ __forceinline__ bool worth_segments(int64_t chunks, int64_t len) { return 4 * chunks >= 7 * len; }
+
 // A CTA's part of a sequence: `chunks` chunks from `first` on, segment `seg` of `segs`.  The segment slots of sequence n
 // start at cu[n] / (C seg_chunks) + n, like the chunk slots.
 struct Segment {
@@ -161,8 +168,47 @@ struct Segment {
   int64_t first, chunks;
   int64_t seg, segs;        // segs 0: no such segment
 };
+// A packed call's sequence of a segment slot, the last one whose first segment slot is not behind it (or -1), its range, and
+// whether the call's sequences are cut at all.  A call with segments has at most kMostCut sequences: the lanes of a warp
+// load them all at once (whole warps call it; not inlined, it takes registers from the chains).
+constexpr int32_t kMostCut = (kSms - 1) / 2;
+struct PackedSegment {
+  int32_t n, start, len, cut;
+};
+__device__ __noinline__ PackedSegment find_segment(const int32_t* cu, int32_t N, int64_t tokens, int32_t seg_chunks, int64_t slot) {
+  constexpr int32_t kEach = kMostCut / 32 + 1;
+  const int32_t rows = static_cast<int32_t>(tokens), lane = threadIdx.x & 31;
+  int32_t a[kEach], l[kEach], longest = 0;
+#pragma unroll
+  for (int32_t j = 0; j < kEach; ++j) {
+    a[j] = l[j] = 0;
+    if (lane + 32 * j < N) a[j] = __ldg(cu + lane + 32 * j), l[j] = __ldg(cu + lane + 32 * j + 1);
+  }
+  const int64_t rows_of_segment = static_cast<int64_t>(kC) * seg_chunks;
+  PackedSegment s{-1, 0, 0, 0};
+#pragma unroll
+  for (int32_t j = 0; j < kEach; ++j) {
+    if (32 * j >= N) break;
+    a[j] = a[j] < 0 ? 0 : (a[j] > rows ? rows : a[j]);  // as in seq_range
+    l[j] = (l[j] > rows ? rows : (l[j] < a[j] ? a[j] : l[j])) - a[j];
+    longest = l[j] > longest ? l[j] : longest;
+    const uint32_t found = __ballot_sync(0xffffffffu, lane + 32 * j < N && a[j] < (slot - (lane + 32 * j) + 1) * rows_of_segment);
+    if (found) {
+      const int at = 31 - __clz(static_cast<int>(found));
+      s.n = 32 * j + at;
+      s.start = __shfl_sync(0xffffffffu, a[j], at);
+      s.len = __shfl_sync(0xffffffffu, l[j], at);
+    }
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  s.cut = worth_segments((static_cast<int64_t>(longest) + kC - 1) / kC, seg_chunks);
+  return s;
+}
 __device__ __forceinline__ int64_t first_segment(const ScanParams& p, int64_t n, int64_t start) {
   return p.cu == nullptr ? n * p.seq_segs : start / (static_cast<int64_t>(kC) * p.seg_chunks) + n;
+}
+__device__ __forceinline__ int64_t segments_of(const ScanParams& p, int64_t chunks, bool cut) {
+  return cut && chunks > 0 ? (chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
 }
 // The segment of a slot (whole warps call it).
 __device__ __forceinline__ Segment locate_segment(const ScanParams& p, int64_t slot) {
@@ -174,18 +220,21 @@ __device__ __forceinline__ Segment locate_segment(const ScanParams& p, int64_t s
     s.chunks = (s.len + kC - 1) / kC;
     return s;
   }
+  bool cut = true;
   if (p.cu == nullptr) {
     s.n = slot / p.seq_segs;
     seq_range(p, s.n, s.start, s.len);
   } else {
-    s.n = find_sequence(p, slot, s.start, s.len, [&](int64_t n, int64_t a) { return first_segment(p, n, a); });
-    if (s.n < 0) return Segment{};
+    const PackedSegment f = find_segment(p.cu, p.N, p.tokens, p.seg_chunks, slot);
+    if (f.n < 0) return Segment{};
+    s.n = f.n, s.start = f.start, s.len = f.len;
+    cut = f.cut;
   }
   const int64_t chunks = (s.len + kC - 1) / kC;
-  s.segs = chunks == 0 ? 1 : (chunks + p.seg_chunks - 1) / p.seg_chunks;
+  s.segs = segments_of(p, chunks, cut);
   s.seg = slot - first_segment(p, s.n, s.start);
   s.first = s.seg * p.seg_chunks;
-  s.chunks = chunks - s.first < p.seg_chunks ? chunks - s.first : p.seg_chunks;
+  s.chunks = s.seg < s.segs - 1 ? p.seg_chunks : chunks - s.first;
   if (s.seg >= s.segs) s.segs = 0;
   return s;
 }

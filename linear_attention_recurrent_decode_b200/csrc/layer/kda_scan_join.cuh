@@ -31,7 +31,8 @@ __global__ void __launch_bounds__(kJoinThreads, 1) kda_scan_join_kernel(const __
   const int warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   int64_t start, len;
   seq_range(p, n, start, len);
-  const int64_t chunks = (len + kC - 1) / kC, segs = (chunks + p.seg_chunks - 1) / p.seg_chunks;
+  const bool cut = p.cu == nullptr || find_segment(p.cu, p.N, p.tokens, p.seg_chunks, 0).cut;
+  const int64_t segs = segments_of(p, (len + kC - 1) / kC, cut);
   wait_upstream();
   if (gridDim.x <= kSms) launch_dependents();  // 1 us of 268 for one sequence of 8192 tokens, 8 heads
   if (segs < 3 || state_block(p, n) < 0) return;

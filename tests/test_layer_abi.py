@@ -73,6 +73,18 @@ def test_workspace_sizes(lib):
     assert g(0) == g(7) == g(12) == g(264) == -1
 
 
+def test_workspace_holds_segments_only_where_they_help(lib):
+    """One sequence of 8192 tokens: cut into segments up to 40 heads; with 48, two walks of them would take longer."""
+    f = lib.kda_scan_workspace_bytes
+    for training in (0, 1):
+        record = f(1, 64, 0, 1, 128, 128, training) - 256
+        for heads, cut in ((8, True), (32, True), (40, True), (48, False), (64, False), (72, False), (80, False)):
+            for packed in (0, 1):
+                records = 256 + (128 + packed) * heads * record
+                assert (f(1, 8192, packed, heads, 128, 128, training) > records) == cut, heads
+                assert f(1, 8192, packed, heads, 128, 128, training) >= records
+
+
 # ------------------------------------------------------------------------------------------------------ C refusals
 BASE = 1 << 32  # fake device addresses, far apart; nothing is dereferenced on the host
 

@@ -68,6 +68,7 @@ LENGTHS = [
 ]
 # walked in segments of 8 chunks: one to five of them, the last from one token to full
 LONG = [([64 * 24], 2), ([1600], 1), ([64 * 16 + 1, 0, 500, 64 * 8], 2), ([2100, 1, 70], 1)]
+LONG += [([64 * 13, 64 * 13 + 1, 3, 64 * 9 + 5, 64 * 14], 2)]  # cut as the longest has 14 chunks
 
 
 @pytest.mark.parametrize("lens,H", LENGTHS + LONG)
@@ -218,6 +219,18 @@ def test_scan_long_sequences_in_place(cuda_device):
     state = start.clone()
     out, final = kda.kda_scan(q, k, v, g, beta, state, cu_seqlens=cu, final_state=state)
     assert final is state and torch.equal(out, want) and torch.equal(state, wfinal)
+
+
+def test_scan_sequences_that_are_not_cut(cuda_device):
+    """Sequences of 13 chunks where segments have 8 would be walked for longer in segments: nothing is written where the
+    segments' states would be."""
+    H, lens = 2, [64 * 13] * 2
+    q, k, v, g, beta, cu = inputs(lens, H, "mild", seed=35)
+    ws = torch.zeros(kda.scan_workspace_bytes(sum(lens), 2, H), dtype=torch.uint8, device=cuda_device)
+    out, final = kda.kda_scan(q, k, v, g, beta, cu_seqlens=cu, workspace=ws)
+    check_scan(out, final, q, k, v, g, beta, torch.zeros_like(final), cu.tolist(), K ** -0.5)
+    slots = 26 // 8 + 2  # of segments
+    assert not bool(ws[-2 * slots * H * K * V * 4:].any())
 
 
 def test_scan_many_sequences(cuda_device):
