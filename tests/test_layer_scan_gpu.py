@@ -457,6 +457,36 @@ def test_scan_gradients_against_differences(cuda_device):
     assert abs(numeric - analytic) <= bound + 1e-3
 
 
+@pytest.mark.parametrize("which", range(6), ids=GRADS)
+def test_scan_each_gradient_against_differences(which, cuda_device):
+    """The derivative of the 64-bit loss along one input at a time, by central differences, so that no gradient hides behind
+    a larger one's rounding."""
+    q, k, v, g, beta, cu = inputs([90, 40], 2, seed=82)
+    gen = torch.Generator(device=cuda_device).manual_seed(83 + which)
+    c, state, d_final = cu.tolist(), states(2, 2, 8), states(2, 2, 9)
+    d_out = torch.randn(130, 2, V, device=cuda_device, generator=gen).bfloat16()
+    grad = kda.kda_scan_backward(d_out, q, k, v, g, beta, state, d_final_state=d_final, cu_seqlens=cu)[which].double()
+    x = double(q, k, v, g, beta, state)
+    way = torch.randn(x[which].shape, device=cuda_device, generator=gen, dtype=torch.float64)
+    # along the gradient's signs: the terms add up instead of cancelling
+    way = way.abs() * torch.where(grad < 0, -1.0, 1.0)
+
+    def loss(eps):
+        y = list(x)
+        y[which] = y[which] + eps * way
+        out, final = ref.scan(*y, c, K ** -0.5)
+        return float((out * d_out.double()).sum() + (final * d_final.double()).sum())
+
+    eps = 1e-6
+    numeric, terms = (loss(eps) - loss(-eps)) / (2 * eps), float((grad * way).sum())
+    # Per element: half a step where the gradient is bf16, and the tolerance of its largest.  The differences' own error is
+    # the loss's 2^-53 / eps, with a loss below 2^12 5e-7 of 1, and eps^2 of the third derivative.
+    rel = ref.DG_REL if which == 3 else ref.SCAN_REL
+    bound = (ref.BF16_HALF_STEP * terms if which < 3 else 0.0) + 2 * rel * float(grad.abs().max() * way.abs().sum()) + 1e-4
+    assert abs(numeric - terms) <= bound
+    assert bound <= 0.05 * terms, "the bound would not see a gradient of zero"
+
+
 def test_scan_dense_gradients_equal_packed(cuda_device):
     N, T, H = 2, 100, 2
     q, k, v, g, beta, cu = inputs([T] * N, H, seed=91)
