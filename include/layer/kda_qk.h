@@ -35,7 +35,9 @@
  * Accuracy.  Sums and products in fp32, angles in fp64 (reduced to one turn
  * before cos and sin, so far positions keep their angle), outputs rounded once
  * to bf16; dweight is summed in fp32 per thread and fp64 across blocks, in a
- * fixed order.  An infinity or NaN stays in its row and head (and in dweight).
+ * fixed order.  A head's sum of squares has to stay in fp32's range: components
+ * below 2^60 (a sum beyond it makes the head zero), and one above 2^-60 or an eps
+ * above 2^-120.  An infinity or NaN stays in its row and head (and in dweight).
  *
  * Execution: forward 1 kernel; backward 1, or 2 with a dweight.  Enqueued on
  * `stream`, no allocation, no host synchronisation, capturable.  The workspace

@@ -94,6 +94,21 @@ def test_qk_far_positions_and_frequencies(cuda_device):
         ref.check(a, want, ref.QK_REL + 2.0 ** -20, f"position {pos}", ref.BF16_HALF_STEP)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -58, 2.0 ** 58])
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+def test_qk_magnitudes_at_the_stated_limits(norm, size, cuda_device):
+    """Components around 2^-58 without an eps, and around 2^58: their squares' sum stays in fp32's range."""
+    q, _, kw = case(40, 3, 1, 128, 64, norm, False, seed=8)
+    q, kw["eps"] = q * size, 0.0
+    got, _ = kda.kda_qk_norm_rope(q, **kw)
+    d = torch.randn(q.shape, generator=gen(9), device="cuda").bfloat16()
+    dq = kda.kda_qk_norm_rope_backward(d, None, q, **kw)[0]
+    x = q.double().requires_grad_()
+    y = reference(x, None, kw)
+    check_heads(got, y.detach(), "q")
+    check_heads(dq, torch.autograd.grad(y, x, d.double())[0], "dq")
+
+
 def test_qk_zero_and_nonfinite_rows(cuda_device):
     """Zero heads stay zero (eps), an infinity or NaN stays in its head."""
     q, k, kw = case(20, 3, 2, 64, 32, "l2", True, seed=2)
