@@ -30,7 +30,7 @@
 // 47000 cycles the first loads take 8000, y and the factors 10000, the products
 // with the states and exp(Gamma_C) sum_v S0 dS1 7000, the pairs 19000 (tf32
 // splits and MMAs, half of either's rate).  Measured (B200): 2112 chunks and
-// heads 403 us; a plain copy would move its bytes in 120.  Blocks that go on with
+// heads 399 us; a plain copy would move its bytes in 120.  Blocks that go on with
 // the next chunk and fetch its first operands under the decays' gradients, as the
 // preparation's do, were 20 us slower.
 #pragma once
