@@ -221,6 +221,33 @@ def test_scan_long_sequences_in_place(cuda_device):
     assert final is state and torch.equal(out, want) and torch.equal(state, wfinal)
 
 
+def test_scan_in_place_captured_and_at_once(cuda_device):
+    """Pools that long sequences update in place: one by a graph replayed on one stream, one eagerly on another, three times
+    each, as one after the other."""
+    H, T = 2, 64 * 30 + 5
+    x, y = inputs([T], H, "mild", seed=36), inputs([T, 100], H, "mild", seed=37)
+    slots = [torch.tensor(s, dtype=torch.int32, device=cuda_device) for s in ([1], [2, 0])]
+
+    def step(z, pool, i):
+        return kda.kda_scan(*z[:5], pool, cu_seqlens=z[5], slot_idx=slots[i])[0]
+
+    want = [states(3, H, 8), states(3, H, 9)]
+    pools = [p.clone() for p in want]
+    outs = [[step(z, p, i) for _ in range(3)][-1] for i, (z, p) in enumerate(zip((x, y), want))]
+    graph, one, two = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        first = step(x, pools[0], 0)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(one):
+            graph.replay()
+        with torch.cuda.stream(two):
+            second = step(y, pools[1], 1)
+    torch.cuda.synchronize()
+    assert torch.equal(first, outs[0]) and torch.equal(second, outs[1])
+    assert torch.equal(pools[0], want[0]) and torch.equal(pools[1], want[1])
+
+
 def test_scan_sequences_that_are_not_cut(cuda_device):
     """Sequences of 13 chunks where segments have 8 would be walked for longer in segments: nothing is written where the
     segments' states would be."""
